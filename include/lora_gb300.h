@@ -84,8 +84,9 @@ typedef enum {
   LORA_ERR_CUDA = 5,          /* a CUDA runtime call or kernel launch failed */
   LORA_ERR_TIMEOUT = 6,       /* a kernel's bounded wait expired (read by lora_poll_status) */
   LORA_ERR_DEVICE_INPUT = 7   /* a value in device memory was out of range: a RoPE position
-                                 outside [0, n_pos) (read by lora_poll_status; position 0
-                                 was used in its place) */
+                                 outside [0, n_pos) (position 0 was used in its place), or a
+                                 cache slot, page or length (see those calls); read by
+                                 lora_poll_status */
 } lora_status_t;
 
 /* One frozen base weight and its adapter: device pointers, bf16, row-major.
@@ -249,6 +250,151 @@ lora_status_t lora_qkvo_backward(int64_t M, int64_t h, int64_t n_q, int64_t n_kv
                                  lora_grads_t d_o, void* ws, size_t ws_bytes,
                                  cudaStream_t stream);
 
+/* ---------------------------------------------------------------- serving: rotary, cache, attention
+ * What stands between the Q/K/V and the O projection when a tuned model answers: the
+ * rotation of q and k, a paged cache of K and V, and the attention of the new tokens
+ * over it.  Tensors of heads are views, so that q, k and v can be slices of one buffer.
+ *
+ * lora_heads_t: bf16 [M x heads x head_dim], feature stride 1, the other strides in
+ * elements, not negative and multiples of 8; data 16-byte aligned.  An output's rows must
+ * not overlap. */
+typedef struct {
+  void* data;
+  int64_t heads;
+  int64_t token_stride;
+  int64_t head_stride;
+} lora_heads_t;
+
+/* Rotary positions of the first rot_dim features of a head; the others pass through.
+ * The pair (a, b) that table column c turns is (x[c], x[c + rot_dim/2]) in the half
+ * layout and (x[2c], x[2c + 1]) in the interleaved one:
+ *   a' = a cos - b sin,   b' = b cos + a sin,   cos, sin = cos[pos[m]][c], sin[pos[m]][c].
+ * Tables f32 [n_pos x rot_dim/2], 16-byte aligned; pos int32 [M].  rot_dim even, at
+ * least 2, at most head_dim (multiples of 16 are fastest).  A position outside
+ * [0, n_pos) is read as 0 and reported by lora_poll_status as LORA_ERR_DEVICE_INPUT.
+ * (lora_rope_t, the rotation inside the Q/K/V projection, is the half layout with
+ * rot_dim == head_dim.) */
+typedef enum { LORA_ROTARY_HALF = 0, LORA_ROTARY_INTERLEAVED = 1 } lora_rotary_layout_t;
+typedef struct {
+  const float* cos;
+  const float* sin;
+  const int32_t* pos;
+  int64_t n_pos;
+  int rot_dim;
+  int layout;               /* lora_rotary_layout_t */
+} lora_rotary_t;
+
+/* yq = rotated q, yk = rotated k (k->data NULL: only q) in one launch; head_dim a
+ * multiple of 8, at most 1024.  inverse != 0 turns back by the same angles: the
+ * gradient of q and k from that of yq and yk.  Products and sums are f32, each rounded,
+ * and the result is rounded to bf16 once.  y may be x itself (same data and strides);
+ * any other overlap is undefined.  ws: at least 256 bytes (the status word). */
+lora_status_t lora_rotary(int64_t M, int head_dim, const lora_heads_t* q, const lora_heads_t* yq,
+                          const lora_heads_t* k, const lora_heads_t* yk, const lora_rotary_t* rot,
+                          int inverse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* lora_rope_table for long contexts: cos, sin [n_pos x rot_dim/2] of p * w_c, times a
+ * magnitude, where w_c = base^(-2c/rot_dim) is changed by `kind`:
+ *   LINEAR      w_c / factor (position interpolation)
+ *   NTK         base becomes base * factor^(rot_dim / (rot_dim - 2)); rot_dim >= 4
+ *   YARN        (1 - g_c) w_c + g_c w_c / factor, g_c rising from 0 to 1 between the
+ *               columns that turn `high` and `low` times in original_len positions
+ *               (rounded outwards); 0 < low < high (the method's own choice: 1, 32)
+ *   WAVELENGTH  wavelengths below original_len / high keep w_c, those above
+ *               original_len / low take w_c / factor, between them a linear blend in
+ *               original_len / wavelength; 0 < low < high
+ * factor >= 1.  magnitude multiplies cos and sin; 0 stands for 1, and with YARN for
+ * 0.1 ln(factor) + 1.  Computed in double and rounded once. */
+typedef enum {
+  LORA_ROPE_PLAIN = 0, LORA_ROPE_LINEAR = 1, LORA_ROPE_NTK = 2, LORA_ROPE_YARN = 3, LORA_ROPE_WAVELENGTH = 4
+} lora_rope_kind_t;
+typedef struct {
+  int kind;                 /* lora_rope_kind_t */
+  double factor;
+  double original_len;
+  double low, high;
+  double magnitude;
+} lora_rope_scaling_t;
+lora_status_t lora_rope_table_scaled(float* cos, float* sin, int64_t n_pos, int rot_dim, double base,
+                                     const lora_rope_scaling_t* scaling, cudaStream_t stream);
+
+/* A paged cache of K and V: pages [n_pages x heads x page_size x head_dim] of bf16, or
+ * of 8-bit codes (e4m3 or int8) with a scale for each row, f32 [n_pages x heads x
+ * page_size] (NULL for bf16).  page_size 16, 32, 64, 128 or 256; head_dim 64, 128 or
+ * 256; pages 16-byte aligned, scales 4-byte aligned.  n_pages * heads * page_size is at
+ * most 2^31 - 1 rows.  Slot number s is row s % page_size of page s / page_size.
+ *
+ * A row x is stored as codes rn(x * (1 / scale)) with scale = max(amax|x| * (1/Q),
+ * the smallest normal f32), Q = 127 for int8 and 448 for e4m3 (all in f32, ties to even).
+ * A row that holds an infinity or a NaN is stored as scale NaN and codes 0. */
+typedef enum { LORA_KV_BF16 = 0, LORA_KV_FP8 = 1, LORA_KV_INT8 = 2 } lora_kv_format_t;
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t n_pages;
+  int page_size;
+  int heads;
+  int head_dim;
+  int format;               /* lora_kv_format_t */
+} lora_kv_cache_t;
+
+/* Writes token m's k and v (views with the cache's heads) to slot slots[m] (int64 [M]) in the
+ * cache's format.  With rot, k is rotated first, and q (NULL or data NULL: none) into yq
+ * in the same launch; the rotated k is not rounded before it is quantised.  A negative
+ * slot is skipped (padding); one past the cache is skipped and reported
+ * (LORA_ERR_DEVICE_INPUT).  The slots of a call must differ from each other.  q needs
+ * rot.  yq may be q itself.  ws: at least 256 bytes. */
+lora_status_t lora_kv_append(int64_t M, const lora_kv_cache_t* cache, const lora_heads_t* k,
+                             const lora_heads_t* v, const int64_t* slots, const lora_heads_t* q,
+                             const lora_heads_t* yq, const lora_rotary_t* rot, void* ws, size_t ws_bytes,
+                             cudaStream_t stream);
+
+/* Reads sequences back: row cu_kv[b] + i of k and v (bf16 [total x heads x head_dim],
+ * dense) is position i of sequence b, 0 <= i < cu_kv[b+1] - cu_kv[b].  cu_kv int32
+ * [n_seqs + 1], rising from 0 to total; page_table int32 [n_seqs x max_pages], entry
+ * [b][i / page_size] the page of position i.  A page outside the cache, a position past
+ * the table and a row that cu_kv does not cover read as 0 and are reported
+ * (LORA_ERR_DEVICE_INPUT).  ws: at least 256 bytes. */
+lora_status_t lora_kv_read(int64_t n_seqs, int64_t total, const lora_kv_cache_t* cache,
+                           const int32_t* page_table, int64_t max_pages, const int32_t* cu_kv, void* k,
+                           void* v, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* The sequences of a call: sequence b owns query rows [cu_q[b], cu_q[b+1]) of M (cu_q int32
+ * [n_seqs + 1], not falling, inside [0, M]) and kv_len[b] cached positions (int32), its
+ * new tokens' own among them; page_table as above.  All on the device: a step can be
+ * captured in a graph and its lengths changed between replays. */
+typedef struct {
+  int64_t n_seqs;
+  const int32_t* page_table;
+  int64_t max_pages;
+  const int32_t* kv_len;
+  const int32_t* cu_q;
+} lora_paged_batch_t;
+
+/* Attention of new tokens over the cache.  Token i of sequence b's n_b = cu_q[b+1] -
+ * cu_q[b] stands at position p = kv_len[b] - n_b + i and sees the positions j <
+ * kv_len[b] with j <= p (causal != 0) and p - j < window (window > 0; 0: no window).
+ * Query head g reads cache head g / (heads_q / heads):
+ *   out = sum_j e^(s_j - max s) v_j / sum_j e^(s_j - max s),  s_j = scale * <q, k_j>.
+ * out bf16 [M x heads_q x head_dim], dense (the O projection's input); lse f32 [M x
+ * heads_q] or NULL receives ln sum_j e^(s_j).  A token that sees nothing (kv_len 0, or
+ * p < 0) gets out 0 and lse -inf.  Rows of M that no sequence owns are not written.
+ * q is a view; heads_q is a multiple of the cache's heads.
+ * Scores, maxima, sums and the accumulated output are f32; the weights e^(...) are
+ * rounded to bf16 before they multiply V (as the matrix units take them), and the
+ * result is rounded once.  What lies past kv_len in a page is not looked at, whatever
+ * bits it holds; a page outside the cache is read as page 0, and a length past the
+ * table or a query range outside M is cut to it, each reported by lora_poll_status
+ * (LORA_ERR_DEVICE_INPUT).  With a bf16 cache, an infinity or NaN inside a sequence's
+ * own V may also reach its tokens that do not see that position.
+ * ws: lora_paged_attention_workspace_bytes. */
+size_t lora_paged_attention_workspace_bytes(int64_t M, int64_t n_seqs, int heads_q, const lora_kv_cache_t* cache);
+lora_status_t lora_paged_attention(int64_t M, int heads_q, const lora_heads_t* q, const lora_kv_cache_t* cache,
+                                   const lora_paged_batch_t* batch, float scale, int causal, int64_t window,
+                                   void* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* ---------------------------------------------------------------- status, counters
  * lora_poll_status: synchronises `stream`, reads the asynchronous status word in
  * ws, clears it, and returns LORA_OK, LORA_ERR_TIMEOUT or LORA_ERR_DEVICE_INPUT
@@ -320,7 +466,9 @@ enum {
   LORA_KIND_PROJ = 5,        /* plain projection GEMM (down, q/k/v, o) */
   LORA_KIND_ACT_BWD = 6,     /* dh GEMM with the activation-derivative epilogue */
   LORA_KIND_DGRAD = 7,       /* input-gradient GEMM (dx, d o_in) */
-  LORA_KIND_ROPE = 8         /* RoPE transpose rotation of dy_q, dy_k; RoPE tables */
+  LORA_KIND_ROPE = 8,        /* RoPE transpose rotation of dy_q, dy_k; RoPE tables; lora_rotary */
+  LORA_KIND_CACHE = 9,       /* cache writes and reads */
+  LORA_KIND_ATTN = 10        /* attention over the cache, and the joining of its split sums */
 };
 lora_status_t lora_trace_enable(int capacity);
 int lora_trace_read(int* kind, float* ms, int max);

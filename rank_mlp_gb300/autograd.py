@@ -2,8 +2,8 @@
 call ``loss.backward()``.
 
 They only route tensors: the forward and backward of each function are one call each
-of ``lora_mlp_forward/backward``, ``lora_qkvo_forward/backward`` (the Q/K/V half) and
-``lora_linear_forward/backward``.  The base weights W are frozen ("Model Patches and
+of ``lora_mlp_forward/backward``, ``lora_qkvo_forward/backward`` (the Q/K/V half),
+``lora_linear_forward/backward`` and ``lora_rotary`` (both ways).  The base weights W are frozen ("Model Patches and
 Kernels": a frozen weight gets no gradient), so they never receive a gradient; the
 adapters A, B and the input x do.  Inputs may carry leading batch dimensions
 ([..., features]); every tensor is bf16 on the GPU.
@@ -86,6 +86,26 @@ class LoraLinearFunction(torch.autograd.Function):
         x2, W, A, B, saved = ctx.saved_tensors
         dx, dA, dB = binding.linear_backward(x2, (W, A, B), ctx.s, saved, _bf16(_flat(dy)))
         return dx.reshape(ctx.xshape), None, dA, dB, None
+
+
+class RotaryFunction(torch.autograd.Function):
+    """Rotary positions of q and k, views [tokens, heads, head_dim] (rope as in
+    ``binding.rotary``); the gradient is the rotation back."""
+
+    @staticmethod
+    def forward(ctx, q, k, rope):
+        ctx.rope = rope
+        return binding.rotary(q, k, rope=rope)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        rows = lambda d: d if d.stride(-1) == 1 and all(s % 8 == 0 for s in d.stride()[:2]) \
+            and d.data_ptr() % 16 == 0 else d.contiguous()  # noqa: E731
+        return *binding.rotary(rows(_bf16(dq)), rows(_bf16(dk)), rope=ctx.rope, inverse=True), None
+
+
+def lora_rotary(q, k, rope):
+    return RotaryFunction.apply(q, k, rope)
 
 
 def lora_mlp(x, gate, up, down, s, act="swiglu"):

@@ -21,7 +21,11 @@ from . import build as _build
 
 ACT = {"swiglu": 0, "geglu_tanh": 1, "geglu_erf": 2}
 KIND_NAMES = {0: "pack", 1: "reduce", 2: "rank_proj", 3: "rank_grad", 4: "gate_up",
-              5: "proj", 6: "act_bwd", 7: "dgrad", 8: "rope"}
+              5: "proj", 6: "act_bwd", 7: "dgrad", 8: "rope", 9: "cache", 10: "attn"}
+LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
+KV_FORMAT = {torch.bfloat16: 0, torch.float8_e4m3fn: 1, torch.int8: 2}
+KV_DTYPE = {"bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn, "int8": torch.int8}
 STATUS = {0: "ok", 1: "invalid argument", 2: "alignment", 3: "unsupported",
           4: "workspace too small", 5: "CUDA error", 6: "timeout", 7: "device input out of range"}
 
@@ -44,6 +48,32 @@ class LoraGrads(ctypes.Structure):
 class LoraRope(ctypes.Structure):
     _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("pos", ctypes.c_void_p),
                 ("n_pos", ctypes.c_int64), ("head_dim", ctypes.c_int)]
+
+
+class LoraHeads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class LoraRotary(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("n_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int), ("layout", ctypes.c_int)]
+
+
+class LoraRopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("magnitude", ctypes.c_double)]
+
+
+class LoraKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int),
+                ("heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("format", ctypes.c_int)]
+
+
+class LoraPagedBatch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int64), ("page_table", ctypes.c_void_p), ("max_pages", ctypes.c_int64),
+                ("kv_len", ctypes.c_void_p), ("cu_q", ctypes.c_void_p)]
 
 
 _LIB = None
@@ -76,6 +106,12 @@ _SIGS = {
     "lora_qkvo_backward": (_INT, [_I64, _I64, _I64, _I64, _INT, _F32, _VP, LoraLinear, LoraLinear, LoraLinear,
                                   _VP, LoraLinear, _VP, ctypes.POINTER(LoraRope), _VP, _VP, _VP, _VP, _VP, _VP,
                                   LoraGrads, LoraGrads, LoraGrads, LoraGrads, _VP, _SZ, _VP]),
+    "lora_rotary": (_INT, [_I64, _INT, _VP, _VP, _VP, _VP, _VP, _INT, _VP, _SZ, _VP]),
+    "lora_rope_table_scaled": (_INT, [_VP, _VP, _I64, _INT, ctypes.c_double, _VP, _VP]),
+    "lora_kv_append": (_INT, [_I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "lora_kv_read": (_INT, [_I64, _I64, _VP, _VP, _I64, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "lora_paged_attention_workspace_bytes": (_SZ, [_I64, _I64, _INT, _VP]),
+    "lora_paged_attention": (_INT, [_I64, _INT, _VP, _VP, _VP, _F32, _INT, _I64, _VP, _VP, _VP, _SZ, _VP]),
     "lora_poll_status": (_INT, [_VP, _VP]),
     "lora_status_string": (ctypes.c_char_p, [_INT]),
     "lora_launch_count": (ctypes.c_uint64, []),
@@ -445,4 +481,207 @@ def qkvo_backward(x, q, k, v, o_in, o, s, saved, dyq=None, dyk=None, dyv=None, d
         _opt(dyq, "dyq"), _opt(dyk, "dyk"), _opt(dyv, "dyv"), _opt(out.get("dx"), "dx"),
         _opt(dyo, "dyo"), _opt(out.get("do_in"), "do_in"), gr("q"), gr("k"), gr("v"), gr("o"),
         ws.data_ptr(), ws.numel(), _stream(dev)), "lora_qkvo_backward")
+    return out
+
+
+# ------------------------------------------------------------------ serving: rotary, cache, attention
+#
+# Tensors of heads are views [tokens, heads, head_dim] (bf16, feature stride 1), so that
+# q, k and v can be slices of one buffer.  The structures handed to the library live
+# until the call returns; the library copies what it needs.
+
+def _heads(t, name) -> LoraHeads:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be a bf16 CUDA tensor [tokens, heads, head_dim] with feature stride 1 "
+                         f"(got {t.dtype}, {t.device}, {tuple(t.shape)}, strides {t.stride()})")
+    n, heads, dim = t.shape
+    ts, hs, _ = t.stride()
+    # the stride of an extent of one says nothing; a whole row satisfies every rule
+    return LoraHeads(t.data_ptr(), heads, ts if n > 1 else heads * dim, hs if heads > 1 else dim)
+
+
+def _ints(t, dtype, shape, name) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {shape} (got {t.dtype}, "
+                         f"{t.device}, {tuple(t.shape)})")
+    return t.data_ptr()
+
+
+def _rotary(rope, tokens) -> LoraRotary:
+    """dict(cos, sin, pos[, layout]): f32 tables [n_pos, rot_dim/2] and int32 positions
+    [tokens] on the device; layout "half" (default) or "interleaved"."""
+    cos, sin = rope["cos"], rope["sin"]
+    if cos.dim() != 2:
+        raise ValueError("rope tables must be [n_pos, rot_dim/2]")
+    shape = tuple(cos.shape)
+    return LoraRotary(_ints(cos, torch.float32, shape, "rope cos"), _ints(sin, torch.float32, shape, "rope sin"),
+                      _ints(rope["pos"], torch.int32, (tokens,), "rope pos"), shape[0], 2 * shape[1],
+                      LAYOUT[rope.get("layout", "half")])
+
+
+def _at(struct):
+    return None if struct is None else ctypes.addressof(struct)
+
+
+def rope_table_scaled(n_pos: int, rot_dim: int, base: float = 10000.0, scaling: dict | None = None, device="cuda"):
+    """(cos, sin), f32 [n_pos, rot_dim/2]: ``rope_table`` with the frequencies scaled for a
+    long context.  scaling: None, or dict(kind="linear" | "ntk" | "yarn" | "wavelength",
+    factor, original_len, low, high, magnitude), the fields of lora_rope_scaling_t (low and
+    high default to 1 and 32 for yarn, 1 and 4 for wavelength)."""
+    sc = dict(scaling or {})
+    kind = sc.pop("kind", "plain")
+    low, high = sc.pop("low", 1.0), sc.pop("high", 32.0 if kind == "yarn" else 4.0)
+    st = LoraRopeScaling(ROPE_SCALING[kind], sc.pop("factor", 1.0), sc.pop("original_len", 0.0), low, high,
+                         sc.pop("magnitude", 0.0))
+    if sc:
+        raise ValueError(f"unknown rope scaling fields {sorted(sc)}")
+    dev = torch.device(device)
+    cos = torch.empty(n_pos, rot_dim // 2, dtype=torch.float32, device=dev)
+    sin = torch.empty_like(cos)
+    _check(load().lora_rope_table_scaled(cos.data_ptr(), sin.data_ptr(), n_pos, rot_dim, float(base), _at(st),
+                                         _stream(dev)), "lora_rope_table_scaled")
+    return cos, sin
+
+
+def rotary(q, k=None, *, rope, inverse=False, q_out=None, k_out=None, ws=None):
+    """Rotary positions of q and k, views [tokens, heads, head_dim], in one launch: returns
+    the rotated q, or (q, k).  rope: dict(cos, sin, pos[, layout]) with tables
+    [n_pos, rot_dim/2]; features from rot_dim on pass through.  inverse turns back (the
+    gradient).  q_out and k_out may be q and k themselves."""
+    lib = load()
+    tokens, _, dim = q.shape
+    st_q, rot = _heads(q, "q"), _rotary(rope, tokens)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    st_yq, st_k, st_yk = _heads(q_out, "q_out"), None, None
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    if k is not None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+        if k.shape[0] != tokens or k.shape[2] != dim or k_out.shape != k.shape:
+            raise ValueError("k must have q's tokens and head_dim, and k_out k's shape")
+        st_k, st_yk = _heads(k, "k"), _heads(k_out, "k_out")
+    ws = workspace(256, q.device) if ws is None else ws
+    _check(lib.lora_rotary(tokens, dim, _at(st_q), _at(st_yq), _at(st_k), _at(st_yk), _at(rot), int(inverse),
+                           ws.data_ptr(), ws.numel(), _stream(q.device)), "lora_rotary")
+    return q_out if k is None else (q_out, k_out)
+
+
+class KVCache:
+    """A paged cache of K and V over tensors that the caller owns: k, v [n_pages, heads,
+    page_size, head_dim] (bf16, float8_e4m3fn or int8) and, for the 8-bit formats, their
+    scales k_scale, v_scale, f32 [n_pages, heads, page_size].  Slot s is row s % page_size
+    of page s // page_size."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.dtype not in KV_FORMAT:
+            raise ValueError("cache pages must be [n_pages, heads, page_size, head_dim] of bf16, float8_e4m3fn or int8")
+        shape = tuple(k.shape)
+        scaled = k.dtype != torch.bfloat16
+        if scaled != (k_scale is not None) or scaled != (v_scale is not None):
+            raise ValueError("scales belong to the 8-bit formats, and to both K and V")
+        sc = [_ints(t, torch.float32, shape[:3], n) if scaled else None
+              for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale"))]
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.heads, self.page_size, self.head_dim = shape
+        self._struct = LoraKvCache(_ints(k, k.dtype, shape, "k"), _ints(v, k.dtype, shape, "v"), sc[0], sc[1],
+                                   shape[0], shape[2], shape[1], shape[3], KV_FORMAT[k.dtype])
+
+
+def kv_cache(n_pages: int, page_size: int, heads: int, head_dim: int, format: str = "bf16", device="cuda") -> KVCache:
+    """A zeroed KVCache of the given format ("bf16", "fp8" or "int8")."""
+    dev = torch.device(device)
+    k, v = (torch.zeros(n_pages, heads, page_size, head_dim, dtype=torch.uint8 if format != "bf16" else torch.bfloat16,
+                        device=dev).view(KV_DTYPE[format]) for _ in range(2))
+    scales = (None, None) if format == "bf16" else         tuple(torch.zeros(n_pages, heads, page_size, dtype=torch.float32, device=dev) for _ in range(2))
+    return KVCache(k, v, *scales)
+
+
+def kv_append(cache: KVCache, k, v, slots, *, q=None, rope=None, q_out=None, ws=None):
+    """Writes k and v (views [tokens, heads, head_dim]) to the cache's slots (int64
+    [tokens]; negative: skipped).  With rope, k is rotated first, and q in the same launch:
+    returns the rotated q (q_out, which may be q), or None without q."""
+    lib = load()
+    tokens = k.shape[0]
+    for t, n in ((k, "k"), (v, "v")):
+        if tuple(t.shape) != (tokens, cache.heads, cache.head_dim):
+            raise ValueError(f"{n} must be [tokens, {cache.heads}, {cache.head_dim}]")
+    st_k, st_v, st_q, st_yq = _heads(k, "k"), _heads(v, "v"), None, None
+    rot = None if rope is None else _rotary(rope, tokens)
+    if q is not None:
+        if rope is None:
+            raise ValueError("q is passed to be rotated: rope is missing")
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        if q.shape[0] != tokens or q.shape[2] != cache.head_dim or q_out.shape != q.shape:
+            raise ValueError("q must have k's tokens and head_dim, and q_out q's shape")
+        st_q, st_yq = _heads(q, "q"), _heads(q_out, "q_out")
+    ws = workspace(256, k.device) if ws is None else ws
+    _check(lib.lora_kv_append(tokens, _at(cache._struct), _at(st_k), _at(st_v),
+                              _ints(slots, torch.int64, (tokens,), "slots"), _at(st_q), _at(st_yq), _at(rot),
+                              ws.data_ptr(), ws.numel(), _stream(k.device)), "lora_kv_append")
+    return q_out if q is not None else None
+
+
+def kv_read(cache: KVCache, page_table, cu_kv, total: int, *, ws=None):
+    """(k, v), bf16 [total, heads, head_dim]: the sequences' cached rows one after the
+    other, sequence b's at rows [cu_kv[b], cu_kv[b+1]).  page_table int32 [n_seqs,
+    max_pages], cu_kv int32 [n_seqs + 1], both on the device."""
+    lib = load()
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_seqs, max_pages]")
+    n, width = page_table.shape
+    dev = cache.k.device
+    k = torch.empty(total, cache.heads, cache.head_dim, dtype=torch.bfloat16, device=dev)
+    v = torch.empty_like(k)
+    ws = workspace(256, dev) if ws is None else ws
+    _check(lib.lora_kv_read(n, total, _at(cache._struct), _ints(page_table, torch.int32, (n, width), "page_table"),
+                            width, _ints(cu_kv, torch.int32, (n + 1,), "cu_kv"), k.data_ptr(), v.data_ptr(),
+                            ws.data_ptr(), ws.numel(), _stream(dev)), "lora_kv_read")
+    return k, v
+
+
+class PagedBatch:
+    """The sequences of a step: page_table int32 [n_seqs, max_pages], kv_len int32 [n_seqs]
+    (cached positions, the new tokens' own among them) and cu_q int32 [n_seqs + 1] (their
+    query rows), all on the device.  One object serves all layers of a step, and later
+    steps too when the tensors are updated in place."""
+
+    def __init__(self, page_table, kv_len, cu_q):
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [n_seqs, max_pages]")
+        n, width = page_table.shape
+        self.page_table, self.kv_len, self.cu_q = page_table, kv_len, cu_q
+        self._struct = LoraPagedBatch(n, _ints(page_table, torch.int32, (n, width), "page_table"), width,
+                                      _ints(kv_len, torch.int32, (n,), "kv_len"),
+                                      _ints(cu_q, torch.int32, (n + 1,), "cu_q"))
+
+
+def paged_batch(page_table, kv_len, cu_q) -> PagedBatch:
+    return PagedBatch(page_table, kv_len, cu_q)
+
+
+def paged_attention(q, cache: KVCache, batch: PagedBatch, *, scale=None, causal=True, window=0, out=None, lse=None,
+                    ws=None):
+    """Attention of the new tokens' q (view [tokens, heads_q, head_dim]) over the cached
+    positions that each sees: out, bf16 [tokens, heads_q, head_dim].  scale defaults to
+    head_dim ** -0.5; causal and window as in lora_paged_attention.  lse: None, or an f32
+    [tokens, heads_q] tensor that receives the logarithm of each sum."""
+    lib = load()
+    tokens, hq, dim = q.shape
+    if dim != cache.head_dim:
+        raise ValueError(f"q must have the cache's head_dim {cache.head_dim}")
+    st_q = _heads(q, "q")
+    out = torch.empty(tokens, hq, dim, dtype=torch.bfloat16, device=q.device) if out is None else out
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    at_cache, st_b = _at(cache._struct), batch._struct
+    need = lib.lora_paged_attention_workspace_bytes(tokens, st_b.n_seqs, hq, at_cache)
+    ws = workspace(need, q.device) if ws is None else ws
+    _check(lib.lora_paged_attention(
+        tokens, hq, _at(st_q), at_cache, _at(st_b), dim ** -0.5 if scale is None else scale, int(causal), window,
+        _dev(out, "out"), None if lse is None else _ints(lse, torch.float32, (tokens, hq), "lse"), ws.data_ptr(),
+        ws.numel(), _stream(q.device)), "lora_paged_attention")
     return out

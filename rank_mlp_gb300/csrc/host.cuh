@@ -114,6 +114,22 @@ inline cudaError_t launch_pdl(Kernel kernel, dim3 grid, dim3 block, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, arg);
 }
 
+// launch_pdl with the launch counter and the optional event trace.
+// (trace_begin gives the start event's slot, or -1; defined in lora_api.cu)
+int trace_begin(int kind, cudaStream_t st);
+void trace_end(int slot, cudaStream_t st);
+void count_launch();
+template <typename Kernel, typename Arg>
+inline lora_status_t launch_counted(Kernel kernel, dim3 grid, dim3 block, size_t smem, int kind, cudaStream_t st,
+                                    const Arg& arg) {
+  const int slot = trace_begin(kind, st);
+  const cudaError_t e = launch_pdl(kernel, grid, block, smem, st, arg);
+  trace_end(slot, st);
+  if (e != cudaSuccess) return LORA_ERR_CUDA;
+  count_launch();
+  return LORA_OK;
+}
+
 // Raises a kernel's dynamic shared-memory limit to `smem` bytes on the current device,
 // once per device (the attribute belongs to the device's context; bit d of `done`
 // marks device d).
@@ -136,6 +152,8 @@ int tc_smem_bytes(int variant);
 
 // Defined in lora_api.cu.
 int num_sms();
+unsigned long long wait_timeout_ns();           // limit of the kernels' bounded waits
+int take_expiry();                              // 1: this launch lets a wait run out (failure-path tests)
 bool encode_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
                 uint32_t box_inner, uint32_t box_outer, int swizzle_bytes = 128);
 bool encode_map_planes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t d1, uint64_t d2, uint64_t ld,

@@ -104,7 +104,7 @@ struct Trace {
 static Trace g_trace;
 
 // Records the start event of a traced launch; returns its slot or -1.
-static int trace_begin(int kind, cudaStream_t st) {
+int trace_begin(int kind, cudaStream_t st) {
   std::lock_guard<std::mutex> lk(g_trace.mu);
   if (g_trace.capacity == 0 || g_trace.used >= g_trace.capacity || !((g_trace.kinds >> kind) & 1u)) return -1;
   const int slot = g_trace.used++;
@@ -112,18 +112,22 @@ static int trace_begin(int kind, cudaStream_t st) {
   cudaEventRecord(g_trace.ev[2 * slot], st);
   return slot;
 }
-static void trace_end(int slot, cudaStream_t st) {
+void trace_end(int slot, cudaStream_t st) {
   if (slot < 0) return;
   std::lock_guard<std::mutex> lk(g_trace.mu);
   cudaEventRecord(g_trace.ev[2 * slot + 1], st);
 }
+
+void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 // Wait limit of the GEMM kernels' bounded waits, and the number of coming GEMM
 // launches that are told to leave one pipeline stage empty (failure-path tests).
 static std::atomic<unsigned long long> g_timeout_ns{kTimeoutNs};
 static std::atomic<int> g_expire_next{0};
 
-static int take_expiry() {
+unsigned long long wait_timeout_ns() { return g_timeout_ns.load(); }
+
+int take_expiry() {
   int n = g_expire_next.load();
   while (n > 0 && !g_expire_next.compare_exchange_weak(n, n - 1)) {
   }
@@ -665,7 +669,7 @@ extern "C" const char* lora_status_string(lora_status_t status) {
     case LORA_ERR_WORKSPACE: return "workspace smaller than the size query";
     case LORA_ERR_CUDA: return "CUDA runtime or launch failure";
     case LORA_ERR_TIMEOUT: return "a kernel's bounded wait expired";
-    case LORA_ERR_DEVICE_INPUT: return "a device-side input was out of range (RoPE position)";
+    case LORA_ERR_DEVICE_INPUT: return "a device-side input was out of range (position, slot, page or length)";
   }
   return "unknown status";
 }
