@@ -321,7 +321,7 @@ lora_status_t lora_rope_table_scaled(float* cos, float* sin, int64_t n_pos, int 
 /* A paged cache of K and V: pages [n_pages x heads x page_size x head_dim] of bf16, or
  * of 8-bit codes (e4m3 or int8) with a scale for each row, f32 [n_pages x heads x
  * page_size] (NULL for bf16).  page_size 16, 32, 64, 128 or 256; head_dim 64, 128 or
- * 256; pages 16-byte aligned, scales 4-byte aligned.  n_pages * heads * page_size is at
+ * 256; pages and scales 16-byte aligned.  n_pages * heads * page_size is at
  * most 2^31 - 1 rows.  Slot number s is row s % page_size of page s / page_size.
  *
  * A row x is stored as codes rn(x * (1 / scale)) with scale = max(amax|x| * (1/Q),

@@ -52,24 +52,34 @@ static void bind_current_device() {
   if (cudaGetDevice(&dev) == cudaSuccess && dev != bound && cudaSetDevice(dev) == cudaSuccess) bound = dev;
 }
 
-// 2-D bf16 map with a 128-byte, 64-byte, 32-byte or no swizzle (swizzle_bytes 128, 64, 32, 0);
-// out-of-bounds elements read as zero.
-bool encode_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
-                uint32_t box_inner, uint32_t box_outer, int swizzle_bytes) {
+// 2-D map of elements of elem_bytes (2: bf16, 1: bytes) with a 128-byte, 64-byte, 32-byte
+// or no swizzle (swizzle_bytes 128, 64, 32, 0); out-of-bounds elements read as zero.
+static bool encode_map_2d(CUtensorMap* m, const void* base, int elem_bytes, uint64_t inner, uint64_t outer, uint64_t ld,
+                          uint32_t box_inner, uint32_t box_outer, int swizzle_bytes) {
   bind_current_device();
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr || inner == 0 || outer == 0) return false;
   const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {ld * 2};
+  const cuuint64_t strides[1] = {ld * elem_bytes};
   const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE,
+  return fn(m, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             swizzle_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
             : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
             : swizzle_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                   : CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool encode_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
+                uint32_t box_inner, uint32_t box_outer, int swizzle_bytes) {
+  return encode_map_2d(m, base, 2, inner, outer, ld, box_inner, box_outer, swizzle_bytes);
+}
+// Dense rows of row_elems elements in boxes of box_rows rows x box_bytes, swizzled by box_bytes.
+bool encode_map_rows(CUtensorMap* m, const void* base, int elem_bytes, uint64_t rows, uint64_t row_elems,
+                     uint32_t box_rows, uint32_t box_bytes) {
+  return encode_map_2d(m, base, elem_bytes, row_elems, rows, row_elems, box_bytes / elem_bytes, box_rows,
+                       static_cast<int>(box_bytes));
 }
 
 // 3-D bf16 map {inner, d1, d2} with row stride ld (elements) and plane stride

@@ -66,7 +66,7 @@ inline lora_status_t check_cache(const lora_kv_cache_t* c) {
   const int ps = c->page_size, d = c->head_dim;
   if (ps < 16 || ps > 256 || (ps & (ps - 1)) || (d != 64 && d != 128 && d != 256)) return LORA_ERR_UNSUPPORTED;
   if (c->heads > 65535 || c->n_pages > kMaxExtent / (static_cast<int64_t>(c->heads) * ps)) return LORA_ERR_UNSUPPORTED;
-  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
     return LORA_ERR_ALIGNMENT;
   return LORA_OK;
 }
