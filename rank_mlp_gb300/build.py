@@ -21,7 +21,7 @@ OUT_DIR = os.path.join(HERE, "_lib")
 LIB_NAME = "liblora_gb300.so"
 SOURCES = ("lora_api.cu", "lora_linear.cu", "lora_mlp.cu", "lora_qkvo.cu", "gemm_big.cu", "gemm_skinny.cu",
            "noalloc.cu", "rotary.cu", "kv_cache.cu", "paged_attn.cu",
-           "attn_few.cu")
+           "attn_few.cu", "attn_many.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                      "--expt-relaxed-constexpr", "-I" + INCLUDE, "-diag-suppress", "1160"]

@@ -4,12 +4,19 @@
 
 namespace lgb {
 
+// Which kernel: the one whose tiles the rows fill.  A call's lengths are on the device, so
+// the rule takes the mean number of query rows that share a cache head.
+static bool many_rows_call(int64_t M, int64_t n_seqs, int group) {
+  return M * group > kFewRows * n_seqs;
+}
+
 // Workspace: header, the parts' descriptors, maxima and sums, outputs.
-static void carve_parts(Carve& c, int head_dim, AttnParams& p) {
+static void carve_parts(Carve& c, bool many, int head_dim, AttnParams& p) {
+  const int64_t ctas = many ? kMaxManyCtas : kMaxFewCtas, rows = 2 * ctas * (many ? many_rows(head_dim) : kFewRows);
   c.take(kWsHeader);
-  p.join = c.take_n<JoinDesc>(kMaxFewCtas);
-  p.part_ml = c.take_n<float2>(2ll * kMaxFewCtas * kFewRows);
-  p.part_o = c.take_n<float>(2ll * kMaxFewCtas * kFewRows * head_dim);
+  p.join = c.take_n<JoinDesc>(ctas);
+  p.part_ml = c.take_n<float2>(rows);
+  p.part_o = c.take_n<float>(rows * head_dim);
 }
 
 }  // namespace lgb
@@ -23,7 +30,7 @@ extern "C" size_t lora_paged_attention_workspace_bytes(int64_t M, int64_t n_seqs
     return 0;
   AttnParams p;
   Carve c(nullptr);
-  carve_parts(c, cache->head_dim, p);
+  carve_parts(c, many_rows_call(M, n_seqs, heads_q / cache->heads), cache->head_dim, p);
   return c.off;
 }
 
@@ -66,6 +73,8 @@ extern "C" lora_status_t lora_paged_attention(int64_t M, int heads_q, const lora
   p.timeout_ns = wait_timeout_ns();
   p.inject_stall = take_expiry();
   Carve c(ws);
-  carve_parts(c, cache->head_dim, p);
-  return launch_attn_few(p, cache->head_dim, cache->format, stream);
+  const bool many = many_rows_call(M, batch->n_seqs, p.group);
+  carve_parts(c, many, cache->head_dim, p);
+  return many ? launch_attn_many(p, cache->head_dim, cache->format, stream)
+              : launch_attn_few(p, cache->head_dim, cache->format, stream);
 }

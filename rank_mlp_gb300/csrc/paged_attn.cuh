@@ -372,8 +372,11 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnP
 
 // Most CTAs of a launch, whatever the device: the parts' slots are sized for it.
 constexpr int kMaxFewCtas = 320;
+constexpr int kMaxManyCtas = 160;
 
 constexpr int kFewRows = 16;          // rows of the few-row kernel's tiles
+constexpr int many_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
+lora_status_t launch_attn_many(AttnParams& p, int head_dim, int format, cudaStream_t st);
 lora_status_t launch_attn_few(AttnParams& p, int head_dim, int format, cudaStream_t st);
 
 // The cache's pages as rows, in boxes of at most `tile` rows of one page.
