@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
     bool own[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      own[h] = row_owner(p, w.s, w.slice, static_cast<long long>(w.rt) * R + r0 + 8 * h, tok[h], head[h]);
+      own[h] = row_owner(p, w.s, w.slice, static_cast<unsigned>(w.rt) * R + r0 + 8 * h, tok[h], head[h]);
       if (own[h]) row_range(p, w.s, tok[h], lo[h], hi[h]); else lo[h] = 0, hi[h] = 0;
     }
     // the tile rows' common range: tiles inside it need no mask
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
       constexpr int kLanes = D / 4;                 // threads of a row, four features each
       for (int r = threadIdx.x / kLanes; r < R; r += 128 / kLanes) {
         int tk, hd;
-        if (!row_owner(p, w.s, w.slice, static_cast<long long>(w.rt) * R + r, tk, hd)) continue;
+        if (!row_owner(p, w.s, w.slice, static_cast<unsigned>(w.rt) * R + r, tk, hd)) continue;
         const int f = (threadIdx.x % kLanes) * 4;
         float4 v;
         if (FMT == LORA_KV_BF16) {

@@ -1,16 +1,20 @@
 // Attention over the paged cache for many query rows per cache head (prefill chunks): the
 // products run on the tcgen05 tensor cores.
 //
-// A CTA takes tiles of NQ x 128 packed query rows (two row halves up to head_dim 128, one
-// at 256, where the output alone fills half of the tensor memory) against KT positions:
+// A CTA takes tiles of NQ x 128 packed query rows against KT positions.  Two row halves
+// (NQ = 2) read each K and V tile once for 256 rows; one half serves batches of fewer rows,
+// and head_dim 256, where the output alone fills half of the tensor memory.
 //   S = Q K^T        operands in shared memory, S in tensor memory (two buffers)
 //   P = 2^(c S - m)  one thread per row: maximum, exponential and sum without a shuffle;
 //                    P replaces S in place as packed bf16
 //   O += P V         P from tensor memory, V from shared memory as it lies (MN-major)
-// Roles: warp 0 fills a ring of K and V tiles by TMA (one box per page), warp 1 issues the
-// MMAs, eight warps (one row half each four) do the softmax.  The tensor cores work on one
-// half's products while the other half's softmax runs.  An accumulator is rescaled, in
-// tensor memory, only when a row's maximum rises by more than 2^8 (kMaxSlack).
+// Roles: warp 0 fills a ring of K and V tiles by TMA (one box per page); warp 1 (and, with
+// two halves, warp 2) issues the MMAs; warp 3 brings the next item's Q as soon as the last
+// scores of this one are done; four warps per row half do the softmax.  The tensor cores
+// work on one half's products while the other half's softmax runs (one issuing lane per
+// half, so that one lane's barrier work hides behind the other's MMAs); with one half, on
+// the next tile's scores.  An accumulator is rescaled, in tensor memory, only when a row's
+// maximum rises by more than 2^8 (kMaxSlack).
 //
 // 8-bit caches: the ring's raw tiles are turned into bf16 tiles by four more warps, once
 // for all the tile's rows (both formats' codes are bf16 numbers); a position's K scale
@@ -20,11 +24,10 @@
 
 namespace lgb {
 
-template <int D_, int FMT_>
+template <int D_, int FMT_, int NQ_>
 struct ManyCfg {
-  static constexpr int D = D_, FMT = FMT_;
+  static constexpr int D = D_, FMT = FMT_, NQ = NQ_;
   static constexpr bool kRaw = FMT != LORA_KV_BF16;
-  static constexpr int NQ = D == 256 ? 1 : 2;
   static constexpr int R = 128 * NQ;
   static constexpr int KT = D == 256 ? 64 : 128;
   static constexpr int kHalves = D / 64;                     // 128-byte columns of a bf16 row
@@ -33,19 +36,26 @@ struct ManyCfg {
   static constexpr int kRawRow = D, kRawBox = D < 128 ? D : 128, kRawBoxes = D / kRawBox;
   static constexpr int kRawTile = kRaw ? KT * D : 0;
   static constexpr int kRawStages = kRaw ? 3 : 0;
-  static constexpr int kStages = kRaw ? (D == 64 ? 6 : 3) : (D == 64 ? 8 : 5);
+  static constexpr int kStages = kRaw ? (D == 64 ? 6 : NQ == 1 && D == 128 ? 4 : 3) : (D == 64 ? 8 : 5);
   static constexpr int kScaleSlots = (kStages + 2) / 2;      // see the converting warps
   static constexpr int kConvWarps = kRaw ? 4 : 0;
   static constexpr int kSoftWarps = 4 * NQ;
-  static constexpr int kThreads = 32 * (2 + kSoftWarps + kConvWarps);
-  static constexpr bool kHold = !kRaw;                       // scores stay in registers between the two passes
+  static constexpr int kThreads = 32 * (4 + kSoftWarps + kConvWarps);
+  // Registers a thread of each warpgroup: what the block starts with (kRegs each; the file
+  // holds 65536), then shared out so that a softmax row's scores stay in registers.
+  static constexpr int kRegs = kThreads == 256 ? 248 : kThreads == 384 ? 168 : 128;
+  static constexpr bool kSplitRegs = kThreads > 256;
+  static constexpr int kSupportRegs = kRaw && NQ == 2 ? 56 : 80;
+  static constexpr int kSoftRegs = !kRaw ? 208 : NQ == 2 ? 192 : 240;
+  static constexpr int kConvRegs = NQ == 2 ? 72 : 128;
+  static_assert(!kSplitRegs || kSupportRegs + NQ * kSoftRegs + (kRaw ? kConvRegs : 0) <= kRegs * (kThreads / 128), "");
   static constexpr int kSCol0 = 0, kSCols = KT, kOCol0 = 256;
   static constexpr int kOffRing = NQ * kQBytes;
   static constexpr int kOffRaw = kOffRing + kStages * kTile;
   static constexpr int kOffRawScales = kOffRaw + kRawStages * kRawTile;
   static constexpr int kOffScales = kOffRawScales + (kRaw ? kRawStages * KT * 4 : 0);
   static constexpr int kOffBars = kOffScales + (kRaw ? kScaleSlots * 2 * KT * 4 : 0);
-  static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 2 * NQ + 2 + NQ + NQ + 1;
+  static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 4 + 3 * NQ + NQ;
   static constexpr int kOffPlan = kOffBars + kNumBars * 8 + 8;
   static constexpr int kSmem = kOffPlan + static_cast<int>(sizeof(PlanScratch<kThreads>)) + 1024;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -66,7 +76,7 @@ __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
 // Row halves of an item that hold rows of the sequence.
 template <class C>
 __device__ __forceinline__ int halves_of(const AttnParams& p, const Span& w) {
-  const long long rows = static_cast<long long>(w.s.n) * p.hs - static_cast<long long>(w.rt) * C::R;
+  const unsigned rows = static_cast<unsigned>(w.s.n) * p.hs - static_cast<unsigned>(w.rt) * C::R;
   return C::NQ == 2 && rows > 128 ? 2 : 1;
 }
 
@@ -87,33 +97,34 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
   auto rfull_bar = [&](int s) { return bar0 + 8u * (2 * ST + s); };              // a raw tile
   auto rempty_bar = [&](int s) { return bar0 + 8u * (2 * ST + RS + s); };
   constexpr int kB = 2 * ST + 2 * RS;
-  // scores of half q are in buffer b (a barrier for each pair: a half that an item does not
-  // use must not see phases go by)
-  auto sfull_bar = [&](int q, int b) { return bar0 + 8u * (kB + 2 * q + b); };
-  auto pready_bar = [&](int b) { return bar0 + 8u * (kB + 2 * C::NQ + b); };         // weights ready
-  auto odone_bar = [&](int q) { return bar0 + 8u * (kB + 2 * C::NQ + 2 + q); };      // a half's O += P V is done
-  auto qready_bar = [&](int q) { return bar0 + 8u * (kB + 3 * C::NQ + 2 + q); };
-  const uint32_t drain_bar = bar0 + 8u * (kB + 4 * C::NQ + 2);
+  // score buffer b: half b's with two halves, tile b modulo 2 with one
+  auto sfull_bar = [&](int b) { return bar0 + 8u * (kB + b); };                  // scores ready
+  auto pready_bar = [&](int b) { return bar0 + 8u * (kB + 2 + b); };             // weights ready
+  auto odone_bar = [&](int q) { return bar0 + 8u * (kB + 4 + q); };              // a half's O += P V is done
+  auto qready_bar = [&](int q) { return bar0 + 8u * (kB + 4 + C::NQ + q); };     // a half's Q is in place
+  auto qfree_bar = [&](int q) { return bar0 + 8u * (kB + 4 + 2 * C::NQ + q); };  // its last scores are done
+  auto drain_bar = [&](int q) { return bar0 + 8u * (kB + 4 + 3 * C::NQ + q); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(full_bar(s), C::kRaw ? C::kConvWarps : 1);
-      mbar_init(empty_bar(s), 1);
+      mbar_init(empty_bar(s), C::NQ);
     }
     for (int s = 0; s < RS; ++s) {
       mbar_init(rfull_bar(s), 1);
       mbar_init(rempty_bar(s), C::kConvWarps);
     }
     for (int b = 0; b < 2; ++b) {
-      for (int q = 0; q < C::NQ; ++q) mbar_init(sfull_bar(q, b), 1);
+      mbar_init(sfull_bar(b), 1);
       mbar_init(pready_bar(b), 4);
     }
     for (int q = 0; q < C::NQ; ++q) {
       mbar_init(odone_bar(q), 1);
-      mbar_init(qready_bar(q), 4);
+      mbar_init(qready_bar(q), 1);
+      mbar_init(qfree_bar(q), 1);
+      mbar_init(drain_bar(q), 1);
     }
-    mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_map(&p.kmap);
@@ -133,7 +144,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
   const Plan plan = scratch.plan;
   Walker<R, KT> walk(p, plan);
   Span w;
-
+  // (each warpgroup sets its registers at the head of its own branch: the compiler then
+  // allocates that branch by the new count)
+  if (warp < 4) {
+  if constexpr (C::kSplitRegs) regs_lower<C::kSupportRegs>();
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     const int ps = 1 << p.cache.page_shift;
@@ -207,113 +221,197 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
       for (int f = armed > NS ? armed - NS : (p.inject_stall ? 1 : 0); f < armed; ++f)
         attn_wait_drain(fbar(f % NS), (f / NS) & 1, p);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+  } else if (warp <= C::NQ) {
+    // ------------------------------------------------------------ MMA issuers, one lane per half
     if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, KT, 0, 0);
+      const int q = warp - 1;
       constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, 0, 1);
-      const uint64_t qdesc0 = smem_desc_sw128(sbase, 16u, 1024u);
+      // a negative scale negates Q as it is read (bit 13)
+      const uint32_t idesc_s = idesc_bf16_f32(128, KT, 0, 0) | (p.scale_log2 < 0.0f ? 1u << 13 : 0u);
+      const uint64_t qdesc = smem_desc_sw128(sbase + q * C::kQBytes, 16u, 1024u);
       const uint64_t kdesc0 = smem_desc_sw128(ring, 16u, 1024u);
       const uint64_t vdesc0 = smem_desc_sw128(ring, KT * 128u, 1024u);
       constexpr uint64_t kTileStep = C::kTile >> 4;
-      uint32_t tile = 0;              // ring tiles consumed before this item: K at tile + 2 i, V at tile + 2 i + 1
-      uint32_t T = 0;                 // score tiles of this CTA so far: buffer T & 1
-      uint32_t items[2] = {0, 0};     // items that used each half
-      bool ok = true;
-      while (ok && walk.next(p, w)) {
-        const int nq = halves_of<C>(p, w), n = w.jb - w.ja, total = n * nq;
-        for (int q = 0; q < nq && ok; ++q) {
-          ok = attn_wait(qready_bar(q), items[q] & 1u, abort_flag, p);
-          ++items[q];
-        }
-        if (!ok) break;
-        auto issue_s = [&](int t) {   // scores of (position tile t / nq, half t % nq)
-          const int i = nq == 2 ? t >> 1 : t, q = nq == 2 ? t & 1 : 0;
-          const uint32_t idx = tile + 2u * i, st = idx % ST;
-          if (q == 0 && !attn_wait(full_bar(st), (idx / ST) & 1u, abort_flag, p)) return false;
-          tc_fence_after_sync();
-          const uint32_t d = tmem + C::kSCol0 + ((T + t) & 1u) * C::kSCols;
-          const uint64_t a = qdesc0 + static_cast<uint64_t>(q) * (C::kQBytes >> 4), b = kdesc0 + st * kTileStep;
+      const uint32_t o_tmem = tmem + C::kOCol0 + q * D;
+      auto scores = [&](int st, int buf) {
+        const uint32_t d = tmem + C::kSCol0 + buf * C::kSCols;
+        const uint64_t b = kdesc0 + st * kTileStep;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc_mma_bf16(d, a + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, b + (k >> 2) * (KT * 128 >> 4) + (k & 3) * 2,
-                        idesc_s, k > 0 ? 1u : 0u);
-          tc_commit(sfull_bar(q, (T + t) & 1u));
-          if (q == nq - 1) tc_commit(empty_bar(st));
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma_bf16(d, qdesc + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, b + (k >> 2) * (KT * 128 >> 4) + (k & 3) * 2,
+                      idesc_s, k > 0 ? 1u : 0u);
+      };
+      auto values = [&](int st, int buf, bool first) {
+        const uint32_t a = tmem + C::kSCol0 + buf * C::kSCols;
+        const uint64_t b = vdesc0 + st * kTileStep;
+#pragma unroll
+        for (int k = 0; k < KT / 16; ++k)
+          tc_mma_bf16_ts(o_tmem, a + 8 * k, b + k * (2048 >> 4), idesc_o, (k > 0 || !first) ? 1u : 0u);
+      };
+      int st = 0;                         // ring stage and its phase
+      uint32_t ph = 0, qphase = 0, pphase = 0;
+      auto step = [&](int& s, uint32_t& f) { if (++s == ST) { s = 0; f ^= 1u; } };
+      bool ok = true;
+      if constexpr (C::NQ == 2) {
+        // per tile: S, then O += P V; the other half's lane fills the tensor cores meanwhile
+        while (ok && walk.next(p, w)) {
+          const bool mine = q < halves_of<C>(p, w);
+          if (mine) {
+            ok = attn_wait(qready_bar(q), qphase, abort_flag, p);
+            qphase ^= 1u;
+          }
+          for (int j = w.ja; ok && j < w.jb; ++j) {
+            ok = attn_wait(full_bar(st), ph, abort_flag, p);
+            if (!ok) break;
+            if (mine) {
+              tc_fence_after_sync();
+              scores(st, q);
+              tc_commit(sfull_bar(q));
+              tc_commit(empty_bar(st));
+              if (j + 1 == w.jb) tc_commit(qfree_bar(q));
+            } else {
+              mbar_arrive(empty_bar(st));     // every lane follows the ring's phases
+            }
+            step(st, ph);
+            ok = attn_wait(full_bar(st), ph, abort_flag, p);
+            if (ok && mine) {
+              ok = attn_wait(pready_bar(q), pphase, abort_flag, p);
+              pphase ^= 1u;
+            }
+            if (!ok) break;
+            if (mine) {
+              tc_fence_after_sync();
+              values(st, q, j == w.ja);
+              tc_commit(odone_bar(q));
+              tc_commit(empty_bar(st));
+            } else {
+              mbar_arrive(empty_bar(st));
+            }
+            step(st, ph);
+          }
+        }
+      } else {
+        // the scores of tile t + 1 (the next item's too) are issued before tile t's O += P V
+        uint32_t T = 0;                   // tiles so far: score buffer T & 1
+        auto next_scores = [&](bool new_item, bool last) {
+          if (new_item) {
+            if (!attn_wait(qready_bar(0), qphase, abort_flag, p)) return false;
+            qphase ^= 1u;
+          }
+          if (!attn_wait(full_bar(st), ph, abort_flag, p)) return false;
+          tc_fence_after_sync();
+          scores(st, T & 1u);
+          tc_commit(sfull_bar(T & 1u));
+          tc_commit(empty_bar(st));
+          if (last) tc_commit(qfree_bar(0));
+          ++T;
+          step(st, ph);
           return true;
         };
-        ok = issue_s(0);
-        for (int t = 0; t < total && ok; ++t) {
-          if (t + 1 < total) ok = issue_s(t + 1);
+        // ring order: K of tile t + 1 stands after V of tile t, so V's stage is remembered
+        bool more = walk.next(p, w);
+        int j = more ? w.ja : 0;
+        if (more) ok = next_scores(true, w.ja + 1 == w.jb);
+        while (ok && more) {
+          const bool first = j == w.ja;
+          const int vst = st;
+          const uint32_t vph = ph, buf = (T - 1u) & 1u;
+          step(st, ph);
+          if (++j == w.jb) {
+            more = walk.next(p, w);
+            if (more) {
+              j = w.ja;
+              ok = next_scores(true, w.ja + 1 == w.jb);
+            }
+          } else {
+            ok = next_scores(false, j + 1 == w.jb);
+          }
+          if (ok) ok = attn_wait(full_bar(vst), vph, abort_flag, p);
+          if (ok) ok = attn_wait(pready_bar(buf), (pphase >> buf) & 1u, abort_flag, p);
           if (!ok) break;
-          const int i = nq == 2 ? t >> 1 : t, q = nq == 2 ? t & 1 : 0;
-          const uint32_t idx = tile + 2u * i + 1u, st = idx % ST, buf = (T + t) & 1u;
-          if (q == 0) ok = attn_wait(full_bar(st), (idx / ST) & 1u, abort_flag, p);
-          if (ok) ok = attn_wait(pready_bar(buf), ((T + t) >> 1) & 1u, abort_flag, p);
-          if (!ok) break;
+          pphase ^= 1u << buf;
           tc_fence_after_sync();
-          const uint32_t d = tmem + C::kOCol0 + q * D, a = tmem + C::kSCol0 + buf * C::kSCols;
-          const uint64_t b = vdesc0 + st * kTileStep;
-#pragma unroll
-          for (int k = 0; k < KT / 16; ++k)
-            tc_mma_bf16_ts(d, a + 8 * k, b + k * (2048 >> 4), idesc_o, (i > 0 || k > 0) ? 1u : 0u);
-          tc_commit(odone_bar(q));
-          if (q == nq - 1) tc_commit(empty_bar(st));
+          values(vst, buf, first);
+          tc_commit(odone_bar(0));
+          tc_commit(empty_bar(vst));
         }
-        T += total;
-        tile += 2u * n;
       }
       if (!ok) {
-        tc_commit(drain_bar);
-        attn_wait_drain(drain_bar, 0, p);
+        tc_commit(drain_bar(q));
+        attn_wait_drain(drain_bar(q), 0, p);
       }
     }
-  } else if (warp < 2 + C::kSoftWarps) {
-    // ------------------------------------------------------------ softmax
-    const int q = (warp - 2) >> 2;                // row half
-    const int quarter = warp & 3;                 // TMEM lanes of this warp
-    const int r = quarter * 32 + lane;            // row of the half
-    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t o_tmem = tmem + lanes + C::kOCol0 + q * D;
-    const float c = fabsf(p.scale_log2);
-    const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;    // a negative scale turns Q's signs
-    uint32_t T = 0, tile = 0, done = 0;           // done: O += P V steps of this half so far
-    uint32_t sphase = 0;                          // bit b: phase of this half's score buffer b
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ Q loader
+    uint32_t used[2] = {0, 0};            // items of each half so far
     bool ok = true;
     while (ok && walk.next(p, w)) {
-      const int nq = halves_of<C>(p, w), n = w.jb - w.ja;
-      if (q >= nq) {
-        T += n * nq;
-        tile += 2u * n;
-        continue;
-      }
-      int tok, head, lo, hi;
-      const bool own = row_owner(p, w.s, w.slice, static_cast<long long>(w.rt) * R + q * 128 + r, tok, head);
-      if (own) row_range(p, w.s, tok, lo, hi); else lo = 0, hi = 0x7fffffff;
-      const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
-      // this row of Q into shared memory, K-major with the 128-byte swizzle
-      {
-        const bf16* x = p.q.x + static_cast<long long>(w.s.q0 + tok) * p.q.ts + head * p.q.hs;
-        const uint32_t dst = sbase + q * C::kQBytes + r * 128;
-#pragma unroll
-        for (int e = 0; e < D / 8; ++e) {
-          uint4 v = own ? __ldg(reinterpret_cast<const uint4*>(x) + e) : make_uint4(0, 0, 0, 0);
-          v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-          st_shared_v4(dst + (e >> 3) * (128 * 128) + (((e & 7) ^ (r & 7)) << 4), v);
+      const int nq = halves_of<C>(p, w);
+#pragma unroll 1
+      for (int q = 0; q < nq; ++q) {
+        if (used[q] > 0) ok = attn_wait(qfree_bar(q), (used[q] - 1u) & 1u, abort_flag, p);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++used[q];
+        // rows to shared memory, K-major with the 128-byte swizzle; rows that are nobody's are 0
+        constexpr int kPieces = D / 8, kRows = 32 / kPieces > 0 ? 32 / kPieces : 1;
+#pragma unroll 1
+        for (int r0 = 0; r0 < 128; r0 += 32) {
+          int tok, head;
+          const bool own = row_owner(p, w.s, w.slice, static_cast<unsigned>(w.rt) * R + q * 128 + r0 + lane, tok, head);
+          const long long at = own ? static_cast<long long>(w.s.q0 + tok) * p.q.ts + head * p.q.hs : -1;
+#pragma unroll 4
+          for (int x = 0; x < 32; x += kRows) {
+            const int rr = x + lane / kPieces, e = lane % kPieces, r = r0 + rr;
+            const long long from = __shfl_sync(0xffffffffu, at, rr);
+            const uint32_t dst = sbase + q * C::kQBytes + r * 128 + (e >> 3) * (128 * 128) + (((e & 7) ^ (r & 7)) << 4);
+            cp_async_16(dst, p.q.x + (from < 0 ? 0 : from) + 8 * e, from < 0 ? 0u : 16u);
+          }
         }
+        cp_async_wait_all();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(qready_bar(q));
       }
-      float top = -INFINITY, sum = 0.0f;
+    }
+  }
+  } else if (warp < 4 + C::kSoftWarps) {
+    if constexpr (C::kSplitRegs) regs_raise<C::kSoftRegs>();
+    // ------------------------------------------------------------ softmax
+    const int q = (warp - 4) >> 2;                // row half
+    const int quarter = warp & 3;                 // TMEM lanes of this warp
+    const int r = quarter * 32 + lane;            // row of the half
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t o_tmem = tmem + lanes + C::kOCol0 + q * D;
+    // (a scale of 0 becomes the smallest normal one: finite scores weigh the same, and a
+    // hidden score stays -inf)
+    const float c = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
+    const bool out_v8 = rows_v8_aligned(p.out, 16);
+    uint32_t T = 0, tile = 0;                     // position tiles, ring tiles before this item
+    uint32_t done = 0;                            // O += P V steps of this half so far
+    uint32_t sphase = 0;                          // bit b: phase of score buffer b
+    bool ok = true;
+    while (ok && walk.next(p, w)) {
+      const int nq = halves_of<C>(p, w), n = w.jb - w.ja;
+      if (q >= nq) {
+        T += n;
+        tile += 2u * n;
+        continue;
+      }
+      int tok, head, lo, hi;
+      const bool own = row_owner(p, w.s, w.slice, static_cast<unsigned>(w.rt) * R + q * 128 + r, tok, head);
+      if (own) row_range(p, w.s, tok, lo, hi); else lo = 0, hi = 0x7fffffff;
+      const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
+      float top = -INFINITY;
+      float2 sum = make_float2(0.0f, 0.0f);          // two partial sums
       for (int i = 0; i < n; ++i) {
-        const uint32_t t = T + (nq == 2 ? 2 * i + q : i), buf = t & 1u;
+        const uint32_t buf = C::NQ == 2 ? q : (T + i) & 1u;
         const int k0 = (w.ja + i) * KT;
         const uint32_t s_tmem = tmem + lanes + C::kSCol0 + buf * C::kSCols;
         const uint32_t vidx = tile + 2u * i + 1u;
         const float* ks = nullptr;
         const float* vs = nullptr;
-        ok = attn_wait(sfull_bar(q, buf), (sphase >> buf) & 1u, abort_flag, p);
+        ok = attn_wait(sfull_bar(buf), (sphase >> buf) & 1u, abort_flag, p);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         sphase ^= 1u << buf;
         if (C::kRaw) {
@@ -326,45 +424,37 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         }
         tc_fence_after_sync();
         const bool edge = k0 < lo_max || k0 + KT > hi_min;
-        // scores of columns [x, x + 32) of this row: K scales, mask
-        auto scores = [&](int x, float (&s)[32]) {
-          uint32_t v[32];
-          tmem_ld32(s_tmem + x, v);
-          tmem_ld_wait();
+        // this row's scores, all at once: K scales, mask, maximum
+        float s[KT];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(v[e]);
-          if (C::kRaw) {
+        for (int x = 0; x < KT; x += 32) tmem_ld32(s_tmem + x, *reinterpret_cast<uint32_t(*)[32]>(&s[x]));
+        tmem_ld_wait();
+        if (C::kRaw) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(ks + x + e);
-              s[e] *= f.x, s[e + 1] *= f.y, s[e + 2] *= f.z, s[e + 3] *= f.w;
-            }
+          for (int e = 0; e < KT; e += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(ks + e);
+            const float2 a = mul_f32x2(make_float2(s[e], s[e + 1]), make_float2(f.x, f.y));
+            const float2 b = mul_f32x2(make_float2(s[e + 2], s[e + 3]), make_float2(f.z, f.w));
+            s[e] = a.x, s[e + 1] = a.y, s[e + 2] = b.x, s[e + 3] = b.y;
           }
-          if (edge) {
+        }
+        if (edge) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int key = k0 + x + e;
-              s[e] = key >= lo && key < hi ? s[e] : -INFINITY;
-            }
-          }
-        };
-        float held[C::kHold ? KT / 32 : 1][32];
+          for (int e = 0; e < KT; ++e) s[e] = k0 + e >= lo && k0 + e < hi ? s[e] : -INFINITY;
+        }
         float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int x = 0; x < KT / 32; ++x) {
-          float(&s)[32] = held[C::kHold ? x : 0];
-          scores(32 * x, s);
+        for (int e = 0; e < KT; e += 8) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], s[e]);
+          for (int k = 0; k < 4; ++k) m[k] = fmaxf(fmaxf(m[k], s[e + 2 * k]), s[e + 2 * k + 1]);
         }
-        const float tile_top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
-        // (0 * -inf is NaN: with a scale of 0 a hidden row's maximum must stay -inf)
-        const float cand = tile_top != tile_top ? (c == 0.0f ? -INFINITY : tile_top) : tile_top;
+        const float cand = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
         if (__any_sync(0xffffffffu, cand > top + kMaxSlack)) {
           const float next = fmaxf(top, cand);
           const float f = next == -INFINITY ? 1.0f : exp2_approx(top - next);
           top = next;
-          sum *= f;
+          sum.x *= f;
+          sum.y *= f;
           if (i > 0) {
             ok = attn_wait(odone_bar(q), (done - 1u) & 1u, abort_flag, p);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -382,34 +472,40 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           }
         }
         const float ref = top == -INFINITY ? 0.0f : top;
-        float l[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const float2 c2 = make_float2(c, c), ref2 = make_float2(-ref, -ref);
+        float2 l[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-        for (int x = 0; x < KT / 32; ++x) {
-          float(&s)[32] = held[C::kHold ? x : 0];
-          if (!C::kHold) scores(32 * x, s);
+        for (int x = 0; x < KT; x += 32) {
           uint32_t u[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            float y[4];
+          for (int e = x; e < x + 32; e += 4) {
+            float2 y[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              // a hidden score is -inf: its weight is 0 for every finite scale but 0
-              y[k] = exp2_approx(fmaf(s[e + k], c, -ref));
-              if (edge && s[e + k] == -INFINITY) y[k] = 0.0f;
-              l[k] += y[k];
+            for (int k = 0; k < 2; ++k) {
+              y[k] = fma_f32x2(make_float2(s[e + 2 * k], s[e + 2 * k + 1]), c2, ref2);
+              y[k].x = exp2_approx(y[k].x);
+              y[k].y = exp2_approx(y[k].y);
+              l[k] = add_f32x2(l[k], y[k]);
             }
             if (C::kRaw) {
-              const float4 f = *reinterpret_cast<const float4*>(vs + 32 * x + e);
-              const float g[4] = {f.x, f.y, f.z, f.w};
+              const float4 f = *reinterpret_cast<const float4*>(vs + e);
+              y[0] = mul_f32x2(y[0], make_float2(f.x, f.y));
+              y[1] = mul_f32x2(y[1], make_float2(f.z, f.w));
+              if (edge) {                 // a hidden position's scale may be anything
 #pragma unroll
-              for (int k = 0; k < 4; ++k) y[k] = edge && s[e + k] == -INFINITY ? 0.0f : y[k] * g[k];
+                for (int k = 0; k < 2; ++k) {
+                  if (s[e + 2 * k] == -INFINITY) y[k].x = 0.0f;
+                  if (s[e + 2 * k + 1] == -INFINITY) y[k].y = 0.0f;
+                }
+              }
             }
-            u[e / 2] = pack_bf16x2(y[0], y[1]);
-            u[e / 2 + 1] = pack_bf16x2(y[2], y[3]);
+            u[(e - x) / 2] = pack_bf16x2(y[0].x, y[0].y);
+            u[(e - x) / 2 + 1] = pack_bf16x2(y[1].x, y[1].y);
           }
-          tmem_st16(s_tmem + 16 * x, u);
+          tmem_st16(s_tmem + x / 2, u);
         }
-        sum += (l[0] + l[1]) + (l[2] + l[3]);
+        l[0] = add_f32x2(l[0], l[1]);
+        sum = add_f32x2(sum, l[0]);
         tmem_st_wait();
         if (!C::kRaw && k0 + KT > w.s.kv) {
           // rows of V past the sequence hold anything, and zero weights do not silence a
@@ -427,7 +523,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         if (lane == 0) mbar_arrive(pready_bar(buf));
         ++done;
       }
-      T += n * nq;
+      T += n;
       tile += 2u * n;
       if (!ok) break;
       ok = attn_wait(odone_bar(q), (done - 1u) & 1u, abort_flag, p);
@@ -435,35 +531,38 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
       tc_fence_after_sync();
       const bool whole = w.starts && w.ends;
       const long long slot = 2ll * blockIdx.x + (w.starts ? 1 : 0);
-      const bool none = top == -INFINITY && sum == 0.0f;
-      const float inv = whole ? (none ? 0.0f : 1.0f / sum) : 1.0f;
+      const float all = sum.x + sum.y;
+      const bool none = top == -INFINITY && all == 0.0f;
+      const float inv = none ? 0.0f : 1.0f / all;
       const long long orow = static_cast<long long>(w.s.q0 + tok) * p.hq + head;
       const long long prow = slot * R + q * 128 + r;
-#pragma unroll 1
-      for (int x = 0; x < D; x += 32) {
-        uint32_t v[32];
+#pragma unroll
+      for (int x = 0; x < D; x += 64) {
+        uint32_t v[2][32];
         __syncwarp();
-        tmem_ld32(o_tmem + x, v);
+        tmem_ld32(o_tmem + x, v[0]);
+        tmem_ld32(o_tmem + x + 32, v[1]);
         tmem_ld_wait();
         if (!own) continue;
-        if (whole) {
-          uint32_t u[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            u[e] = none ? 0u : pack_bf16x2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
+        for (int h = 0; h < 2; ++h) {
+          if (whole) {
+            uint32_t u[16];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(p.out + orow * D + x + 8 * e) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
-        } else {
+            for (int e = 0; e < 16; ++e)
+              u[e] = none ? 0u : pack_bf16x2(__uint_as_float(v[h][2 * e]) * inv, __uint_as_float(v[h][2 * e + 1]) * inv);
+            store_row32_bf16(p.out + orow * D + x + 32 * h, u, 0, 32, out_v8);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) st_global_v8(p.part_o + prow * D + x + e, v + e);
+            for (int e = 0; e < 32; e += 8) st_global_v8(p.part_o + prow * D + x + 32 * h + e, v[h] + e);
+          }
         }
       }
       if (own) {
         if (!whole)
-          p.part_ml[prow] = make_float2(top, sum);
+          p.part_ml[prow] = make_float2(top, all);
         else if (p.lse != nullptr)
-          p.lse[orow] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+          p.lse[orow] = none ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
       }
       tc_fence_before_sync();
       __syncwarp();
@@ -471,7 +570,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
   } else {
     // ------------------------------------------------------------ converting warps (8-bit)
     if constexpr (C::kRaw) {
-      const int cw = warp - 2 - C::kSoftWarps, tid = cw * 32 + lane;
+      if constexpr (C::kSplitRegs) regs_lower<C::kConvRegs>();
+      const int cw = warp - 4 - C::kSoftWarps, tid = cw * 32 + lane;
       uint32_t idx = 0;
       bool ok = true;
       while (ok && walk.next(p, w)) {
@@ -559,6 +659,14 @@ static lora_status_t launch_many(AttnParams& p, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   if (!encode_pages(p, C::D, C::kRaw ? 1 : 2, C::kRaw ? C::kRawBox : 128, C::KT)) return LORA_ERR_CUDA;
   if (ensure_smem_limit(attn_many_kernel<C>, C::kSmem, done) != cudaSuccess) return LORA_ERR_CUDA;
+  if constexpr (C::kSplitRegs) {
+    // the warpgroups' shares must fit what the block is launched with: checked once
+    static const bool fits = [] {
+      cudaFuncAttributes a;
+      return cudaFuncGetAttributes(&a, attn_many_kernel<C>) == cudaSuccess && a.numRegs >= C::kRegs;
+    }();
+    if (!fits) return LORA_ERR_CUDA;
+  }
   int grid = num_sms();
   grid = grid > kMaxManyCtas ? kMaxManyCtas : grid;
   p.spg = static_cast<int>(ceil_div(p.group, C::R));
@@ -568,16 +676,17 @@ static lora_status_t launch_many(AttnParams& p, cudaStream_t st) {
   return launch_counted(join_kernel<C::D, C::R>, dim3(grid, 16), dim3(128), 0, LORA_KIND_ATTN, st, p);
 }
 
-template <int D>
+template <int D, int NQ>
 static lora_status_t launch_many_d(AttnParams& p, int format, cudaStream_t st) {
-  return format == LORA_KV_BF16 ? launch_many<ManyCfg<D, LORA_KV_BF16>>(p, st)
-                                : format == LORA_KV_FP8 ? launch_many<ManyCfg<D, LORA_KV_FP8>>(p, st)
-                                                        : launch_many<ManyCfg<D, LORA_KV_INT8>>(p, st);
+  return format == LORA_KV_BF16 ? launch_many<ManyCfg<D, LORA_KV_BF16, NQ>>(p, st)
+                                : format == LORA_KV_FP8 ? launch_many<ManyCfg<D, LORA_KV_FP8, NQ>>(p, st)
+                                                        : launch_many<ManyCfg<D, LORA_KV_INT8, NQ>>(p, st);
 }
 
-lora_status_t launch_attn_many(AttnParams& p, int head_dim, int format, cudaStream_t st) {
-  return head_dim == 64 ? launch_many_d<64>(p, format, st) : head_dim == 128 ? launch_many_d<128>(p, format, st)
-                                                                             : launch_many_d<256>(p, format, st);
+lora_status_t launch_attn_many(AttnParams& p, int halves, int head_dim, int format, cudaStream_t st) {
+  if (head_dim == 256) return launch_many_d<256, 1>(p, format, st);
+  if (head_dim == 128) return halves == 2 ? launch_many_d<128, 2>(p, format, st) : launch_many_d<128, 1>(p, format, st);
+  return halves == 2 ? launch_many_d<64, 2>(p, format, st) : launch_many_d<64, 1>(p, format, st);
 }
 
 }  // namespace lgb

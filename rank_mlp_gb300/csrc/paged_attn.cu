@@ -5,14 +5,16 @@
 namespace lgb {
 
 // Which kernel: the one whose tiles the rows fill.  A call's lengths are on the device, so
-// the rule takes the mean number of query rows that share a cache head.
-static bool many_rows_call(int64_t M, int64_t n_seqs, int group) {
-  return M * group > kFewRows * n_seqs;
+// the rule takes the mean number of query rows that share a cache head.  Returns the row
+// halves of the tcgen05 kernel, or 0 for the few-row kernel.
+static int row_halves(int64_t M, int64_t n_seqs, int group, int head_dim) {
+  if (M * group <= kFewRows * n_seqs) return 0;
+  return head_dim == 256 || M * group <= 128 * n_seqs ? 1 : 2;
 }
 
 // Workspace: header, the parts' descriptors, maxima and sums, outputs.
-static void carve_parts(Carve& c, bool many, int head_dim, AttnParams& p) {
-  const int64_t ctas = many ? kMaxManyCtas : kMaxFewCtas, rows = 2 * ctas * (many ? many_rows(head_dim) : kFewRows);
+static void carve_parts(Carve& c, int halves, int head_dim, AttnParams& p) {
+  const int64_t ctas = halves ? kMaxManyCtas : kMaxFewCtas, rows = 2 * ctas * (halves ? 128 * halves : kFewRows);
   c.take(kWsHeader);
   p.join = c.take_n<JoinDesc>(ctas);
   p.part_ml = c.take_n<float2>(rows);
@@ -25,12 +27,12 @@ using namespace lgb;
 
 extern "C" size_t lora_paged_attention_workspace_bytes(int64_t M, int64_t n_seqs, int heads_q,
                                                        const lora_kv_cache_t* cache) {
-  if (M < 0 || M > kMaxExtent || n_seqs < 1 || n_seqs > kMaxExtent || heads_q < 1 || check_cache(cache) != LORA_OK ||
+  if (M < 0 || n_seqs < 1 || n_seqs > kMaxExtent || heads_q < 1 || M > kMaxExtent / heads_q || check_cache(cache) != LORA_OK ||
       heads_q % cache->heads)
     return 0;
   AttnParams p;
   Carve c(nullptr);
-  carve_parts(c, many_rows_call(M, n_seqs, heads_q / cache->heads), cache->head_dim, p);
+  carve_parts(c, row_halves(M, n_seqs, heads_q / cache->heads, cache->head_dim), cache->head_dim, p);
   return c.off;
 }
 
@@ -44,7 +46,7 @@ extern "C" lora_status_t lora_paged_attention(int64_t M, int heads_q, const lora
     return LORA_ERR_INVALID_ARG;
   LGB_TRY(check_cache(cache));
   if (heads_q < 1 || heads_q % cache->heads || q->heads != heads_q) return LORA_ERR_INVALID_ARG;
-  if (M > kMaxExtent || batch->n_seqs > kMaxExtent || batch->max_pages > kMaxExtent / cache->page_size)
+  if (M > kMaxExtent / heads_q || batch->n_seqs > kMaxExtent || batch->max_pages > kMaxExtent / cache->page_size)
     return LORA_ERR_UNSUPPORTED;
   LGB_TRY(check_heads_in(q));
   if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(batch->page_table, 4) || !aligned(batch->kv_len, 4) ||
@@ -73,8 +75,8 @@ extern "C" lora_status_t lora_paged_attention(int64_t M, int heads_q, const lora
   p.timeout_ns = wait_timeout_ns();
   p.inject_stall = take_expiry();
   Carve c(ws);
-  const bool many = many_rows_call(M, batch->n_seqs, p.group);
-  carve_parts(c, many, cache->head_dim, p);
-  return many ? launch_attn_many(p, cache->head_dim, cache->format, stream)
-              : launch_attn_few(p, cache->head_dim, cache->format, stream);
+  const int halves = row_halves(M, batch->n_seqs, p.group, cache->head_dim);
+  carve_parts(c, halves, cache->head_dim, p);
+  return halves ? launch_attn_many(p, halves, cache->head_dim, cache->format, stream)
+                : launch_attn_few(p, cache->head_dim, cache->format, stream);
 }

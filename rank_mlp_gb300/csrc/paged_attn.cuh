@@ -63,16 +63,17 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b, bool report)
   return s;
 }
 
+// (packed rows are below 2^31: M * heads_q is)
 template <int R>
 __device__ __forceinline__ int row_tiles(const AttnParams& p, const Seq& s) {
-  return static_cast<int>((static_cast<long long>(s.n) * p.hs + R - 1) / R);
+  return static_cast<int>((static_cast<unsigned>(s.n) * p.hs + R - 1) / R);
 }
 
 // Tiles [j0, j1) of KT positions that row tile rt sees any of; one empty tile if none.
 template <int R, int KT>
 __device__ __forceinline__ void item_tiles(const AttnParams& p, const Seq& s, int rt, int& j0, int& j1) {
-  const long long r0 = static_cast<long long>(rt) * R;
-  const int t0 = static_cast<int>(r0 / p.hs), t1 = min(s.n - 1, static_cast<int>((r0 + R - 1) / p.hs));
+  const unsigned r0 = static_cast<unsigned>(rt) * R, hs = p.hs;
+  const int t0 = static_cast<int>(r0 / hs), t1 = min(s.n - 1, static_cast<int>((r0 + R - 1) / hs));
   const int off = s.kv - s.n;
   const int hi = p.causal ? max(0, min(s.kv, off + t1 + 1)) : s.kv;
   const int lo = p.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(off) + t0 - p.window + 1)) : 0;
@@ -88,9 +89,9 @@ __device__ __forceinline__ void row_range(const AttnParams& p, const Seq& s, int
 }
 
 // Token and query head of packed row pr of a slice; false past the sequence or the slice.
-__device__ __forceinline__ bool row_owner(const AttnParams& p, const Seq& s, int slice, long long pr, int& tok, int& head) {
-  tok = static_cast<int>(pr / p.hs);
-  const int g = static_cast<int>(pr - static_cast<long long>(tok) * p.hs);
+__device__ __forceinline__ bool row_owner(const AttnParams& p, const Seq& s, int slice, unsigned pr, int& tok, int& head) {
+  tok = static_cast<int>(pr / static_cast<unsigned>(p.hs));
+  const int g = static_cast<int>(pr) - tok * p.hs;
   const int kvh = slice / p.spg, first = (slice - kvh * p.spg) * p.hs;
   head = kvh * p.group + first + g;
   return tok < s.n && first + g < p.group;
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnP
   const int col = threadIdx.x % kCols;
   for (int r = blockIdx.y * (128 / kCols) + threadIdx.x / kCols; r < R; r += gridDim.y * (128 / kCols)) {
     int tok, head;
-    if (!row_owner(p, s, d.slice, static_cast<long long>(d.rt) * R + r, tok, head)) continue;
+    if (!row_owner(p, s, d.slice, static_cast<unsigned>(d.rt) * R + r, tok, head)) continue;
     const float2* ml = p.part_ml + r;
     float top = -INFINITY;
 #pragma unroll 4
@@ -375,8 +376,8 @@ constexpr int kMaxFewCtas = 320;
 constexpr int kMaxManyCtas = 160;
 
 constexpr int kFewRows = 16;          // rows of the few-row kernel's tiles
-constexpr int many_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
-lora_status_t launch_attn_many(AttnParams& p, int head_dim, int format, cudaStream_t st);
+// The many-row kernel's tiles: one or two row halves of 128 (one at head_dim 256).
+lora_status_t launch_attn_many(AttnParams& p, int halves, int head_dim, int format, cudaStream_t st);
 lora_status_t launch_attn_few(AttnParams& p, int head_dim, int format, cudaStream_t st);
 
 // The cache's pages as rows, in boxes of at most `tile` rows of one page.
