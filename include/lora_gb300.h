@@ -381,7 +381,7 @@ typedef struct {
  * out bf16 [M x heads_q x head_dim], dense (the O projection's input); lse f32 [M x
  * heads_q] or NULL receives ln sum_j e^(s_j).  A token that sees nothing (kv_len 0, or
  * p < 0) gets out 0 and lse -inf.  Rows of M that no sequence owns are not written.
- * q is a view; heads_q is a multiple of the cache's heads, and M * heads_q at most 2^31 - 1.
+ * q is a view (of strides above 0); heads_q is a multiple of the cache's heads, and M * heads_q at most 2^31 - 1.
  * Scores, maxima, sums and the accumulated output are f32; the weights e^(...) are
  * rounded to bf16 before they multiply V (as the matrix units take them), and the
  * result is rounded once.  What lies past kv_len in a page is not looked at, whatever

@@ -75,12 +75,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
-  make_plan<R, KT, C::kThreads>(p, scratch);
+  make_plan<KT, C::kThreads>(p, scratch);
   const Plan plan = scratch.plan;
   if (threadIdx.x == 0) p.join[blockIdx.x].parts = 0;     // set below by the item that starts here and goes on
   if (plan.units == 0) return;
 
-  Walker<R, KT> walk(p, plan);
+  Walker<KT> walk(p, plan);
   Span w;
   int stage = 0;
   uint32_t phase = 0;
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
     bool own[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      own[h] = row_owner(p, w.s, w.slice, static_cast<unsigned>(w.rt) * R + r0 + 8 * h, tok[h], head[h]);
+      own[h] = row_owner(p, w.s, w.slice, w.rt, 0, r0 + 8 * h, tok[h], head[h]);
       if (own[h]) row_range(p, w.s, tok[h], lo[h], hi[h]); else lo[h] = 0, hi[h] = 0;
     }
     // the tile rows' common range: tiles inside it need no mask
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
       constexpr int kLanes = D / 4;                 // threads of a row, four features each
       for (int r = threadIdx.x / kLanes; r < R; r += 128 / kLanes) {
         int tk, hd;
-        if (!row_owner(p, w.s, w.slice, static_cast<unsigned>(w.rt) * R + r, tk, hd)) continue;
+        if (!row_owner(p, w.s, w.slice, w.rt, 0, r, tk, hd)) continue;
         const int f = (threadIdx.x % kLanes) * 4;
         float4 v;
         if (FMT == LORA_KV_BF16) {
@@ -446,9 +446,7 @@ static lora_status_t launch_few_d(AttnParams& p, int format, cudaStream_t st) {
 }
 
 lora_status_t launch_attn_few(AttnParams& p, int head_dim, int format, cudaStream_t st) {
-  p.spg = static_cast<int>(ceil_div(p.group, kFewRows));
-  p.hs = static_cast<int>(ceil_div(p.group, p.spg));
-  p.slices = p.cache.heads * p.spg;
+  set_tiles(p, kFewRows, 1);
   return head_dim == 64 ? launch_few_d<64>(p, format, st) : head_dim == 128 ? launch_few_d<128>(p, format, st)
                                                                             : launch_few_d<256>(p, format, st);
 }

@@ -55,7 +55,7 @@ struct ManyCfg {
   static constexpr int kOffRawScales = kOffRaw + kRawStages * kRawTile;
   static constexpr int kOffScales = kOffRawScales + (kRaw ? kRawStages * KT * 4 : 0);
   static constexpr int kOffBars = kOffScales + (kRaw ? kScaleSlots * 2 * KT * 4 : 0);
-  static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 4 + 3 * NQ + NQ;
+  static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 8 + 4 * NQ;
   static constexpr int kOffPlan = kOffBars + kNumBars * 8 + 8;
   static constexpr int kSmem = kOffPlan + static_cast<int>(sizeof(PlanScratch<kThreads>)) + 1024;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -76,8 +76,7 @@ __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
 // Row halves of an item that hold rows of the sequence.
 template <class C>
 __device__ __forceinline__ int halves_of(const AttnParams& p, const Span& w) {
-  const unsigned rows = static_cast<unsigned>(w.s.n) * p.hs - static_cast<unsigned>(w.rt) * C::R;
-  return C::NQ == 2 && rows > 128 ? 2 : 1;
+  return C::NQ == 2 && w.s.n - w.rt * p.tt > p.th ? 2 : 1;
 }
 
 template <class C>
@@ -99,11 +98,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
   constexpr int kB = 2 * ST + 2 * RS;
   // score buffer b: half b's with two halves, tile b modulo 2 with one
   auto sfull_bar = [&](int b) { return bar0 + 8u * (kB + b); };                  // scores ready
-  auto pready_bar = [&](int b) { return bar0 + 8u * (kB + 2 + b); };             // weights ready
-  auto odone_bar = [&](int q) { return bar0 + 8u * (kB + 4 + q); };              // a half's O += P V is done
-  auto qready_bar = [&](int q) { return bar0 + 8u * (kB + 4 + C::NQ + q); };     // a half's Q is in place
-  auto qfree_bar = [&](int q) { return bar0 + 8u * (kB + 4 + 2 * C::NQ + q); };  // its last scores are done
-  auto drain_bar = [&](int q) { return bar0 + 8u * (kB + 4 + 3 * C::NQ + q); };
+  // weights of the tile's first (h = 0) and second KT / 2 positions ready
+  auto pready_bar = [&](int b, int h) { return bar0 + 8u * (kB + 2 + 2 * h + b); };
+  auto odone_bar = [&](int q) { return bar0 + 8u * (kB + 6 + q); };              // a half's O += P V is done
+  auto qready_bar = [&](int q) { return bar0 + 8u * (kB + 6 + C::NQ + q); };     // a half's Q is in place
+  auto qfree_bar = [&](int q) { return bar0 + 8u * (kB + 6 + 2 * C::NQ + q); };  // its last scores are done
+  auto drain_bar = [&](int q) { return bar0 + 8u * (kB + 6 + 3 * C::NQ + q); };
+  auto turn_bar = [&](int q) { return bar0 + 8u * (kB + 6 + 4 * C::NQ + q); };   // half q's lane may issue
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -117,18 +118,21 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(sfull_bar(b), 1);
-      mbar_init(pready_bar(b), 4);
+      mbar_init(pready_bar(b, 0), 4);
+      mbar_init(pready_bar(b, 1), 4);
     }
     for (int q = 0; q < C::NQ; ++q) {
       mbar_init(odone_bar(q), 1);
       mbar_init(qready_bar(q), 1);
       mbar_init(qfree_bar(q), 1);
       mbar_init(drain_bar(q), 1);
+      mbar_init(turn_bar(q), 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_map(&p.kmap);
     tma_prefetch_map(&p.vmap);
+    tma_prefetch_map(&p.qmap);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -140,9 +144,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_launch_dependents();
-  make_plan<R, KT, C::kThreads>(p, scratch);
+  make_plan<KT, C::kThreads>(p, scratch);
   const Plan plan = scratch.plan;
-  Walker<R, KT> walk(p, plan);
+  Walker<KT> walk(p, plan);
   Span w;
   // (each warpgroup sets its registers at the head of its own branch: the compiler then
   // allocates that branch by the new count)
@@ -222,9 +226,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         attn_wait_drain(fbar(f % NS), (f / NS) & 1, p);
     }
   } else if (warp <= C::NQ) {
-    // ------------------------------------------------------------ MMA issuers, one lane per half
-    if (lane == 0) {
-      const int q = warp - 1;
+    // ------------------------------------------------------------ MMA issuers, one warp per half
+    // The whole warp walks the loop, converged, and one elected lane issues: the operands
+    // then stay in uniform registers (an MMA of 128 x 128 x 16 lasts 64 cycles, and issuing
+    // it from a diverged lane took longer).
+    {
+      const int q = __shfl_sync(0xffffffffu, warp - 1, 0);
       constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, 0, 1);
       // a negative scale negates Q as it is read (bit 13)
       const uint32_t idesc_s = idesc_bf16_f32(128, KT, 0, 0) | (p.scale_log2 < 0.0f ? 1u << 13 : 0u);
@@ -233,61 +240,99 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
       const uint64_t vdesc0 = smem_desc_sw128(ring, KT * 128u, 1024u);
       constexpr uint64_t kTileStep = C::kTile >> 4;
       const uint32_t o_tmem = tmem + C::kOCol0 + q * D;
+      auto commit = [&](uint32_t bar) { if (elect_one()) tc_commit(bar); };
+      auto arrive = [&](uint32_t bar) { if (elect_one()) mbar_arrive(bar); };
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, attn_wait(bar, parity, abort_flag, p)) != 0;
+      };
+      auto next_item = [&]() {          // the walk's values, as uniform ones
+        if (!__shfl_sync(0xffffffffu, static_cast<int>(walk.next(p, w)), 0)) return false;
+        w.ja = __shfl_sync(0xffffffffu, w.ja, 0);
+        w.jb = __shfl_sync(0xffffffffu, w.jb, 0);
+        return true;
+      };
       auto scores = [&](int st, int buf) {
         const uint32_t d = tmem + C::kSCol0 + buf * C::kSCols;
         const uint64_t b = kdesc0 + st * kTileStep;
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc_mma_bf16(d, qdesc + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, b + (k >> 2) * (KT * 128 >> 4) + (k & 3) * 2,
-                      idesc_s, k > 0 ? 1u : 0u);
+          for (int k = 0; k < D / 16; ++k)
+            tc_mma_bf16(d, qdesc + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, b + (k >> 2) * (KT * 128 >> 4) + (k & 3) * 2,
+                        idesc_s, k > 0 ? 1u : 0u);
+        }
       };
-      auto values = [&](int st, int buf, bool first) {
+      // O += P V, each half of the positions as soon as its weights are there
+      auto values = [&](int st, int buf, uint32_t phase, bool first) {
         const uint32_t a = tmem + C::kSCol0 + buf * C::kSCols;
         const uint64_t b = vdesc0 + st * kTileStep;
 #pragma unroll
-        for (int k = 0; k < KT / 16; ++k)
-          tc_mma_bf16_ts(o_tmem, a + 8 * k, b + k * (2048 >> 4), idesc_o, (k > 0 || !first) ? 1u : 0u);
+        for (int h = 0; h < 2; ++h) {
+          if (!wait(pready_bar(buf, h), phase)) return false;
+          tc_fence_after_sync();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = h * (KT / 32); k < (h + 1) * (KT / 32); ++k)
+              tc_mma_bf16_ts(o_tmem, a + 8 * k, b + k * (2048 >> 4), idesc_o, (k > 0 || !first) ? 1u : 0u);
+          }
+        }
+        return true;
       };
       int st = 0;                         // ring stage and its phase
       uint32_t ph = 0, qphase = 0, pphase = 0;
       auto step = [&](int& s, uint32_t& f) { if (++s == ST) { s = 0; f ^= 1u; } };
       bool ok = true;
       if constexpr (C::NQ == 2) {
-        // per tile: S, then O += P V; the other half's lane fills the tensor cores meanwhile
-        while (ok && walk.next(p, w)) {
-          const bool mine = q < halves_of<C>(p, w);
-          if (mine) {
-            ok = attn_wait(qready_bar(q), qphase, abort_flag, p);
-            qphase ^= 1u;
-          }
-          for (int j = w.ja; ok && j < w.jb; ++j) {
-            ok = attn_wait(full_bar(st), ph, abort_flag, p);
-            if (!ok) break;
+        // Turns: O += P V of a tile and the scores of the next go out together, half 0's and
+        // half 1's in alternation, so that one half's softmax always has the other half's
+        // MMAs to run beside (left to themselves the halves fall into step: both wait for
+        // the tensor cores, then both for the exponentials; 10% slower).
+        uint32_t tphase = q == 0 ? 1u : 0u;        // half 0 has the first turn
+        while (ok && next_item()) {
+          const int nq = __shfl_sync(0xffffffffu, halves_of<C>(p, w), 0);
+          const bool mine = q < nq, both = nq == 2;
+          auto take_turn = [&]() {
+            if (!both) return true;
+            const bool got = wait(turn_bar(q), tphase);
+            tphase ^= 1u;
+            return got;
+          };
+          auto issue_scores = [&](bool last) {
             if (mine) {
               tc_fence_after_sync();
               scores(st, q);
-              tc_commit(sfull_bar(q));
-              tc_commit(empty_bar(st));
-              if (j + 1 == w.jb) tc_commit(qfree_bar(q));
+              commit(sfull_bar(q));
+              commit(empty_bar(st));
+              if (last) commit(qfree_bar(q));
             } else {
-              mbar_arrive(empty_bar(st));     // every lane follows the ring's phases
+              arrive(empty_bar(st));          // every lane follows the ring's phases
             }
             step(st, ph);
-            ok = attn_wait(full_bar(st), ph, abort_flag, p);
-            if (ok && mine) {
-              ok = attn_wait(pready_bar(q), pphase, abort_flag, p);
-              pphase ^= 1u;
-            }
+          };
+          if (mine) {
+            ok = wait(qready_bar(q), qphase);
+            qphase ^= 1u;
+          }
+          if (ok) ok = wait(full_bar(st), ph) && take_turn();
+          if (!ok) break;
+          issue_scores(w.ja + 1 == w.jb);
+          if (both) arrive(turn_bar(q ^ 1));
+          for (int j = w.ja; j < w.jb; ++j) {
+            const int vst = st;
+            ok = wait(full_bar(vst), ph);
+            step(st, ph);
+            if (ok && j + 1 < w.jb) ok = wait(full_bar(st), ph);
+            if (ok) ok = take_turn();
+            if (ok && mine) ok = values(vst, q, pphase, j == w.ja);
             if (!ok) break;
             if (mine) {
-              tc_fence_after_sync();
-              values(st, q, j == w.ja);
-              tc_commit(odone_bar(q));
-              tc_commit(empty_bar(st));
+              pphase ^= 1u;
+              commit(odone_bar(q));
+              commit(empty_bar(vst));
             } else {
-              mbar_arrive(empty_bar(st));
+              arrive(empty_bar(vst));
             }
-            step(st, ph);
+            if (j + 1 < w.jb) issue_scores(j + 2 == w.jb);
+            if (both) arrive(turn_bar(q ^ 1));
           }
         }
       } else {
@@ -295,21 +340,21 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         uint32_t T = 0;                   // tiles so far: score buffer T & 1
         auto next_scores = [&](bool new_item, bool last) {
           if (new_item) {
-            if (!attn_wait(qready_bar(0), qphase, abort_flag, p)) return false;
+            if (!wait(qready_bar(0), qphase)) return false;
             qphase ^= 1u;
           }
-          if (!attn_wait(full_bar(st), ph, abort_flag, p)) return false;
+          if (!wait(full_bar(st), ph)) return false;
           tc_fence_after_sync();
           scores(st, T & 1u);
-          tc_commit(sfull_bar(T & 1u));
-          tc_commit(empty_bar(st));
-          if (last) tc_commit(qfree_bar(0));
+          commit(sfull_bar(T & 1u));
+          commit(empty_bar(st));
+          if (last) commit(qfree_bar(0));
           ++T;
           step(st, ph);
           return true;
         };
         // ring order: K of tile t + 1 stands after V of tile t, so V's stage is remembered
-        bool more = walk.next(p, w);
+        bool more = next_item();
         int j = more ? w.ja : 0;
         if (more) ok = next_scores(true, w.ja + 1 == w.jb);
         while (ok && more) {
@@ -318,7 +363,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           const uint32_t vph = ph, buf = (T - 1u) & 1u;
           step(st, ph);
           if (++j == w.jb) {
-            more = walk.next(p, w);
+            more = next_item();
             if (more) {
               j = w.ja;
               ok = next_scores(true, w.ja + 1 == w.jb);
@@ -326,53 +371,45 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           } else {
             ok = next_scores(false, j + 1 == w.jb);
           }
-          if (ok) ok = attn_wait(full_bar(vst), vph, abort_flag, p);
-          if (ok) ok = attn_wait(pready_bar(buf), (pphase >> buf) & 1u, abort_flag, p);
+          if (ok) ok = wait(full_bar(vst), vph);
+          if (ok) ok = values(vst, buf, (pphase >> buf) & 1u, first);
           if (!ok) break;
           pphase ^= 1u << buf;
-          tc_fence_after_sync();
-          values(vst, buf, first);
-          tc_commit(odone_bar(0));
-          tc_commit(empty_bar(vst));
+          commit(odone_bar(0));
+          commit(empty_bar(vst));
         }
       }
       if (!ok) {
-        tc_commit(drain_bar(q));
+        commit(drain_bar(q));
         attn_wait_drain(drain_bar(q), 0, p);
       }
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ Q loader
-    uint32_t used[2] = {0, 0};            // items of each half so far
-    bool ok = true;
-    while (ok && walk.next(p, w)) {
-      const int nq = halves_of<C>(p, w);
+    // One box of th tokens x hs heads for 64 features: the packed rows in order, K-major with
+    // the 128-byte swizzle.  Rows past the box, the sequence or the slice hold other data
+    // and are nobody's.
+    if (lane == 0) {
+      uint32_t used[2] = {0, 0};          // items of each half so far
+      bool ok = true;
+      while (ok && walk.next(p, w)) {
+        const int nq = halves_of<C>(p, w), kvh = w.slice / p.spg;
+        const int head = kvh * p.group + (w.slice - kvh * p.spg) * p.hs;
 #pragma unroll 1
-      for (int q = 0; q < nq; ++q) {
-        if (used[q] > 0) ok = attn_wait(qfree_bar(q), (used[q] - 1u) & 1u, abort_flag, p);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        ++used[q];
-        // rows to shared memory, K-major with the 128-byte swizzle; rows that are nobody's are 0
-        constexpr int kPieces = D / 8, kRows = 32 / kPieces > 0 ? 32 / kPieces : 1;
-#pragma unroll 1
-        for (int r0 = 0; r0 < 128; r0 += 32) {
-          int tok, head;
-          const bool own = row_owner(p, w.s, w.slice, static_cast<unsigned>(w.rt) * R + q * 128 + r0 + lane, tok, head);
-          const long long at = own ? static_cast<long long>(w.s.q0 + tok) * p.q.ts + head * p.q.hs : -1;
-#pragma unroll 4
-          for (int x = 0; x < 32; x += kRows) {
-            const int rr = x + lane / kPieces, e = lane % kPieces, r = r0 + rr;
-            const long long from = __shfl_sync(0xffffffffu, at, rr);
-            const uint32_t dst = sbase + q * C::kQBytes + r * 128 + (e >> 3) * (128 * 128) + (((e & 7) ^ (r & 7)) << 4);
-            cp_async_16(dst, p.q.x + (from < 0 ? 0 : from) + 8 * e, from < 0 ? 0u : 16u);
-          }
+        for (int q = 0; q < nq; ++q) {
+          if (used[q] > 0) ok = attn_wait(qfree_bar(q), (used[q] - 1u) & 1u, abort_flag, p);
+          if (!ok) break;
+          ++used[q];
+          mbar_arrive_expect_tx(qready_bar(q), static_cast<uint32_t>(p.th * p.hs * D * 2));
+#pragma unroll
+          for (int x = 0; x < C::kHalves; ++x)
+            tma_load_3d(sbase + q * C::kQBytes + x * (128 * 128), &p.qmap, qready_bar(q), 64 * x, head,
+                        w.s.q0 + w.rt * p.tt + q * p.th);
         }
-        cp_async_wait_all();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(qready_bar(q));
       }
+      if (!ok)                            // copies in flight land before the block ends
+        for (int q = 0; q < C::NQ; ++q)
+          if (used[q] > 0) attn_wait_drain(qready_bar(q), (used[q] - 1u) & 1u, p);
     }
   }
   } else if (warp < 4 + C::kSoftWarps) {
@@ -399,7 +436,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         continue;
       }
       int tok, head, lo, hi;
-      const bool own = row_owner(p, w.s, w.slice, static_cast<unsigned>(w.rt) * R + q * 128 + r, tok, head);
+      const bool own = row_owner(p, w.s, w.slice, w.rt, q, r, tok, head);
       if (own) row_range(p, w.s, tok, lo, hi); else lo = 0, hi = 0x7fffffff;
       const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
       float top = -INFINITY;
@@ -424,29 +461,43 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         }
         tc_fence_after_sync();
         const bool edge = k0 < lo_max || k0 + KT > hi_min;
-        // this row's scores, all at once: K scales, mask, maximum
-        float s[KT];
+        // the row's scores, read once and held in registers, 32 columns on their way while
+        // the 32 before are worked on
+        uint32_t v[KT / 32][32];
+        // scores of columns [x, x + 32): K scales, mask
+        auto finish = [&](uint32_t (&v)[32], int x) {
+          if (C::kRaw) {
 #pragma unroll
-        for (int x = 0; x < KT; x += 32) tmem_ld32(s_tmem + x, *reinterpret_cast<uint32_t(*)[32]>(&s[x]));
-        tmem_ld_wait();
-        if (C::kRaw) {
-#pragma unroll
-          for (int e = 0; e < KT; e += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(ks + e);
-            const float2 a = mul_f32x2(make_float2(s[e], s[e + 1]), make_float2(f.x, f.y));
-            const float2 b = mul_f32x2(make_float2(s[e + 2], s[e + 3]), make_float2(f.z, f.w));
-            s[e] = a.x, s[e + 1] = a.y, s[e + 2] = b.x, s[e + 3] = b.y;
+            for (int e = 0; e < 32; e += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(ks + x + e);
+              const float2 a = mul_f32x2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), make_float2(f.x, f.y));
+              const float2 b = mul_f32x2(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), make_float2(f.z, f.w));
+              v[e] = __float_as_uint(a.x), v[e + 1] = __float_as_uint(a.y);
+              v[e + 2] = __float_as_uint(b.x), v[e + 3] = __float_as_uint(b.y);
+            }
           }
-        }
-        if (edge) {
+          if (edge) {
+            const int key = k0 + x;
 #pragma unroll
-          for (int e = 0; e < KT; ++e) s[e] = k0 + e >= lo && k0 + e < hi ? s[e] : -INFINITY;
-        }
+            for (int e = 0; e < 32; ++e) v[e] = key + e >= lo && key + e < hi ? v[e] : 0xFF800000u;   // -inf
+          }
+        };
         float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto maxima = [&](const uint32_t (&v)[32]) {
 #pragma unroll
-        for (int e = 0; e < KT; e += 8) {
+          for (int e = 0; e < 32; e += 8) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) m[k] = fmaxf(fmaxf(m[k], s[e + 2 * k]), s[e + 2 * k + 1]);
+            for (int k = 0; k < 4; ++k)
+              m[k] = fmaxf(fmaxf(m[k], __uint_as_float(v[e + 2 * k])), __uint_as_float(v[e + 2 * k + 1]));
+          }
+        };
+        tmem_ld32(s_tmem, v[0]);
+#pragma unroll
+        for (int x = 0; x < KT / 32; ++x) {
+          tmem_ld_wait_for(v[x]);
+          if (x + 1 < KT / 32) tmem_ld32(s_tmem + 32 * (x + 1), v[x + 1]);
+          finish(v[x], 32 * x);
+          maxima(v[x]);
         }
         const float cand = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
         if (__any_sync(0xffffffffu, cand > top + kMaxSlack)) {
@@ -474,42 +525,39 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         const float ref = top == -INFINITY ? 0.0f : top;
         const float2 c2 = make_float2(c, c), ref2 = make_float2(-ref, -ref);
         float2 l[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-        for (int x = 0; x < KT; x += 32) {
+        auto weights = [&](const uint32_t (&v)[32], int x) {
           uint32_t u[16];
 #pragma unroll
-          for (int e = x; e < x + 32; e += 4) {
+          for (int e = 0; e < 32; e += 4) {
             float2 y[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              y[k] = fma_f32x2(make_float2(s[e + 2 * k], s[e + 2 * k + 1]), c2, ref2);
+              y[k] = fma_f32x2(make_float2(__uint_as_float(v[e + 2 * k]), __uint_as_float(v[e + 2 * k + 1])), c2, ref2);
               y[k].x = exp2_approx(y[k].x);
               y[k].y = exp2_approx(y[k].y);
               l[k] = add_f32x2(l[k], y[k]);
             }
             if (C::kRaw) {
-              const float4 f = *reinterpret_cast<const float4*>(vs + e);
+              const float4 f = *reinterpret_cast<const float4*>(vs + x + e);
               y[0] = mul_f32x2(y[0], make_float2(f.x, f.y));
               y[1] = mul_f32x2(y[1], make_float2(f.z, f.w));
               if (edge) {                 // a hidden position's scale may be anything
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                  if (s[e + 2 * k] == -INFINITY) y[k].x = 0.0f;
-                  if (s[e + 2 * k + 1] == -INFINITY) y[k].y = 0.0f;
+                  if (v[e + 2 * k] == 0xFF800000u) y[k].x = 0.0f;
+                  if (v[e + 2 * k + 1] == 0xFF800000u) y[k].y = 0.0f;
                 }
               }
             }
-            u[(e - x) / 2] = pack_bf16x2(y[0].x, y[0].y);
-            u[(e - x) / 2 + 1] = pack_bf16x2(y[1].x, y[1].y);
+            u[e / 2] = pack_bf16x2(y[0].x, y[0].y);
+            u[e / 2 + 1] = pack_bf16x2(y[1].x, y[1].y);
           }
           tmem_st16(s_tmem + x / 2, u);
-        }
-        l[0] = add_f32x2(l[0], l[1]);
-        sum = add_f32x2(sum, l[0]);
-        tmem_st_wait();
+        };
         if (!C::kRaw && k0 + KT > w.s.kv) {
           // rows of V past the sequence hold anything, and zero weights do not silence a
-          // NaN: they are cleared here (both halves' warps may, with the same zeros)
+          // NaN: they are cleared before the first weights are handed over (both halves'
+          // warps may, with the same zeros)
           ok = attn_wait(full_bar(vidx % ST), (vidx / ST) & 1u, abort_flag, p);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           const uint32_t vt = ring + (vidx % ST) * C::kTile;
@@ -518,9 +566,18 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
               st_shared_v4(vt + (e >> 3) * (KT * 128) + row * 128 + ((e & 7) << 4), make_uint4(0, 0, 0, 0));
           fence_proxy_async_smem();
         }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pready_bar(buf));
+        // half of a tile's weights are handed over while the other half is made
+#pragma unroll
+        for (int x = 0; x < KT / 32; ++x) {
+          weights(v[x], 32 * x);
+          if (x != KT / 64 - 1 && x != KT / 32 - 1) continue;
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pready_bar(buf, x == KT / 32 - 1 ? 1 : 0));
+        }
+        l[0] = add_f32x2(l[0], l[1]);
+        sum = add_f32x2(sum, l[0]);
         ++done;
       }
       T += n;
@@ -632,7 +689,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
   __syncthreads();
   if (threadIdx.x == 0) {
     JoinDesc d = {};
-    Walker<R, KT> again(p, plan);
+    Walker<KT> again(p, plan);
     while (again.next(p, w))
       if (w.starts && !w.ends) {
         d.parts = 1 + static_cast<int>((w.after + plan.quota - 1) / plan.quota);
@@ -669,9 +726,8 @@ static lora_status_t launch_many(AttnParams& p, cudaStream_t st) {
   }
   int grid = num_sms();
   grid = grid > kMaxManyCtas ? kMaxManyCtas : grid;
-  p.spg = static_cast<int>(ceil_div(p.group, C::R));
-  p.hs = static_cast<int>(ceil_div(p.group, p.spg));
-  p.slices = p.cache.heads * p.spg;
+  set_tiles(p, 128, C::NQ);
+  if (!encode_map_3d(&p.qmap, p.q.x, C::D, p.hq, p.M, p.q.hs, p.q.ts, 64, p.hs, p.th)) return LORA_ERR_CUDA;
   LGB_TRY(launch_counted(attn_many_kernel<C>, dim3(grid), dim3(C::kThreads), C::kSmem, LORA_KIND_ATTN, st, p));
   return launch_counted(join_kernel<C::D, C::R>, dim3(grid, 16), dim3(128), 0, LORA_KIND_ATTN, st, p);
 }

@@ -158,6 +158,8 @@ bool encode_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer
                 uint32_t box_inner, uint32_t box_outer, int swizzle_bytes = 128);
 bool encode_map_rows(CUtensorMap* m, const void* base, int elem_bytes, uint64_t rows, uint64_t row_elems,
                      uint32_t box_rows, uint32_t box_bytes);
+bool encode_map_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t d1, uint64_t d2, uint64_t ld1,
+                   uint64_t ld2, uint32_t box_inner, uint32_t box_d1, uint32_t box_d2);
 bool encode_map_planes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t d1, uint64_t d2, uint64_t ld,
                        uint32_t box_inner, uint32_t box_d1);
 lora_status_t launch_gemm(int variant, const TcParams& p, int kind, cudaStream_t st);

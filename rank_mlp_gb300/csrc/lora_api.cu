@@ -82,6 +82,22 @@ bool encode_map_rows(CUtensorMap* m, const void* base, int elem_bytes, uint64_t 
                        static_cast<int>(box_bytes));
 }
 
+// 3-D bf16 map {inner, d1, d2} with strides ld1, ld2 (elements) in boxes {box_inner,
+// box_d1, box_d2} of 128-byte rows (128-byte swizzle).
+bool encode_map_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t d1, uint64_t d2, uint64_t ld1,
+                   uint64_t ld2, uint32_t box_inner, uint32_t box_d1, uint32_t box_d2) {
+  bind_current_device();
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr || inner == 0 || d1 == 0 || d2 == 0) return false;
+  const cuuint64_t dims[3] = {inner, d1, d2};
+  const cuuint64_t strides[2] = {ld1 * 2, ld2 * 2};
+  const cuuint32_t box[3] = {box_inner, box_d1, box_d2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 3-D bf16 map {inner, d1, d2} with row stride ld (elements) and plane stride
 // ld * d1; box {box_inner, box_d1, 1}.
 bool encode_map_planes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t d1, uint64_t d2, uint64_t ld,

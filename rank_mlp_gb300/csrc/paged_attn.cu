@@ -49,6 +49,7 @@ extern "C" lora_status_t lora_paged_attention(int64_t M, int heads_q, const lora
   if (M > kMaxExtent / heads_q || batch->n_seqs > kMaxExtent || batch->max_pages > kMaxExtent / cache->page_size)
     return LORA_ERR_UNSUPPORTED;
   LGB_TRY(check_heads_in(q));
+  if ((M > 1 && q->token_stride == 0) || (heads_q > 1 && q->head_stride == 0)) return LORA_ERR_UNSUPPORTED;
   if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(batch->page_table, 4) || !aligned(batch->kv_len, 4) ||
       !aligned(batch->cu_q, 4))
     return LORA_ERR_ALIGNMENT;
@@ -56,7 +57,8 @@ extern "C" lora_status_t lora_paged_attention(int64_t M, int heads_q, const lora
   if (M == 0) return LORA_OK;
   AttnParams p;
   std::memset(static_cast<void*>(&p), 0, sizeof(p));
-  p.q = HeadsView{static_cast<const bf16*>(q->data), q->token_stride, q->head_stride};
+  // the stride of an extent of one is never taken; the tensor map wants one all the same
+  p.q = HeadsView{static_cast<const bf16*>(q->data), M > 1 ? q->token_stride : 8, heads_q > 1 ? q->head_stride : 8};
   p.hq = heads_q;
   p.group = heads_q / cache->heads;
   p.M = static_cast<int>(M);

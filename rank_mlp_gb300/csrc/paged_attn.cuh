@@ -3,9 +3,9 @@
 //
 // Work.  Query rows of one sequence that read the same cache head are packed, row = token *
 // hs + head of the slice (a slice is the hs query heads of a cache head that one tile
-// takes, all of them unless they outnumber a tile's rows), and cut into tiles of R rows.
-// An item is (sequence, slice, row tile); it has one unit for every KT positions that its
-// rows see (one where they see none).  The lengths are known on the device only, so every
+// takes, all of them unless they outnumber its rows), as many whole tokens as a tile's
+// rows hold.  An item is (sequence, slice, tile of tt tokens); it has one unit for every KT
+// positions that its rows see (one where they see none).  The lengths are known on the device only, so every
 // CTA counts all units itself and takes an equal, contiguous share of them: long and
 // short sequences, causal tiles and few-row batches fill the GPU alike.  An item that a
 // share boundary cuts leaves its parts' maxima, sums and unnormalised outputs in the
@@ -18,9 +18,11 @@ namespace lgb {
 
 struct AttnParams {
   CUtensorMap kmap, vmap;    // pages as rows [n_pages * heads * page_size] x head_dim
+  CUtensorMap qmap;          // many-row kernel: q as [tokens x heads x head_dim]
   HeadsView q;
   int hq, group;             // query heads; of them per cache head
   int hs, spg, slices;       // heads per slice, slices per cache head, slices in all
+  int th, tt;                // tokens of a row half (rows / hs), and of a tile
   int M;
   CacheArgs cache;
   const int* table;
@@ -63,17 +65,12 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b, bool report)
   return s;
 }
 
-// (packed rows are below 2^31: M * heads_q is)
-template <int R>
-__device__ __forceinline__ int row_tiles(const AttnParams& p, const Seq& s) {
-  return static_cast<int>((static_cast<unsigned>(s.n) * p.hs + R - 1) / R);
-}
+__device__ __forceinline__ int row_tiles(const AttnParams& p, const Seq& s) { return (s.n + p.tt - 1) / p.tt; }
 
 // Tiles [j0, j1) of KT positions that row tile rt sees any of; one empty tile if none.
-template <int R, int KT>
+template <int KT>
 __device__ __forceinline__ void item_tiles(const AttnParams& p, const Seq& s, int rt, int& j0, int& j1) {
-  const unsigned r0 = static_cast<unsigned>(rt) * R, hs = p.hs;
-  const int t0 = static_cast<int>(r0 / hs), t1 = min(s.n - 1, static_cast<int>((r0 + R - 1) / hs));
+  const int t0 = rt * p.tt, t1 = min(s.n, t0 + p.tt) - 1;
   const int off = s.kv - s.n;
   const int hi = p.causal ? max(0, min(s.kv, off + t1 + 1)) : s.kv;
   const int lo = p.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(off) + t0 - p.window + 1)) : 0;
@@ -88,13 +85,15 @@ __device__ __forceinline__ void row_range(const AttnParams& p, const Seq& s, int
   lo = p.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(pos) - p.window + 1)) : 0;
 }
 
-// Token and query head of packed row pr of a slice; false past the sequence or the slice.
-__device__ __forceinline__ bool row_owner(const AttnParams& p, const Seq& s, int slice, unsigned pr, int& tok, int& head) {
-  tok = static_cast<int>(pr / static_cast<unsigned>(p.hs));
-  const int g = static_cast<int>(pr) - tok * p.hs;
+// Token and query head of row r of tile rt's half q; false past the half's tokens, the
+// sequence or the slice.
+__device__ __forceinline__ bool row_owner(const AttnParams& p, const Seq& s, int slice, int rt, int q, int r, int& tok,
+                                          int& head) {
+  const int t = r / p.hs, g = r - t * p.hs;
   const int kvh = slice / p.spg, first = (slice - kvh * p.spg) * p.hs;
+  tok = rt * p.tt + q * p.th + t;
   head = kvh * p.group + first + g;
-  return tok < s.n && first + g < p.group;
+  return t < p.th && tok < s.n && first + g < p.group;
 }
 
 // A CTA's share, found by all NT threads together.
@@ -109,15 +108,15 @@ struct PlanScratch {
   Plan plan;
 };
 
-template <int R, int KT>
+template <int KT>
 __device__ __forceinline__ long long seq_cost(const AttnParams& p, const Seq& s, bool live) {
   // units of one slice; sequences of more than four row tiles are counted by the whole warp
-  const int nrt = live ? row_tiles<R>(p, s) : 0;
+  const int nrt = live ? row_tiles(p, s) : 0;
   long long c = 0;
   if (nrt <= 4)
     for (int rt = 0; rt < nrt; ++rt) {
       int j0, j1;
-      item_tiles<R, KT>(p, s, rt, j0, j1);
+      item_tiles<KT>(p, s, rt, j0, j1);
       c += j1 - j0;
     }
   unsigned many = __ballot_sync(0xffffffffu, nrt > 4);
@@ -133,7 +132,7 @@ __device__ __forceinline__ long long seq_cost(const AttnParams& p, const Seq& s,
     long long sum = 0;
     for (int rt = lane; rt < tiles; rt += 32) {
       int j0, j1;
-      item_tiles<R, KT>(p, o, rt, j0, j1);
+      item_tiles<KT>(p, o, rt, j0, j1);
       sum += j1 - j0;
     }
 #pragma unroll
@@ -166,7 +165,7 @@ __device__ __forceinline__ long long block_scan(long long v, PlanScratch<NT>& sh
   return before + inc - v;
 }
 
-template <int R, int KT, int NT>
+template <int KT, int NT>
 __device__ __forceinline__ void make_plan(const AttnParams& p, PlanScratch<NT>& sh) {
   const int tid = threadIdx.x;
   const bool one = p.n_seqs <= NT;
@@ -175,7 +174,7 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanScratch<NT>& 
     const bool live = b0 + tid < p.n_seqs;
     Seq s = {0, 0, 0};
     if (live) s = load_seq(p, b0 + tid, blockIdx.x == 0);
-    c = seq_cost<R, KT>(p, s, live) * p.slices;
+    c = seq_cost<KT>(p, s, live) * p.slices;
     long long total;
     first = block_scan<NT>(c, sh, total);
     all += total;
@@ -195,7 +194,7 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanScratch<NT>& 
       const bool live = b0 + tid < p.n_seqs;
       Seq s = {0, 0, 0};
       if (live) s = load_seq(p, b0 + tid, false);
-      c = seq_cost<R, KT>(p, s, live) * p.slices;
+      c = seq_cost<KT>(p, s, live) * p.slices;
       first = block_scan<NT>(c, sh, total);
     }
     if (u0 >= before + first && u0 < before + first + c) {
@@ -210,10 +209,10 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanScratch<NT>& 
     const Seq s = load_seq(p, sh.plan.b, false);
     const int slice = static_cast<int>(sh.base / sh.cost);
     long long rem = sh.base - slice * sh.cost;
-    const int tiles = row_tiles<R>(p, s);
+    const int tiles = row_tiles(p, s);
     for (int rt0 = 0; rt0 < tiles; rt0 += 32) {
       int j0 = 0, j1 = 0;
-      if (rt0 + tid < tiles) item_tiles<R, KT>(p, s, rt0 + tid, j0, j1);
+      if (rt0 + tid < tiles) item_tiles<KT>(p, s, rt0 + tid, j0, j1);
       long long inc = j1 - j0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -243,7 +242,7 @@ struct Span {
 };
 
 // Walks a CTA's share; every role walks it by itself.
-template <int R, int KT>
+template <int KT>
 struct Walker {
   long long left;
   int b, slice, rt, skip, tiles;
@@ -252,7 +251,7 @@ struct Walker {
       : left(plan.units), b(plan.b), slice(plan.slice), rt(plan.rt), skip(plan.skip) {
     if (left > 0) {
       s = load_seq(p, b, false);
-      tiles = row_tiles<R>(p, s);
+      tiles = row_tiles(p, s);
     }
   }
   __device__ __forceinline__ bool next(const AttnParams& p, Span& w) {
@@ -265,11 +264,11 @@ struct Walker {
           if (++b >= p.n_seqs) return false;
           s = load_seq(p, b, false);
         } while (s.n == 0);
-        tiles = row_tiles<R>(p, s);
+        tiles = row_tiles(p, s);
       }
     }
     int j0, j1;
-    item_tiles<R, KT>(p, s, rt, j0, j1);
+    item_tiles<KT>(p, s, rt, j0, j1);
     w.s = s;
     w.b = b;
     w.slice = slice;
@@ -338,7 +337,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnP
   const int col = threadIdx.x % kCols;
   for (int r = blockIdx.y * (128 / kCols) + threadIdx.x / kCols; r < R; r += gridDim.y * (128 / kCols)) {
     int tok, head;
-    if (!row_owner(p, s, d.slice, static_cast<unsigned>(d.rt) * R + r, tok, head)) continue;
+    if (!row_owner(p, s, d.slice, d.rt, R > 128 ? r >> 7 : 0, R > 128 ? r & 127 : r, tok, head)) continue;
     const float2* ml = p.part_ml + r;
     float top = -INFINITY;
 #pragma unroll 4
@@ -379,6 +378,15 @@ constexpr int kFewRows = 16;          // rows of the few-row kernel's tiles
 // The many-row kernel's tiles: one or two row halves of 128 (one at head_dim 256).
 lora_status_t launch_attn_many(AttnParams& p, int halves, int head_dim, int format, cudaStream_t st);
 lora_status_t launch_attn_few(AttnParams& p, int head_dim, int format, cudaStream_t st);
+
+// Slices and tiles of a call whose row halves hold `rows` rows.
+inline void set_tiles(AttnParams& p, int rows, int halves) {
+  p.spg = static_cast<int>(ceil_div(p.group, rows));
+  p.hs = static_cast<int>(ceil_div(p.group, p.spg));
+  p.slices = p.cache.heads * p.spg;
+  p.th = rows / p.hs;
+  p.tt = halves * p.th;
+}
 
 // The cache's pages as rows, in boxes of at most `tile` rows of one page.
 inline bool encode_pages(AttnParams& p, int row_elems, int elem_bytes, int box_bytes, int tile) {
