@@ -232,8 +232,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
               ldmatrix_x4(piece_addr<C>(kt, warp * 16 + 8 * g + (lane & 7), c + (lane >> 3)), b);
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                mma_m16n8k16_bf16(s[g], q[c + e], codes_to_bf16x2<FMT>(__byte_perm(b[e], 0, 0x4140)),
-                                  codes_to_bf16x2<FMT>(__byte_perm(b[e], 0, 0x4342)));
+                mma_m16n8k16_bf16(s[g], q[c + e], codes01_to_bf16x2<FMT>(b[e]), codes23_to_bf16x2<FMT>(b[e]));
             }
           }
         }
@@ -321,10 +320,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
             ldmatrix_x4_trans(piece_addr<C>(vt, warp * 16 + (lane & 15), c + (lane >> 4)), b);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              mma_m16n8k16_bf16(o[2 * (c + e)], a, codes_to_bf16x2<FMT>(b[2 * e]),
-                                codes_to_bf16x2<FMT>(b[2 * e + 1]));
-              mma_m16n8k16_bf16(o[2 * (c + e) + 1], a, codes_to_bf16x2<FMT>(b[2 * e] >> 8),
-                                codes_to_bf16x2<FMT>(b[2 * e + 1] >> 8));
+              mma_m16n8k16_bf16(o[2 * (c + e)], a, codes02_to_bf16x2<FMT>(b[2 * e]),
+                                codes02_to_bf16x2<FMT>(b[2 * e + 1]));
+              mma_m16n8k16_bf16(o[2 * (c + e) + 1], a, codes13_to_bf16x2<FMT>(b[2 * e]),
+                                codes13_to_bf16x2<FMT>(b[2 * e + 1]));
             }
           }
         }

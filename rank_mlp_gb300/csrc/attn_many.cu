@@ -35,8 +35,8 @@ struct ManyCfg {
   static constexpr int kQBytes = 128 * D * 2;                // one row half of Q
   static constexpr int kRawRow = D, kRawBox = D < 128 ? D : 128, kRawBoxes = D / kRawBox;
   static constexpr int kRawTile = kRaw ? KT * D : 0;
-  static constexpr int kRawStages = kRaw ? 3 : 0;
-  static constexpr int kStages = kRaw ? (D == 64 ? 6 : NQ == 1 && D == 128 ? 4 : 3) : (D == 64 ? 8 : 5);
+  static constexpr int kRawStages = !kRaw ? 0 : D == 128 && NQ == 2 ? 2 : 3;
+  static constexpr int kStages = kRaw ? (D == 64 ? 6 : NQ == 1 && D == 128 ? 4 : 3) : (D == 64 ? 8 : D == 128 ? 4 : 5);
   static constexpr int kScaleSlots = (kStages + 2) / 2;      // see the converting warps
   static constexpr int kConvWarps = kRaw ? 4 : 0;
   static constexpr int kSoftWarps = 4 * NQ;
@@ -53,9 +53,15 @@ struct ManyCfg {
   static constexpr int kOffRing = NQ * kQBytes;
   static constexpr int kOffRaw = kOffRing + kStages * kTile;
   static constexpr int kOffRawScales = kOffRaw + kRawStages * kRawTile;
-  static constexpr int kOffScales = kOffRawScales + (kRaw ? kRawStages * KT * 4 : 0);
-  static constexpr int kOffBars = kOffScales + (kRaw ? kScaleSlots * 2 * KT * 4 : 0);
-  static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 8 + 4 * NQ;
+  static constexpr int kOffScales = kOffRawScales + (kRaw ? kRawStages * 2 * KT * 4 : 0);
+  // Output staging: kOutCols bf16 (or half as many f32) columns of a warp's 32 rows.  At
+  // head_dim 256 bf16 tiles leave no room for it, and the fifth ring stage is worth more
+  // (mixed batch of 24: 141 us against 152 us with four stages and staged rows).
+  static constexpr bool kStaged = kRaw || D < 256;
+  static constexpr int kOutCols = kRaw && D >= 128 ? 32 : 64;
+  static constexpr int kOffOut = kOffScales + (kRaw ? kScaleSlots * 2 * KT * 4 : 0);
+  static constexpr int kOffBars = kOffOut + (kStaged ? kSoftWarps * 32 * kOutCols * 2 : 0);
+  static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 6 + 5 * NQ + (kRaw ? kScaleSlots : 0);
   static constexpr int kOffPlan = kOffBars + kNumBars * 8 + 8;
   static constexpr int kSmem = kOffPlan + static_cast<int>(sizeof(PlanScratch<kThreads>)) + 1024;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -104,6 +110,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
   auto qready_bar = [&](int q) { return bar0 + 8u * (kB + 6 + C::NQ + q); };     // a half's Q is in place
   auto qfree_bar = [&](int q) { return bar0 + 8u * (kB + 6 + 2 * C::NQ + q); };  // its last scores are done
   auto drain_bar = [&](int q) { return bar0 + 8u * (kB + 6 + 3 * C::NQ + q); };
+  auto scale_bar = [&](int s) { return bar0 + 8u * (kB + 6 + 5 * C::NQ + s); };  // a tile's scales are in slot s
   auto turn_bar = [&](int q) { return bar0 + 8u * (kB + 6 + 4 * C::NQ + q); };   // half q's lane may issue
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -116,6 +123,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
       mbar_init(rfull_bar(s), 1);
       mbar_init(rempty_bar(s), C::kConvWarps);
     }
+    if (C::kRaw)
+      for (int s = 0; s < C::kScaleSlots; ++s) mbar_init(scale_bar(s), C::kConvWarps);
     for (int b = 0; b < 2; ++b) {
       mbar_init(sfull_bar(b), 1);
       mbar_init(pready_bar(b, 0), 4);
@@ -201,7 +210,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             first = false;
             if (lane == 0) {
               if (live > 0)
-                mbar_arrive_expect_tx(fb, live * box_rows * (static_cast<uint32_t>(D * kEl) + (C::kRaw ? 4u : 0u)));
+                mbar_arrive_expect_tx(fb, live * box_rows * (static_cast<uint32_t>(D * kEl) + (C::kRaw && kv == 0 ? 8u : 0u)));
               else
                 mbar_arrive(fb);
             }
@@ -211,9 +220,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
 #pragma unroll
               for (int x = 0; x < kBoxes; ++x)
                 tma_load_2d(dst + x * (KT * kBox), kv ? &p.vmap : &p.kmap, fb, x * (kBox / kEl), static_cast<int>(src));
-              if (C::kRaw)
-                bulk_load(sbase + C::kOffRawScales + stage * (KT * 4) + r0 * 4, (kv ? p.cache.vs : p.cache.ks) + src,
-                          box_rows * 4, fb);
+              if (C::kRaw && kv == 0) {   // the K tile brings both tiles' scales
+                const uint32_t sc = sbase + C::kOffRawScales + stage * (2 * KT * 4) + r0 * 4;
+                bulk_load(sc, p.cache.ks + src, box_rows * 4, fb);
+                bulk_load(sc + KT * 4, p.cache.vs + src, box_rows * 4, fb);
+              }
             }
           }
           ++armed;
@@ -261,14 +272,16 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
                         idesc_s, k > 0 ? 1u : 0u);
         }
       };
-      // O += P V, each half of the positions as soon as its weights are there
+      // O += P V: all at once if the weights are there, else each half of the positions as
+      // soon as its weights are
       auto values = [&](int st, int buf, uint32_t phase, bool first) {
         const uint32_t a = tmem + C::kSCol0 + buf * C::kSCols;
         const uint64_t b = vdesc0 + st * kTileStep;
+        bool all = __all_sync(0xffffffffu, mbar_test_wait(pready_bar(buf, 1), phase));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!wait(pready_bar(buf, h), phase)) return false;
-          tc_fence_after_sync();
+          if (!all && !wait(pready_bar(buf, h), phase)) return false;
+          if (h == 0 || !all) tc_fence_after_sync();
           if (elect_one()) {
 #pragma unroll
             for (int k = h * (KT / 32); k < (h + 1) * (KT / 32); ++k)
@@ -296,43 +309,51 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             tphase ^= 1u;
             return got;
           };
-          auto issue_scores = [&](bool last) {
-            if (mine) {
-              tc_fence_after_sync();
-              scores(st, q);
-              commit(sfull_bar(q));
-              commit(empty_bar(st));
-              if (last) commit(qfree_bar(q));
-            } else {
-              arrive(empty_bar(st));          // every lane follows the ring's phases
-            }
-            step(st, ph);
-          };
           if (mine) {
             ok = wait(qready_bar(q), qphase);
             qphase ^= 1u;
           }
-          if (ok) ok = wait(full_bar(st), ph) && take_turn();
-          if (!ok) break;
-          issue_scores(w.ja + 1 == w.jb);
-          if (both) arrive(turn_bar(q ^ 1));
-          for (int j = w.ja; j < w.jb; ++j) {
+          // step j: O += P V of tile j - 1, then the scores of tile j
+          for (int j = w.ja; ok && j <= w.jb; ++j) {
+            const bool pv = j > w.ja, s = j < w.jb;
             const int vst = st;
-            ok = wait(full_bar(vst), ph);
-            step(st, ph);
-            if (ok && j + 1 < w.jb) ok = wait(full_bar(st), ph);
+            if (pv) {
+              ok = wait(full_bar(vst), ph);
+              step(st, ph);
+            }
+            if (ok && s) ok = wait(full_bar(st), ph);
             if (ok) ok = take_turn();
-            if (ok && mine) ok = values(vst, q, pphase, j == w.ja);
             if (!ok) break;
-            if (mine) {
+            if (!mine) {                           // every warp follows the ring's phases
+              if (pv) arrive(empty_bar(vst));
+              if (s) {
+                arrive(empty_bar(st));
+                step(st, ph);
+              }
+              continue;
+            }
+            if (pv) {
+              ok = values(vst, q, pphase, j == w.ja + 1);
+              if (!ok) break;
               pphase ^= 1u;
+            } else {
+              tc_fence_after_sync();
+            }
+            // the other half's warp wakes while these scores are issued
+            if (both) arrive(turn_bar(q ^ 1));
+            if (s) {
+              scores(st, q);
+              commit(sfull_bar(q));
+            }
+            if (pv) {
               commit(odone_bar(q));
               commit(empty_bar(vst));
-            } else {
-              arrive(empty_bar(vst));
             }
-            if (j + 1 < w.jb) issue_scores(j + 2 == w.jb);
-            if (both) arrive(turn_bar(q ^ 1));
+            if (s) {
+              commit(empty_bar(st));
+              if (j + 1 == w.jb) commit(qfree_bar(q));
+              step(st, ph);
+            }
           }
         }
       } else {
@@ -452,11 +473,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         sphase ^= 1u << buf;
         if (C::kRaw) {
-          // the tile's scales were written before its V tile was handed over (its stage is
-          // not reused before these weights are)
-          ok = attn_wait(full_bar(vidx % ST), (vidx / ST) & 1u, abort_flag, p);
+          const uint32_t sc = (vidx >> 1) % C::kScaleSlots;
+          ok = attn_wait(scale_bar(sc), ((vidx >> 1) / C::kScaleSlots) & 1u, abort_flag, p);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          ks = reinterpret_cast<const float*>(smem + C::kOffScales) + ((vidx >> 1) % C::kScaleSlots) * 2 * KT;
+          ks = reinterpret_cast<const float*>(smem + C::kOffScales) + sc * 2 * KT;
           vs = ks + KT;
         }
         tc_fence_after_sync();
@@ -591,27 +611,76 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
       const float all = sum.x + sum.y;
       const bool none = top == -INFINITY && all == 0.0f;
       const float inv = none ? 0.0f : 1.0f / all;
-      const long long orow = static_cast<long long>(w.s.q0 + tok) * p.hq + head;
+      const int orow = own ? (w.s.q0 + tok) * p.hq + head : -1;       // below 2^31
       const long long prow = slot * R + q * 128 + r;
+      if constexpr (C::kStaged) {
+        // Out through shared memory, a warp's own 32 rows at a time: a store instruction then
+        // writes whole lines of a few rows (a row per lane would touch 32 lines and keep the
+        // load/store unit busy four times as long).
+        const uint32_t buf = sbase + C::kOffOut + (warp - 4) * (32 * C::kOutCols * 2);
+        constexpr int kRowBytes = C::kOutCols * 2, kPieces = kRowBytes / 16;    // of the staging
+        auto piece = [&](int row, int e) { return buf + row * kRowBytes + ((e ^ (kPieces == 8 ? row & 7 : (row >> 1) & 3)) << 4); };
+        const int cols = whole ? C::kOutCols : C::kOutCols / 2;
+#pragma unroll 1
+        for (int x = 0; x < D; x += cols) {
+          uint32_t v[C::kOutCols];
+          __syncwarp();
+          if (C::kOutCols == 32 && !whole)            // 16 columns: never past the accumulator
+            tmem_ld16(o_tmem + x, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+          else
+            tmem_ld32(o_tmem + x, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+          if (C::kOutCols == 64 && whole) tmem_ld32(o_tmem + x + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[C::kOutCols - 32]));
+          tmem_ld_wait();
+          if (whole) {
 #pragma unroll
-      for (int x = 0; x < D; x += 64) {
-        uint32_t v[2][32];
-        __syncwarp();
-        tmem_ld32(o_tmem + x, v[0]);
-        tmem_ld32(o_tmem + x + 32, v[1]);
-        tmem_ld_wait();
-        if (!own) continue;
+            for (int e = 0; e < kPieces; ++e) {
+              uint32_t u[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+              for (int k = 0; k < 4; ++k)
+                u[k] = none ? 0u : pack_bf16x2(__uint_as_float(v[8 * e + 2 * k]) * inv, __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
+              st_shared_v4(piece(lane, e), make_uint4(u[0], u[1], u[2], u[3]));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < kPieces; ++e)
+              st_shared_v4(piece(lane, e), make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
+          }
+          __syncwarp();
+          uint4 u[kPieces];
+          int to[kPieces];
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            const int row = (i * 32 + lane) / kPieces;
+            to[i] = __shfl_sync(0xffffffffu, orow, row);
+            u[i] = ld_shared_v4(piece(row, lane % kPieces));
+          }
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            const int row = (i * 32 + lane) / kPieces, e = lane % kPieces;
+            if (to[i] < 0) continue;
+            if (whole)
+              *reinterpret_cast<uint4*>(p.out + static_cast<long long>(to[i]) * D + x + 8 * e) = u[i];
+            else
+              *reinterpret_cast<uint4*>(p.part_o + (slot * R + q * 128 + quarter * 32 + row) * D + x + 4 * e) = u[i];
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int x = 0; x < D; x += 32) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld32(o_tmem + x, v);
+          tmem_ld_wait();
+          if (!own) continue;
           if (whole) {
             uint32_t u[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              u[e] = none ? 0u : pack_bf16x2(__uint_as_float(v[h][2 * e]) * inv, __uint_as_float(v[h][2 * e + 1]) * inv);
-            store_row32_bf16(p.out + orow * D + x + 32 * h, u, 0, 32, out_v8);
+              u[e] = none ? 0u : pack_bf16x2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
+            store_row32_bf16(p.out + static_cast<long long>(orow) * D + x, u, 0, 32, out_v8);
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) st_global_v8(p.part_o + prow * D + x + 32 * h + e, v[h] + e);
+            for (int e = 0; e < 32; e += 8) st_global_v8(p.part_o + prow * D + x + e, v + e);
           }
         }
       }
@@ -629,6 +698,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
     if constexpr (C::kRaw) {
       if constexpr (C::kSplitRegs) regs_lower<C::kConvRegs>();
       const int cw = warp - 4 - C::kSoftWarps, tid = cw * 32 + lane;
+      constexpr int kStepRows = 8 * 4 / C::kHalves;       // rows between a warp's steps
+      const int half = cw % C::kHalves, x = lane & 3, r7 = (lane >> 3) ^ (((lane >> 2) & 1) * 5);
+      const int row = cw / C::kHalves * 8 + r7;
+      const uint32_t src_at = C::kRawBox == 128
+                                  ? (half >> 1) * (KT * 128) + row * 128 + ((((4 * half + x) & 7) ^ r7) << 4)
+                                  : row * 64 + ((x ^ ((row >> 1) & 3)) << 4);
+      const uint32_t dst_at0 = half * (KT * 128) + row * 128 + (((2 * x) ^ r7) << 4);
+      const uint32_t dst_at1 = half * (KT * 128) + row * 128 + (((2 * x + 1) ^ r7) << 4);
       uint32_t idx = 0;
       bool ok = true;
       while (ok && walk.next(p, w)) {
@@ -640,37 +717,33 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             if (ok) ok = attn_wait(empty_bar(st), ((idx / ST) & 1u) ^ 1u, abort_flag, p);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            // scales of K tile and V tile of position tile idx / 2: the slot was last read by
-            // the softmax of kScaleSlots tiles before, whose V tile has left the ring
-            if (tid < KT)
-              reinterpret_cast<float*>(smem + C::kOffScales)[((idx >> 1) % C::kScaleSlots * 2 + kv) * KT + tid] =
-                  reinterpret_cast<const float*>(smem + C::kOffRawScales)[rs * KT + tid];
-            const uint32_t src = sbase + C::kOffRaw + rs * C::kRawTile, dst = ring + st * C::kTile;
-            constexpr int kPieces = D / 16;          // 16-byte pieces of a raw row
-#pragma unroll 2
-            for (int e = tid; e < KT * kPieces; e += 128) {
-              const int row = e / kPieces, x = e % kPieces;
-              const uint32_t at = C::kRawBox == 128
-                                      ? src + (x >> 3) * (KT * 128) + row * 128 + (((x & 7) ^ (row & 7)) << 4)
-                                      : src + row * 64 + ((x ^ ((row >> 1) & 3)) << 4);
-              const uint4 v = ld_shared_v4(at);
-              uint4 y[2];
-              y[0] = make_uint4(codes_to_bf16x2<C::FMT>(__byte_perm(v.x, 0, 0x4140)),
-                                codes_to_bf16x2<C::FMT>(__byte_perm(v.x, 0, 0x4342)),
-                                codes_to_bf16x2<C::FMT>(__byte_perm(v.y, 0, 0x4140)),
-                                codes_to_bf16x2<C::FMT>(__byte_perm(v.y, 0, 0x4342)));
-              y[1] = make_uint4(codes_to_bf16x2<C::FMT>(__byte_perm(v.z, 0, 0x4140)),
-                                codes_to_bf16x2<C::FMT>(__byte_perm(v.z, 0, 0x4342)),
-                                codes_to_bf16x2<C::FMT>(__byte_perm(v.w, 0, 0x4140)),
-                                codes_to_bf16x2<C::FMT>(__byte_perm(v.w, 0, 0x4342)));
-              // the lanes of a row's second 64 features store their second piece first, so
-              // that eight lanes always fill all banks
-              const int odd = (x >> 2) & 1;
-              const uint32_t base = dst + (x >> 2) * (KT * 128) + row * 128;
+            // scales of position tile idx / 2, both tiles': the slot was last read by the
+            // softmax of kScaleSlots tiles before, whose V tile has left the ring
+            if (kv == 0) {
+              const uint32_t sc = (idx >> 1) % C::kScaleSlots;
+              for (int e = tid; e < 2 * KT; e += 128)
+                reinterpret_cast<float*>(smem + C::kOffScales)[sc * 2 * KT + e] =
+                    reinterpret_cast<const float*>(smem + C::kOffRawScales)[rs * 2 * KT + e];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(scale_bar(sc));
+            }
+            // four 16-byte pieces (64 codes) of eight rows a step; of eight lanes four take
+            // row r and four row r ^ 5, which keeps both the raw pieces they read and the
+            // (even or odd) bf16 pieces they write in eight different bank groups
+            const uint32_t src = sbase + C::kOffRaw + rs * C::kRawTile + src_at, dst = ring + st * C::kTile;
+            constexpr int kSteps = KT / 8 * C::kHalves / 4, kBatch = 4;
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int piece = 2 * (x & 3) + (h ^ odd);
-                st_shared_v4(base + ((piece ^ (row & 7)) << 4), (h ^ odd) ? y[1] : y[0]);
+            for (int k0 = 0; k0 < kSteps; k0 += kBatch) {
+              uint4 v[kBatch];
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) v[k] = ld_shared_v4(src + (k0 + k) * kStepRows * C::kRawBox);
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) {
+                const uint32_t to = dst + (k0 + k) * kStepRows * 128;
+                st_shared_v4(to + dst_at0, make_uint4(codes01_to_bf16x2<C::FMT>(v[k].x), codes23_to_bf16x2<C::FMT>(v[k].x),
+                                                      codes01_to_bf16x2<C::FMT>(v[k].y), codes23_to_bf16x2<C::FMT>(v[k].y)));
+                st_shared_v4(to + dst_at1, make_uint4(codes01_to_bf16x2<C::FMT>(v[k].z), codes23_to_bf16x2<C::FMT>(v[k].z),
+                                                      codes01_to_bf16x2<C::FMT>(v[k].w), codes23_to_bf16x2<C::FMT>(v[k].w)));
               }
             }
             fence_proxy_async_smem();

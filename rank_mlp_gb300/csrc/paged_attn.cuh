@@ -287,10 +287,10 @@ struct Walker {
 
 // Bounded wait (the GEMM kernels' rule: wall-clock limit, abort flag shared by the CTA).
 __device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, const AttnParams& p) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait_short(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_short(bar, parity)) return true;
     if (*abort_flag) return false;
     if (global_timer_ns() - t0 > p.timeout_ns) {
       *abort_flag = 1;
