@@ -3,11 +3,18 @@
 // bounds it; the products run on the warp-level matrix units (m16n8k16), whose 16 rows
 // these few rows fill, straight from the tiles in shared memory.
 //
-// A CTA: one producer warp fills a ring of K/V tiles of 64 positions by TMA (128- or
-// 64-byte swizzle, one box per page), four warps take 16 positions of each tile and keep
-// a running maximum, sum and output of their own in registers, merged when the item's
-// part ends.  8-bit codes become bf16 exactly in registers (both formats' values fit
-// bf16), the row scales multiply the scores and the weights in f32.
+// A CTA: one producer warp fills a ring of K/V tiles of 64 or 128 positions by TMA (128- or
+// 64-byte swizzle, one box per page), four warps take a quarter of each tile's positions
+// and keep a running maximum, sum and output of their own in registers, merged when the
+// item's part ends.
+//
+// 8-bit caches run in f16, which holds both formats' codes exactly and to which they turn
+// in fewer instructions than to bf16 (the conversions, not memory, set the pace).  A row of
+// Q is scaled by a power of two to f16's upper range (exact for features down to 2^-29 of
+// the row's largest).  A position's K scale multiplies its score in f32; its V scale joins
+// the weight as an exponent, 2^(s + log2 vs - m'), with a running maximum m' of its own, so
+// that the f16 weights stay at the top of their range whatever the scales are, while the
+// sum of the weights without it keeps the scores' maximum m.
 #include "paged_attn.cuh"
 #include "codes.cuh"
 
@@ -20,7 +27,8 @@ struct FewCfg {
   static constexpr int kRow = D * kEl;                        // bytes of a cached row
   static constexpr int kBox = kRow < 128 ? kRow : 128;        // bytes of a row that one box holds
   static constexpr int kBoxes = kRow / kBox;
-  static constexpr int kKT = 64;
+  static constexpr int kKT = D == 256 || (FMT == LORA_KV_BF16 && D == 128) ? 64 : 128;
+  static constexpr int kGroups = kKT / 64;                    // of 16 positions, per warp and tile
   static constexpr int kTile = kKT * kRow;
   static constexpr int kStage = 2 * kTile;
   // D = 256 needs the registers of a whole SM for 160 threads; otherwise two CTAs share one
@@ -38,14 +46,6 @@ struct FewCfg {
   static constexpr int kOffPlan = kOffBars + 2 * kStages * 8 + 16;
   static constexpr int kSmem = kOffPlan + static_cast<int>(sizeof(PlanScratch<kThreads>)) + 1024;
 };
-
-// Shared-memory address of 16-byte piece c of row r of a tile: boxes of kBox-byte rows, the
-// pieces of a row permuted as TMA's swizzle of that row width does.
-template <class C>
-__device__ __forceinline__ uint32_t piece_addr(uint32_t tile, int r, int c) {
-  if (C::kBox == 128) return tile + (c >> 3) * (C::kKT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-  return tile + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-}
 
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const __grid_constant__ AttnParams p) {
@@ -159,9 +159,24 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
   }
 
   // -------------------------------------------------------------- the four product warps
+  constexpr bool k8 = FMT != LORA_KV_BF16;
+  constexpr int NG = C::kGroups;
   const int t = lane & 3, r0 = lane >> 2;         // fragment column pair and row (rows r0, r0 + 8)
   float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
+  // Shared-memory offsets of this lane's ldmatrix rows in a tile (its warp's first rows).  A
+  // 16-byte piece is permuted within its row by the row's low bits (TMA's swizzle), so that
+  // piece x + 4 lies at an offset that differs in one bit, and other rows of the same lane
+  // at a constant distance.
+  const int first = warp * 16 * NG;
+  const uint32_t k_at = C::kBox == 128 ? (first + (lane & 7)) * 128 + (((lane >> 3) ^ (lane & 7)) << 4)
+                                       : (first + (lane & 7)) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+  const uint32_t v_at = C::kBox == 128 ? (first + (lane & 15)) * 128 + (((lane >> 4) ^ (lane & 7)) << 4)
+                                       : (first + (lane & 15)) * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4);
+  // a negative scale turns Q's signs; a scale of 0 becomes the smallest normal one (finite
+  // scores weigh the same, a hidden one stays -inf)
+  const float scale = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
+  const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
   bool ok = true;
   while (walk.next(p, w)) {
     int tok[2], head[2], lo[2], hi[2];
@@ -179,19 +194,39 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
     // Q fragments.  A step multiplies 16 features; which ones a fragment column stands for
     // is free as long as Q and K agree, so 8-bit K takes four neighbouring bytes a lane.
     uint32_t q[D / 16][4];
+    float c[2] = {scale, scale};
+    unsigned big[2] = {0, 0};
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const bf16* x = p.q.x + static_cast<long long>(w.s.q0 + tok[h]) * p.q.ts + head[h] * p.q.hs + 16 * s;
-        if (FMT == LORA_KV_BF16) {
+        if (!k8) {
           q[s][h] = own[h] ? __ldg(reinterpret_cast<const uint32_t*>(x + 2 * t)) : 0u;
           q[s][2 + h] = own[h] ? __ldg(reinterpret_cast<const uint32_t*>(x + 2 * t + 8)) : 0u;
         } else {
           const uint2 v = own[h] ? __ldg(reinterpret_cast<const uint2*>(x + 4 * t)) : make_uint2(0u, 0u);
           q[s][h] = v.x;
           q[s][2 + h] = v.y;
+          big[h] = max(max(big[h], max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu)), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu));
         }
+        q[s][h] ^= flip;
+        q[s][2 + h] ^= flip;
+      }
+    }
+    if (k8) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        big[h] = max(big[h], __shfl_xor_sync(0xffffffffu, big[h], 1));
+        big[h] = max(big[h], __shfl_xor_sync(0xffffffffu, big[h], 2));
+        // the row times 2^(14 - exponent of its largest), and the score scale without it
+        const float f = __uint_as_float(static_cast<unsigned>(min(254, 268 - static_cast<int>(big[h] >> 7))) << 23);
+        c[h] = scale / f;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+          for (int x = h; x < 4; x += 2)
+            q[s][x] = pack_f16x2(__uint_as_float(q[s][x] << 16) * f, __uint_as_float(q[s][x] & 0xFFFF0000u) * f);
       }
     }
     float o[D / 8][4];
@@ -200,6 +235,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
     float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};
+    float vtop[2] = {-INFINITY, -INFINITY};       // 8-bit: of the scores with log2 of the V scales
 
     for (int j = w.ja; j < w.jb; ++j) {
       if (ok) ok = attn_wait(full_bar(stage), phase, abort_flag, p);
@@ -207,123 +243,126 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
       // after an expired wait the warp walks on without data, so that the merge's barriers
       // below still meet
       if (ok) {
-        const int k0 = j * KT + warp * 16;
-        const uint32_t kt = sbase + stage * C::kStage, vt = kt + C::kTile;
-        const float* ks = reinterpret_cast<const float*>(smem + C::kOffScales + stage * C::kScales) + warp * 16;
+        const int k0 = j * KT + first;
+        const uint32_t ka = sbase + stage * C::kStage + k_at, va = sbase + stage * C::kStage + C::kTile + v_at;
+        const float* ks = reinterpret_cast<const float*>(smem + C::kOffScales + stage * C::kScales) + first;
         const float* vs = ks + KT;
-        float s[2][4] = {};                       // positions k0 + 8 g + 2 t + {0, 1}, rows r0 and r0 + 8
-        if (FMT == LORA_KV_BF16) {
+        float s[2 * NG][4];                       // positions k0 + 8 g + 2 t + {0, 1}, rows r0 and r0 + 8
 #pragma unroll
-          for (int c = 0; c < D / 16; c += 2) {
+        for (int g = 0; g < 2 * NG; ++g)
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              uint32_t b[4];
-              ldmatrix_x4(piece_addr<C>(kt, warp * 16 + 8 * g + (lane & 7), 2 * c + (lane >> 3)), b);
-              mma_m16n8k16_bf16(s[g], q[c], b[0], b[1]);
-              mma_m16n8k16_bf16(s[g], q[c + 1], b[2], b[3]);
-            }
-          }
-        } else {
+          for (int e = 0; e < 4; ++e) s[g][e] = 0.0f;
 #pragma unroll
-          for (int c = 0; c < D / 16; c += 4) {
+        for (int x = 0; x < C::kRow / 16; x += 4) {          // four 16-byte pieces of a row
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              uint32_t b[4];
-              ldmatrix_x4(piece_addr<C>(kt, warp * 16 + 8 * g + (lane & 7), c + (lane >> 3)), b);
+          for (int g = 0; g < 2 * NG; ++g) {
+            uint32_t b[4];
+            ldmatrix_x4((ka ^ ((x & 7) << 4)) + (x >> 3) * (KT * 128) + 8 * g * C::kBox, b);
+            if (!k8) {
+              mma_m16n8k16_bf16(s[g], q[x / 2], b[0], b[1]);
+              mma_m16n8k16_bf16(s[g], q[x / 2 + 1], b[2], b[3]);
+            } else {
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                mma_m16n8k16_bf16(s[g], q[c + e], codes01_to_bf16x2<FMT>(b[e]), codes23_to_bf16x2<FMT>(b[e]));
+                mma_m16n8k16_f16(s[g], q[k8 ? x + e : 0], codes01_to_f16x2<FMT>(b[e]), codes23_to_f16x2<FMT>(b[e]));
             }
           }
         }
-        const bool edge = k0 < lo_max || k0 + 16 > hi_min;
-        float tile_top[2] = {-INFINITY, -INFINITY};
+        const bool edge = k0 < lo_max || k0 + 16 * NG > hi_min;
+        float most[2] = {-INFINITY, -INFINITY}, vmost[2] = {-INFINITY, -INFINITY};
+        float2 lv[2 * NG];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float f0 = p.scale_log2, f1 = p.scale_log2;
-          if (FMT != LORA_KV_BF16) {
+        for (int g = 0; g < 2 * NG; ++g) {
+          if (k8) {
             const float2 sc = *reinterpret_cast<const float2*>(ks + 8 * g + 2 * t);
-            f0 *= sc.x;
-            f1 *= sc.y;
+            s[g][0] *= sc.x, s[g][1] *= sc.y, s[g][2] *= sc.x, s[g][3] *= sc.y;
+            const float2 v = *reinterpret_cast<const float2*>(vs + 8 * g + 2 * t);
+            lv[g] = make_float2(log2_approx(v.x), log2_approx(v.y));
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            s[g][e] *= (e & 1) ? f1 : f0;
             if (edge) {
               const int key = k0 + 8 * g + 2 * t + (e & 1);
               if (key < lo[e >> 1] || key >= hi[e >> 1]) s[g][e] = -INFINITY;
             }
-            tile_top[e >> 1] = fmaxf(tile_top[e >> 1], s[g][e]);
+            most[e >> 1] = fmaxf(most[e >> 1], s[g][e]);
+            if (k8) vmost[e >> 1] = fmaxf(vmost[e >> 1], fmaf(s[g][e], c[e >> 1], (e & 1) ? lv[g].y : lv[g].x));
           }
         }
+        bool rise = false;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          tile_top[h] = fmaxf(tile_top[h], __shfl_xor_sync(0xffffffffu, tile_top[h], 1));
-          tile_top[h] = fmaxf(tile_top[h], __shfl_xor_sync(0xffffffffu, tile_top[h], 2));
+          most[h] = fmaxf(most[h], __shfl_xor_sync(0xffffffffu, most[h], 1));
+          most[h] = fmaxf(most[h], __shfl_xor_sync(0xffffffffu, most[h], 2)) * c[h];
+          rise = rise || most[h] > top[h] + kMaxSlack;
+          if (k8) {
+            vmost[h] = fmaxf(vmost[h], __shfl_xor_sync(0xffffffffu, vmost[h], 1));
+            vmost[h] = fmaxf(vmost[h], __shfl_xor_sync(0xffffffffu, vmost[h], 2));
+            rise = rise || vmost[h] > vtop[h] + kMaxSlack;
+          }
         }
-        const bool rise = tile_top[0] > top[0] + kMaxSlack || tile_top[1] > top[1] + kMaxSlack;
         if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float next = fmaxf(top[h], tile_top[h]);
+            const float next = fmaxf(top[h], most[h]), vnext = fmaxf(vtop[h], vmost[h]);
             const float f = next == -INFINITY ? 1.0f : exp2_approx(top[h] - next);
+            const float fo = !k8 ? f : vnext == -INFINITY ? 1.0f : exp2_approx(vtop[h] - vnext);
             top[h] = next;
+            vtop[h] = vnext;
             sum[h] *= f;
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
+            for (int n = 0; n < D / 8; ++n) o[n][2 * h] *= fo, o[n][2 * h + 1] *= fo;
           }
         }
-        const float m0 = top[0] == -INFINITY ? 0.0f : top[0], m1 = top[1] == -INFINITY ? 0.0f : top[1];
-        uint32_t a[4];
+        const float m[2] = {top[0] == -INFINITY ? 0.0f : top[0], top[1] == -INFINITY ? 0.0f : top[1]};
+        const float vm[2] = {vtop[0] == -INFINITY ? 0.0f : vtop[0], vtop[1] == -INFINITY ? 0.0f : vtop[1]};
+        uint32_t a[NG][4];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < 2 * NG; ++g) {
           float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[e] = exp2_approx(s[g][e] - (e < 2 ? m0 : m1));
-            sum[e >> 1] += x[e];
-          }
-          if (FMT != LORA_KV_BF16) {
-            const float2 sc = *reinterpret_cast<const float2*>(vs + 8 * g + 2 * t);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float y = x[e] * ((e & 1) ? sc.y : sc.x);
-              x[e] = edge && s[g][e] == -INFINITY ? 0.0f : y;       // a hidden position's scale is not looked at
+            const int h = e >> 1;
+            x[e] = exp2_approx(fmaf(s[g][e], c[h], -m[h]));
+            sum[h] += x[e];
+            if (k8) {
+              x[e] = exp2_approx(fmaf(s[g][e], c[h], ((e & 1) ? lv[g].y : lv[g].x) - vm[h]));
+              if (edge && s[g][e] == -INFINITY) x[e] = 0.0f;        // a hidden position's scale is not looked at
             }
           }
-          a[2 * g] = pack_bf16x2(x[0], x[1]);
-          a[2 * g + 1] = pack_bf16x2(x[2], x[3]);
+          a[g >> 1][2 * (g & 1)] = k8 ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
+          a[g >> 1][2 * (g & 1) + 1] = k8 ? pack_f16x2(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
         }
-        if (FMT == LORA_KV_BF16) {
-          // rows of V past the sequence hold anything: zero weights do not silence a NaN
+        // rows of V past the sequence hold anything: zero weights do not silence a NaN
+        const bool past = k0 + 16 * NG > w.s.kv;
+#pragma unroll
+        for (int kg = 0; kg < NG; ++kg) {
           uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-          const bool past = k0 + 16 > w.s.kv;
           if (past) {
-            const int a0 = w.s.kv - k0 - 2 * t, a1 = a0 - 8;        // positions left from this lane's first
+            const int a0 = w.s.kv - k0 - 16 * kg - 2 * t, a1 = a0 - 8;      // positions left from this lane's first
             keep0 = a0 >= 2 ? 0xffffffffu : a0 == 1 ? 0x0000ffffu : 0u;
             keep1 = a1 >= 2 ? 0xffffffffu : a1 == 1 ? 0x0000ffffu : 0u;
           }
 #pragma unroll
-          for (int n = 0; n < D / 8; n += 2) {
+          for (int x = 0; x < C::kRow / 16; x += 2) {        // two 16-byte pieces of 16 rows
             uint32_t b[4];
-            ldmatrix_x4_trans(piece_addr<C>(vt, warp * 16 + (lane & 15), n + (lane >> 4)), b);
-            if (past) b[0] &= keep0, b[1] &= keep1, b[2] &= keep0, b[3] &= keep1;
-            mma_m16n8k16_bf16(o[n], a, b[0], b[1]);
-            mma_m16n8k16_bf16(o[n + 1], a, b[2], b[3]);
-          }
-        } else {
-          // a 16-bit element of the transposed tile is two features' codes: o[2c] holds
-          // features 16 c + 2 n, o[2c + 1] features 16 c + 2 n + 1
+            ldmatrix_x4_trans((va ^ ((x & 7) << 4)) + (x >> 3) * (KT * 128) + 16 * kg * C::kBox, b);
+            if (past) {
+              // (8-bit: a 16-bit element of the transposed tile is two features' codes)
+              b[0] &= keep0, b[1] &= keep1, b[2] &= keep0, b[3] &= keep1;
+            }
+            if (!k8) {
+              mma_m16n8k16_bf16(o[x], a[kg], b[0], b[1]);
+              mma_m16n8k16_bf16(o[x + 1], a[kg], b[2], b[3]);
+            } else {
+              // o[2 x] holds features 16 x + 2 n, o[2 x + 1] features 16 x + 2 n + 1
 #pragma unroll
-          for (int c = 0; c < D / 16; c += 2) {
-            uint32_t b[4];
-            ldmatrix_x4_trans(piece_addr<C>(vt, warp * 16 + (lane & 15), c + (lane >> 4)), b);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              mma_m16n8k16_bf16(o[2 * (c + e)], a, codes02_to_bf16x2<FMT>(b[2 * e]),
-                                codes02_to_bf16x2<FMT>(b[2 * e + 1]));
-              mma_m16n8k16_bf16(o[2 * (c + e) + 1], a, codes13_to_bf16x2<FMT>(b[2 * e]),
-                                codes13_to_bf16x2<FMT>(b[2 * e + 1]));
+              for (int e = 0; e < 2; ++e) {
+                mma_m16n8k16_f16(o[k8 ? 2 * (x + e) : 0], a[kg], codes02_to_f16x2<FMT>(b[2 * e]),
+                                 codes02_to_f16x2<FMT>(b[2 * e + 1]));
+                mma_m16n8k16_f16(o[k8 ? 2 * (x + e) + 1 : 0], a[kg], codes13_to_f16x2<FMT>(b[2 * e]),
+                                 codes13_to_f16x2<FMT>(b[2 * e + 1]));
+              }
             }
           }
         }
@@ -331,6 +370,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
         if (lane == 0) mbar_arrive(empty_bar(stage));
       }
       if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+    }
+    if (k8) {
+      // the outputs back to the scores' maximum
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float f = vtop[h] == -INFINITY ? 0.0f : exp2_approx(vtop[h] - top[h]);
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
+      }
     }
 
     // the four warps' parts: a common maximum, then the outputs one after the other

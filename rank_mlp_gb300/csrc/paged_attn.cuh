@@ -315,6 +315,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // A running maximum is raised only when a tile exceeds it by more than this (log2): until
 // then the weights are at most 2^8, which f32 sums and bf16 weights hold as exactly as
 // smaller ones, and the output accumulators need no rescaling.
