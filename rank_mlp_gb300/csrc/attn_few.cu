@@ -15,6 +15,8 @@
 // the weight as an exponent, 2^(s + log2 vs - m'), with a running maximum m' of its own, so
 // that the f16 weights stay at the top of their range whatever the scales are, while the
 // sum of the weights without it keeps the scores' maximum m.
+#include <type_traits>
+
 #include "paged_attn.cuh"
 #include "codes.cuh"
 
@@ -27,13 +29,14 @@ struct FewCfg {
   static constexpr int kRow = D * kEl;                        // bytes of a cached row
   static constexpr int kBox = kRow < 128 ? kRow : 128;        // bytes of a row that one box holds
   static constexpr int kBoxes = kRow / kBox;
-  static constexpr int kKT = D == 256 || (FMT == LORA_KV_BF16 && D == 128) ? 64 : 128;
+  static constexpr int kKT = 64;
+  static constexpr int kItem = 2;                             // an item's own cost, in tiles
   static constexpr int kGroups = kKT / 64;                    // of 16 positions, per warp and tile
   static constexpr int kTile = kKT * kRow;
   static constexpr int kStage = 2 * kTile;
   // D = 256 needs the registers of a whole SM for 160 threads; otherwise two CTAs share one
-  static constexpr int kCtas = D == 256 ? 1 : 2;
-  static constexpr int kStagesFit = (kCtas == 1 ? 192 * 1024 : 96 * 1024) / kStage;
+  static constexpr int kCtas = D == 256 ? 1 : D == 128 && FMT == LORA_KV_BF16 ? 2 : 3;
+  static constexpr int kStagesFit = (kCtas == 1 ? 192 * 1024 : kCtas == 2 ? 96 * 1024 : 62 * 1024) / kStage;
   static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
   static constexpr int kScales = FMT == LORA_KV_BF16 ? 0 : 2 * kKT * 4;    // bytes per stage
   static constexpr int kMergeLd = D + 4;
@@ -75,12 +78,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
-  make_plan<KT, C::kThreads>(p, scratch);
+  make_plan<KT, C::kItem, C::kThreads>(p, scratch);
   const Plan plan = scratch.plan;
   if (threadIdx.x == 0) p.join[blockIdx.x].parts = 0;     // set below by the item that starts here and goes on
   if (plan.units == 0) return;
 
-  Walker<KT> walk(p, plan);
+  Walker<KT, C::kItem> walk(p, plan);
   Span w;
   int stage = 0;
   uint32_t phase = 0;
@@ -244,6 +247,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
       // below still meet
       if (ok) {
         const int k0 = j * KT + first;
+        // compiled twice: for tiles that all rows see whole (nearly all), and for the others
+        auto tile = [&](auto at_edge) {
+        constexpr bool kEdge = decltype(at_edge)::value;
         const uint32_t ka = sbase + stage * C::kStage + k_at, va = sbase + stage * C::kStage + C::kTile + v_at;
         const float* ks = reinterpret_cast<const float*>(smem + C::kOffScales + stage * C::kScales) + first;
         const float* vs = ks + KT;
@@ -268,7 +274,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
             }
           }
         }
-        const bool edge = k0 < lo_max || k0 + 16 * NG > hi_min;
         float most[2] = {-INFINITY, -INFINITY}, vmost[2] = {-INFINITY, -INFINITY};
         float2 lv[2 * NG];
 #pragma unroll
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if (edge) {
+            if (kEdge) {
               const int key = k0 + 8 * g + 2 * t + (e & 1);
               if (key < lo[e >> 1] || key >= hi[e >> 1]) s[g][e] = -INFINITY;
             }
@@ -327,18 +332,17 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
             sum[h] += x[e];
             if (k8) {
               x[e] = exp2_approx(fmaf(s[g][e], c[h], ((e & 1) ? lv[g].y : lv[g].x) - vm[h]));
-              if (edge && s[g][e] == -INFINITY) x[e] = 0.0f;        // a hidden position's scale is not looked at
+              if (kEdge && s[g][e] == -INFINITY) x[e] = 0.0f;        // a hidden position's scale is not looked at
             }
           }
           a[g >> 1][2 * (g & 1)] = k8 ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
           a[g >> 1][2 * (g & 1) + 1] = k8 ? pack_f16x2(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
         }
         // rows of V past the sequence hold anything: zero weights do not silence a NaN
-        const bool past = k0 + 16 * NG > w.s.kv;
 #pragma unroll
         for (int kg = 0; kg < NG; ++kg) {
           uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-          if (past) {
+          if (kEdge) {
             const int a0 = w.s.kv - k0 - 16 * kg - 2 * t, a1 = a0 - 8;      // positions left from this lane's first
             keep0 = a0 >= 2 ? 0xffffffffu : a0 == 1 ? 0x0000ffffu : 0u;
             keep1 = a1 >= 2 ? 0xffffffffu : a1 == 1 ? 0x0000ffffu : 0u;
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
           for (int x = 0; x < C::kRow / 16; x += 2) {        // two 16-byte pieces of 16 rows
             uint32_t b[4];
             ldmatrix_x4_trans((va ^ ((x & 7) << 4)) + (x >> 3) * (KT * 128) + 16 * kg * C::kBox, b);
-            if (past) {
+            if (kEdge) {
               // (8-bit: a 16-bit element of the transposed tile is two features' codes)
               b[0] &= keep0, b[1] &= keep1, b[2] &= keep0, b[3] &= keep1;
             }
@@ -366,6 +370,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
             }
           }
         }
+        };
+        if (k0 >= lo_max && k0 + 16 * NG <= hi_min)
+          tile(std::false_type{});
+        else
+          tile(std::true_type{});
         __syncwarp();
         if (lane == 0) mbar_arrive(empty_bar(stage));
       }
@@ -381,94 +390,87 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
       }
     }
 
-    // the four warps' parts: a common maximum, then the outputs one after the other
+    // The four warps' parts, four rows at a time: each warp lays its outputs down as they
+    // are, and a thread joins four features of a row under the common maximum.  (Adding
+    // them up in turn, one warp after the other, took 13 thousand cycles an item.)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
       sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
       if (t == 0) ml[warp * R + r0 + 8 * h] = make_float2(top[h], sum[h]);
     }
-    named_barrier(1, 128);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float m = -INFINITY;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) m = fmaxf(m, ml[x * R + r0 + 8 * h].x);
-      const float f = exp2_approx(top[h] - (m == -INFINITY ? 0.0f : m));
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
-    }
-#pragma unroll 1
-    for (int x = 0; x < 4; ++x) {
-      if (warp == x) {
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float2* cell = reinterpret_cast<float2*>(merge + (r0 + 8 * h) * C::kMergeLd + 8 * n + 2 * t);
-            float2 v = make_float2(o[n][2 * h], o[n][2 * h + 1]);
-            if (!own[h]) continue;
-            if (x > 0) {
-              const float2 b = *cell;
-              v.x += b.x;
-              v.y += b.y;
-            }
-            *cell = v;
-          }
-      }
-      named_barrier(1, 128);
-    }
-    // merged rows out: feature order in `merge` is the fragments' (see above)
     const bool whole = w.starts && w.ends;
     const int slot = 2 * blockIdx.x + (w.starts ? 1 : 0);
-    if (ok) {
-      constexpr int kLanes = D / 4;                 // threads of a row, four features each
-      for (int r = threadIdx.x / kLanes; r < R; r += 128 / kLanes) {
+    const int used = p.th * p.hs;                 // rows of the tile
+#pragma unroll 1
+    for (int pass = 0; 4 * pass < used; ++pass) {
+      if ((r0 >> 2) == (pass & 1)) {
+        float* line = merge + (4 * warp + (r0 & 3)) * C::kMergeLd + 2 * t;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+          *reinterpret_cast<float2*>(line + 8 * n) = pass < 2 ? make_float2(o[n][0], o[n][1]) : make_float2(o[n][2], o[n][3]);
+      }
+      named_barrier(1, 128);
+#pragma unroll
+      for (int i0 = 0; i0 < D; i0 += 128) {
+        const int i = i0 + threadIdx.x, r = 4 * pass + i / (D / 4), f = i % (D / 4) * 4;
         int tk, hd;
-        if (!row_owner(p, w.s, w.slice, w.rt, 0, r, tk, hd)) continue;
-        const int f = (threadIdx.x % kLanes) * 4;
-        float4 v;
-        if (FMT == LORA_KV_BF16) {
-          v = *reinterpret_cast<const float4*>(merge + r * C::kMergeLd + f);
-        } else {
-          // features 16 c + 4 t + {0, 1, 2, 3} are columns 2 t, 2 t + 1 of o[2c] and of o[2c + 1]
-          const int c = f / 16, tt = (f % 16) / 4;
-          const float2 even = *reinterpret_cast<const float2*>(merge + r * C::kMergeLd + 16 * c + 2 * tt);
-          const float2 odd = *reinterpret_cast<const float2*>(merge + r * C::kMergeLd + 16 * c + 8 + 2 * tt);
-          v = make_float4(even.x, odd.x, even.y, odd.y);
+        if (!ok || i >= D || !row_owner(p, w.s, w.slice, w.rt, 0, r, tk, hd)) continue;
+        float2 v[4];
+        float m = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          v[x] = ml[x * R + r];
+          m = fmaxf(m, v[x].x);
         }
-        float m = -INFINITY, l = 0.0f;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) m = fmaxf(m, ml[x * R + r].x);
         const float ref = m == -INFINITY ? 0.0f : m;
+        float l = 0.0f;
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) l += ml[x * R + r].y * exp2_approx(ml[x * R + r].x - ref);
+        for (int x = 0; x < 4; ++x) {
+          const float* line = merge + (4 * x + (r & 3)) * C::kMergeLd;
+          float4 u;
+          if (!k8) {
+            u = *reinterpret_cast<const float4*>(line + f);
+          } else {
+            // features 16 c + 4 t + {0, 1, 2, 3} are columns 2 t, 2 t + 1 of o[2c] and of o[2c + 1]
+            const float2 even = *reinterpret_cast<const float2*>(line + f / 16 * 16 + f % 16 / 2);
+            const float2 odd = *reinterpret_cast<const float2*>(line + f / 16 * 16 + 8 + f % 16 / 2);
+            u = make_float4(even.x, odd.x, even.y, odd.y);
+          }
+          const float g = exp2_approx(v[x].x - ref);
+          l += g * v[x].y;
+          y.x += g * u.x;
+          y.y += g * u.y;
+          y.z += g * u.z;
+          y.w += g * u.w;
+        }
         if (whole) {
           const bool none = m == -INFINITY && l == 0.0f;
           const float inv = none ? 0.0f : 1.0f / l;
           const long long row = static_cast<long long>(w.s.q0 + tk) * p.hq + hd;
           uint2 u;
-          u.x = pack_bf16x2(v.x * inv, v.y * inv);
-          u.y = pack_bf16x2(v.z * inv, v.w * inv);
+          u.x = pack_bf16x2(y.x * inv, y.y * inv);
+          u.y = pack_bf16x2(y.z * inv, y.w * inv);
           *reinterpret_cast<uint2*>(p.out + row * D + f) = u;
           if (p.lse != nullptr && f == 0) p.lse[row] = none ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
         } else {
-          *reinterpret_cast<float4*>(p.part_o + (static_cast<long long>(slot) * R + r) * D + f) = v;
+          *reinterpret_cast<float4*>(p.part_o + (static_cast<long long>(slot) * R + r) * D + f) = y;
           if (f == 0) p.part_ml[static_cast<long long>(slot) * R + r] = make_float2(m, l);
         }
       }
-      if (threadIdx.x == 0 && w.starts && !w.ends) {
-        JoinDesc d;
-        d.parts = 1 + static_cast<int>((w.after + plan.quota - 1) / plan.quota);
-        d.q0 = w.s.q0;
-        d.n = w.s.n;
-        d.kv = w.s.kv;
-        d.slice = w.slice;
-        d.rt = w.rt;
-        p.join[blockIdx.x] = d;
-      }
+      named_barrier(1, 128);            // `merge` is free again (after the last pass `ml` too)
     }
-    named_barrier(1, 128);            // `merge` and `ml` are free again
+    if (ok && threadIdx.x == 0 && w.starts && !w.ends) {
+      JoinDesc d;
+      d.parts = 1 + static_cast<int>((w.after + plan.quota - 1) / plan.quota);
+      d.q0 = w.s.q0;
+      d.n = w.s.n;
+      d.kv = w.s.kv;
+      d.slice = w.slice;
+      d.rt = w.rt;
+      p.join[blockIdx.x] = d;
+    }
   }
 }
 

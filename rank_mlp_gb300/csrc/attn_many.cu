@@ -30,6 +30,7 @@ struct ManyCfg {
   static constexpr bool kRaw = FMT != LORA_KV_BF16;
   static constexpr int R = 128 * NQ;
   static constexpr int KT = D == 256 ? 64 : 128;
+  static constexpr int kItem = 2;                            // an item's own cost, in tiles
   static constexpr int kHalves = D / 64;                     // 128-byte columns of a bf16 row
   static constexpr int kTile = KT * D * 2;                   // one bf16 K or V tile
   static constexpr int kQBytes = 128 * D * 2;                // one row half of Q
@@ -153,9 +154,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_launch_dependents();
-  make_plan<KT, C::kThreads>(p, scratch);
+  make_plan<KT, C::kItem, C::kThreads>(p, scratch);
   const Plan plan = scratch.plan;
-  Walker<KT> walk(p, plan);
+  Walker<KT, C::kItem> walk(p, plan);
   Span w;
   // (each warpgroup sets its registers at the head of its own branch: the compiler then
   // allocates that branch by the new count)
@@ -762,7 +763,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
   __syncthreads();
   if (threadIdx.x == 0) {
     JoinDesc d = {};
-    Walker<KT> again(p, plan);
+    Walker<KT, C::kItem> again(p, plan);
     while (again.next(p, w))
       if (w.starts && !w.ends) {
         d.parts = 1 + static_cast<int>((w.after + plan.quota - 1) / plan.quota);

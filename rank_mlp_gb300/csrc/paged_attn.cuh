@@ -5,7 +5,8 @@
 // hs + head of the slice (a slice is the hs query heads of a cache head that one tile
 // takes, all of them unless they outnumber its rows), as many whole tokens as a tile's
 // rows hold.  An item is (sequence, slice, tile of tt tokens); it has one unit for every KT
-// positions that its rows see (one where they see none).  The lengths are known on the device only, so every
+// positions that its rows see (one where they see none) and IT units before them, for what
+// an item costs beside its tiles (Q, merging, the output).  The lengths are known on the device only, so every
 // CTA counts all units itself and takes an equal, contiguous share of them: long and
 // short sequences, causal tiles and few-row batches fill the GPU alike.  An item that a
 // share boundary cuts leaves its parts' maxima, sums and unnormalised outputs in the
@@ -100,6 +101,7 @@ __device__ __forceinline__ bool row_owner(const AttnParams& p, const Seq& s, int
 struct Plan {
   long long units, quota;    // of this CTA; of a full share
   int b, slice, rt, skip;    // where it starts: the item, and the units of it that precede
+  Seq s;                     // that item's sequence
 };
 template <int NT>
 struct PlanScratch {
@@ -108,7 +110,7 @@ struct PlanScratch {
   Plan plan;
 };
 
-template <int KT>
+template <int KT, int IT>
 __device__ __forceinline__ long long seq_cost(const AttnParams& p, const Seq& s, bool live) {
   // units of one slice; sequences of more than four row tiles are counted by the whole warp
   const int nrt = live ? row_tiles(p, s) : 0;
@@ -117,7 +119,7 @@ __device__ __forceinline__ long long seq_cost(const AttnParams& p, const Seq& s,
     for (int rt = 0; rt < nrt; ++rt) {
       int j0, j1;
       item_tiles<KT>(p, s, rt, j0, j1);
-      c += j1 - j0;
+      c += j1 - j0 + IT;
     }
   unsigned many = __ballot_sync(0xffffffffu, nrt > 4);
   const int lane = threadIdx.x & 31;
@@ -133,7 +135,7 @@ __device__ __forceinline__ long long seq_cost(const AttnParams& p, const Seq& s,
     for (int rt = lane; rt < tiles; rt += 32) {
       int j0, j1;
       item_tiles<KT>(p, o, rt, j0, j1);
-      sum += j1 - j0;
+      sum += j1 - j0 + IT;
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -165,21 +167,23 @@ __device__ __forceinline__ long long block_scan(long long v, PlanScratch<NT>& sh
   return before + inc - v;
 }
 
-template <int KT, int NT>
+template <int KT, int IT, int NT>
 __device__ __forceinline__ void make_plan(const AttnParams& p, PlanScratch<NT>& sh) {
   const int tid = threadIdx.x;
   const bool one = p.n_seqs <= NT;
-  long long all = 0, c = 0, first = 0;
+  long long all = 0, c = 0, cost1 = 0, first = 0;
+  Seq s = {0, 0, 0};
   for (int b0 = 0; b0 < p.n_seqs; b0 += NT) {
     const bool live = b0 + tid < p.n_seqs;
-    Seq s = {0, 0, 0};
     if (live) s = load_seq(p, b0 + tid, blockIdx.x == 0);
-    c = seq_cost<KT>(p, s, live) * p.slices;
+    cost1 = seq_cost<KT, IT>(p, s, live);
+    c = cost1 * p.slices;
     long long total;
     first = block_scan<NT>(c, sh, total);
     all += total;
   }
-  const long long quota = max((all + gridDim.x - 1) / gridDim.x, 1ll);
+  const long long up = all + gridDim.x - 1;
+  const long long quota = max(up <= 0x7fffffff ? static_cast<long long>(static_cast<unsigned>(up) / gridDim.x) : up / gridDim.x, 1ll);
   const long long u0 = quota * blockIdx.x;
   if (tid == 0) {
     sh.plan.quota = quota;
@@ -192,37 +196,43 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanScratch<NT>& 
     long long total = 0;
     if (!one) {
       const bool live = b0 + tid < p.n_seqs;
-      Seq s = {0, 0, 0};
       if (live) s = load_seq(p, b0 + tid, false);
-      c = seq_cost<KT>(p, s, live) * p.slices;
+      cost1 = seq_cost<KT, IT>(p, s, live);
+      c = cost1 * p.slices;
       first = block_scan<NT>(c, sh, total);
     }
-    if (u0 >= before + first && u0 < before + first + c) {
+    if (u0 >= before + first && u0 < before + first + c) {     // (c is the slices' units together)
       sh.plan.b = b0 + tid;
+      sh.plan.s = s;
       sh.base = u0 - before - first;
-      sh.cost = c / p.slices;
+      sh.cost = cost1;
     }
     before += total;
   }
   __syncthreads();
   if (tid < 32) {
-    const Seq s = load_seq(p, sh.plan.b, false);
-    const int slice = static_cast<int>(sh.base / sh.cost);
-    long long rem = sh.base - slice * sh.cost;
+    // 32-bit division where it fits (a 64-bit one takes several times as long)
+    s = sh.plan.s;
+    const long long base = sh.base, cost = sh.cost;
+    const int slice = base <= 0x7fffffff && cost <= 0x7fffffff
+                          ? static_cast<int>(static_cast<unsigned>(base) / static_cast<unsigned>(cost))
+                          : static_cast<int>(base / cost);
+    long long rem = base - slice * cost;
     const int tiles = row_tiles(p, s);
     for (int rt0 = 0; rt0 < tiles; rt0 += 32) {
-      int j0 = 0, j1 = 0;
+      int j0 = 0, j1 = -IT;
       if (rt0 + tid < tiles) item_tiles<KT>(p, s, rt0 + tid, j0, j1);
-      long long inc = j1 - j0;
+      const int units = j1 - j0 + IT;
+      long long inc = units;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const long long o = __shfl_up_sync(0xffffffffu, inc, d);
         if (tid >= d) inc += o;
       }
-      if (rem < inc && rem >= inc - (j1 - j0)) {
+      if (rem < inc && rem >= inc - units) {
         sh.plan.slice = slice;
         sh.plan.rt = rt0 + tid;
-        sh.plan.skip = static_cast<int>(rem - (inc - (j1 - j0)));
+        sh.plan.skip = static_cast<int>(rem - (inc - units));
       }
       const long long window = __shfl_sync(0xffffffffu, inc, 31);
       if (rem < window) break;
@@ -242,46 +252,48 @@ struct Span {
 };
 
 // Walks a CTA's share; every role walks it by itself.
-template <int KT>
+template <int KT, int IT>
 struct Walker {
   long long left;
-  int b, slice, rt, skip, tiles;
+  int b, slice, rt, skip;
   Seq s;
+  int tiles;
   __device__ __forceinline__ Walker(const AttnParams& p, const Plan& plan)
-      : left(plan.units), b(plan.b), slice(plan.slice), rt(plan.rt), skip(plan.skip) {
-    if (left > 0) {
-      s = load_seq(p, b, false);
-      tiles = row_tiles(p, s);
-    }
+      : left(plan.units), b(plan.b), slice(plan.slice), rt(plan.rt), skip(plan.skip), s(plan.s) {
+    tiles = left > 0 ? row_tiles(p, s) : 0;
   }
   __device__ __forceinline__ bool next(const AttnParams& p, Span& w) {
-    if (left <= 0) return false;
-    if (rt == tiles) {
-      rt = 0;
-      if (++slice == p.slices) {
-        slice = 0;
-        do {
-          if (++b >= p.n_seqs) return false;
-          s = load_seq(p, b, false);
-        } while (s.n == 0);
-        tiles = row_tiles(p, s);
+    while (left > 0) {
+      if (rt == tiles) {
+        rt = 0;
+        if (++slice == p.slices) {
+          slice = 0;
+          do {
+            if (++b >= p.n_seqs) return false;
+            s = load_seq(p, b, false);
+          } while (s.n == 0);
+          tiles = row_tiles(p, s);
+        }
       }
+      int j0, j1;
+      item_tiles<KT>(p, s, rt, j0, j1);
+      // units [skip, till) of the item's IT + (j1 - j0)
+      const int units = IT + j1 - j0, till = static_cast<int>(min(static_cast<long long>(units), skip + left));
+      left -= till - skip;
+      w.ja = j0 + max(0, skip - IT);
+      w.jb = j0 + max(0, till - IT);
+      w.s = s;
+      w.b = b;
+      w.slice = slice;
+      w.rt = rt;
+      w.starts = w.ja == j0;
+      w.ends = w.jb == j1;
+      w.after = units - till;
+      skip = 0;
+      ++rt;
+      if (w.ja < w.jb) return true;       // else the share ended in the item's first units
     }
-    int j0, j1;
-    item_tiles<KT>(p, s, rt, j0, j1);
-    w.s = s;
-    w.b = b;
-    w.slice = slice;
-    w.rt = rt;
-    w.ja = j0 + skip;
-    w.jb = static_cast<int>(min(static_cast<long long>(j1), w.ja + left));
-    w.starts = skip == 0;
-    w.ends = w.jb == j1;
-    w.after = j1 - w.jb;
-    left -= w.jb - w.ja;
-    skip = 0;
-    ++rt;
-    return true;
+    return false;
   }
 };
 
@@ -377,7 +389,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnP
 // ---------------------------------------------------------------- launches
 
 // Most CTAs of a launch, whatever the device: the parts' slots are sized for it.
-constexpr int kMaxFewCtas = 320;
+constexpr int kMaxFewCtas = 480;
 constexpr int kMaxManyCtas = 160;
 
 constexpr int kFewRows = 16;          // rows of the few-row kernel's tiles
