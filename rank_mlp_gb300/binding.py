@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -490,41 +491,71 @@ def qkvo_backward(x, q, k, v, o_in, o, s, saved, dyq=None, dyk=None, dyv=None, d
 # q, k and v can be slices of one buffer.  The structures handed to the library live
 # until the call returns; the library copies what it needs.
 
-def _heads(t, name) -> LoraHeads:
+# A call of a few microseconds on the GPU is bounded by this code, so it checks each tensor
+# once, asks for the stream once, and packs the small structures as bytes (a ctypes
+# Structure takes four times as long to fill).
+
+_BF16 = torch.bfloat16
+_PACK_HEADS = struct.Struct("=Q3q").pack         # lora_heads_t
+_PACK_ROTARY = struct.Struct("=3Qq2i").pack      # lora_rotary_t
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda idx: torch.cuda.current_stream(idx).cuda_stream)
+
+
+def _bad_heads(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name} must be a bf16 CUDA tensor [tokens, heads, head_dim] with feature stride 1 "
-                         f"(got {t.dtype}, {t.device}, {tuple(t.shape)}, strides {t.stride()})")
+    raise ValueError(f"{name} must be a bf16 CUDA tensor [tokens, heads, head_dim] with feature stride 1 "
+                     f"(got {t.dtype}, {t.device}, {tuple(t.shape)}, strides {t.stride()})")
+
+
+def _heads(t, name):
+    """t as a lora_heads_t (bytes)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or not t.is_cuda or t.dim() != 3:
+        _bad_heads(t, name)
     n, heads, dim = t.shape
-    ts, hs, _ = t.stride()
+    ts, hs, one = t.stride()
+    if one != 1 and dim > 1:
+        _bad_heads(t, name)
     # the stride of an extent of one says nothing; a whole row satisfies every rule
-    return LoraHeads(t.data_ptr(), heads, ts if n > 1 else heads * dim, hs if heads > 1 else dim)
+    return _PACK_HEADS(t.data_ptr(), heads, ts if n > 1 else heads * dim, hs if heads > 1 else dim)
 
 
 def _ints(t, dtype, shape, name) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {shape} (got {t.dtype}, "
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)} (got {t.dtype}, "
                          f"{t.device}, {tuple(t.shape)})")
     return t.data_ptr()
 
 
-def _rotary(rope, tokens) -> LoraRotary:
-    """dict(cos, sin, pos[, layout]): f32 tables [n_pos, rot_dim/2] and int32 positions
+def _rotary(rope, tokens) -> bytes:
+    """A lora_rotary_t of dict(cos, sin, pos[, layout]): f32 tables [n_pos, rot_dim/2] and int32 positions
     [tokens] on the device; layout "half" (default) or "interleaved"."""
-    cos, sin = rope["cos"], rope["sin"]
-    if cos.dim() != 2:
+    cos = rope["cos"]
+    shape = cos.shape
+    if len(shape) != 2:
         raise ValueError("rope tables must be [n_pos, rot_dim/2]")
-    shape = tuple(cos.shape)
-    return LoraRotary(_ints(cos, torch.float32, shape, "rope cos"), _ints(sin, torch.float32, shape, "rope sin"),
-                      _ints(rope["pos"], torch.int32, (tokens,), "rope pos"), shape[0], 2 * shape[1],
-                      LAYOUT[rope.get("layout", "half")])
+    return _PACK_ROTARY(_ints(cos, torch.float32, shape, "rope cos"),
+                        _ints(rope["sin"], torch.float32, shape, "rope sin"),
+                        _ints(rope["pos"], torch.int32, (tokens,), "rope pos"), shape[0], 2 * shape[1],
+                        LAYOUT[rope.get("layout", "half")])
 
 
-def _at(struct):
-    return None if struct is None else ctypes.addressof(struct)
+def _call(t, nbytes, ws):
+    """(stream, workspace address, its bytes) of a call on t's device; ws as the caller's, or
+    the current stream's cached one."""
+    idx = t.get_device()
+    stream = _RAW_STREAM(idx)
+    if ws is None:
+        ws = _WS.get((idx, stream))
+        if ws is None or ws.numel() < nbytes:
+            ws = workspace(nbytes, t.device)
+    return stream, ws.data_ptr(), ws.numel()
+
+
+_at = ctypes.addressof
 
 
 def rope_table_scaled(n_pos: int, rot_dim: int, base: float = 10000.0, scaling: dict | None = None, device="cuda"):
@@ -552,22 +583,30 @@ def rotary(q, k=None, *, rope, inverse=False, q_out=None, k_out=None, ws=None):
     the rotated q, or (q, k).  rope: dict(cos, sin, pos[, layout]) with tables
     [n_pos, rot_dim/2]; features from rot_dim on pass through.  inverse turns back (the
     gradient).  q_out and k_out may be q and k themselves."""
-    lib = load()
-    tokens, _, dim = q.shape
-    st_q, rot = _heads(q, "q"), _rotary(rope, tokens)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    st_yq, st_k, st_yk = _heads(q_out, "q_out"), None, None
-    if q_out.shape != q.shape:
+    lib = _LIB or load()
+    shape = q.shape
+    view = _heads(q, "q")
+    tokens, dim = shape[0], shape[2]
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=_BF16, device=q.device)
+    elif q_out.shape != shape:
         raise ValueError("q_out must have q's shape")
-    if k is not None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-        if k.shape[0] != tokens or k.shape[2] != dim or k_out.shape != k.shape:
-            raise ValueError("k must have q's tokens and head_dim, and k_out k's shape")
-        st_k, st_yk = _heads(k, "k"), _heads(k_out, "k_out")
-    ws = workspace(256, q.device) if ws is None else ws
-    _check(lib.lora_rotary(tokens, dim, _at(st_q), _at(st_yq), _at(st_k), _at(st_yk), _at(rot), int(inverse),
-                           ws.data_ptr(), ws.numel(), _stream(q.device)), "lora_rotary")
-    return q_out if k is None else (q_out, k_out)
+    rot = _rotary(rope, tokens)
+    stream, wp, wn = _call(q, 256, ws)
+    if k is None:
+        _check(lib.lora_rotary(tokens, dim, view, _heads(q_out, "q_out"), None, None, rot, int(inverse), wp, wn, stream),
+               "lora_rotary")
+        return q_out
+    kshape = k.shape
+    if kshape[0] != tokens or kshape[2] != dim:
+        raise ValueError("k must have q's tokens and head_dim")
+    if k_out is None:
+        k_out = torch.empty(kshape, dtype=_BF16, device=q.device)
+    elif k_out.shape != kshape:
+        raise ValueError("k_out must have k's shape")
+    _check(lib.lora_rotary(tokens, dim, view, _heads(q_out, "q_out"), _heads(k, "k"), _heads(k_out, "k_out"), rot,
+                           int(inverse), wp, wn, stream), "lora_rotary")
+    return q_out, k_out
 
 
 class KVCache:
@@ -589,6 +628,7 @@ class KVCache:
         self.n_pages, self.heads, self.page_size, self.head_dim = shape
         self._struct = LoraKvCache(_ints(k, k.dtype, shape, "k"), _ints(v, k.dtype, shape, "v"), sc[0], sc[1],
                                    shape[0], shape[2], shape[1], shape[3], KV_FORMAT[k.dtype])
+        self._at = _at(self._struct)
 
 
 def kv_cache(n_pages: int, page_size: int, heads: int, head_dim: int, format: str = "bf16", device="cuda") -> KVCache:
@@ -604,42 +644,47 @@ def kv_append(cache: KVCache, k, v, slots, *, q=None, rope=None, q_out=None, ws=
     """Writes k and v (views [tokens, heads, head_dim]) to the cache's slots (int64
     [tokens]; negative: skipped).  With rope, k is rotated first, and q in the same launch:
     returns the rotated q (q_out, which may be q), or None without q."""
-    lib = load()
-    tokens = k.shape[0]
-    for t, n in ((k, "k"), (v, "v")):
-        if tuple(t.shape) != (tokens, cache.heads, cache.head_dim):
-            raise ValueError(f"{n} must be [tokens, {cache.heads}, {cache.head_dim}]")
-    st_k, st_v, st_q, st_yq = _heads(k, "k"), _heads(v, "v"), None, None
+    lib = _LIB or load()
+    shape = k.shape
+    view = _heads(k, "k")
+    tokens, dim = shape[0], cache.head_dim
+    if shape[1] != cache.heads or shape[2] != dim or v.shape != shape:
+        raise ValueError(f"k and v must be [tokens, {cache.heads}, {dim}]")
+    slot_at = _ints(slots, torch.int64, (tokens,), "slots")
     rot = None if rope is None else _rotary(rope, tokens)
-    if q is not None:
-        if rope is None:
-            raise ValueError("q is passed to be rotated: rope is missing")
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        if q.shape[0] != tokens or q.shape[2] != cache.head_dim or q_out.shape != q.shape:
-            raise ValueError("q must have k's tokens and head_dim, and q_out q's shape")
-        st_q, st_yq = _heads(q, "q"), _heads(q_out, "q_out")
-    ws = workspace(256, k.device) if ws is None else ws
-    _check(lib.lora_kv_append(tokens, _at(cache._struct), _at(st_k), _at(st_v),
-                              _ints(slots, torch.int64, (tokens,), "slots"), _at(st_q), _at(st_yq), _at(rot),
-                              ws.data_ptr(), ws.numel(), _stream(k.device)), "lora_kv_append")
-    return q_out if q is not None else None
+    stream, wp, wn = _call(k, 256, ws)
+    if q is None:
+        _check(lib.lora_kv_append(tokens, cache._at, view, _heads(v, "v"), slot_at, None, None, rot, wp, wn, stream),
+               "lora_kv_append")
+        return None
+    if rot is None:
+        raise ValueError("q is passed to be rotated: rope is missing")
+    qshape = q.shape
+    if qshape[0] != tokens or qshape[2] != dim:
+        raise ValueError("q must have k's tokens and head_dim")
+    if q_out is None:
+        q_out = torch.empty(qshape, dtype=_BF16, device=q.device)
+    elif q_out.shape != qshape:
+        raise ValueError("q_out must have q's shape")
+    _check(lib.lora_kv_append(tokens, cache._at, view, _heads(v, "v"), slot_at, _heads(q, "q"), _heads(q_out, "q_out"),
+                              rot, wp, wn, stream), "lora_kv_append")
+    return q_out
 
 
 def kv_read(cache: KVCache, page_table, cu_kv, total: int, *, ws=None):
     """(k, v), bf16 [total, heads, head_dim]: the sequences' cached rows one after the
     other, sequence b's at rows [cu_kv[b], cu_kv[b+1]).  page_table int32 [n_seqs,
     max_pages], cu_kv int32 [n_seqs + 1], both on the device."""
-    lib = load()
+    lib = _LIB or load()
     if page_table.dim() != 2:
         raise ValueError("page_table must be [n_seqs, max_pages]")
     n, width = page_table.shape
-    dev = cache.k.device
-    k = torch.empty(total, cache.heads, cache.head_dim, dtype=torch.bfloat16, device=dev)
-    v = torch.empty_like(k)
-    ws = workspace(256, dev) if ws is None else ws
-    _check(lib.lora_kv_read(n, total, _at(cache._struct), _ints(page_table, torch.int32, (n, width), "page_table"),
-                            width, _ints(cu_kv, torch.int32, (n + 1,), "cu_kv"), k.data_ptr(), v.data_ptr(),
-                            ws.data_ptr(), ws.numel(), _stream(dev)), "lora_kv_read")
+    shape, dev = (total, cache.heads, cache.head_dim), cache.k.device
+    k, v = torch.empty(shape, dtype=_BF16, device=dev), torch.empty(shape, dtype=_BF16, device=dev)
+    stream, wp, wn = _call(cache.k, 256, ws)
+    _check(lib.lora_kv_read(n, total, cache._at, _ints(page_table, torch.int32, (n, width), "page_table"), width,
+                            _ints(cu_kv, torch.int32, (n + 1,), "cu_kv"), k.data_ptr(), v.data_ptr(), wp, wn, stream),
+           "lora_kv_read")
     return k, v
 
 
@@ -657,6 +702,7 @@ class PagedBatch:
         self._struct = LoraPagedBatch(n, _ints(page_table, torch.int32, (n, width), "page_table"), width,
                                       _ints(kv_len, torch.int32, (n,), "kv_len"),
                                       _ints(cu_q, torch.int32, (n + 1,), "cu_q"))
+        self._at, self.n_seqs = _at(self._struct), n
 
 
 def paged_batch(page_table, kv_len, cu_q) -> PagedBatch:
@@ -669,19 +715,22 @@ def paged_attention(q, cache: KVCache, batch: PagedBatch, *, scale=None, causal=
     positions that each sees: out, bf16 [tokens, heads_q, head_dim].  scale defaults to
     head_dim ** -0.5; causal and window as in lora_paged_attention.  lse: None, or an f32
     [tokens, heads_q] tensor that receives the logarithm of each sum."""
-    lib = load()
-    tokens, hq, dim = q.shape
+    lib = _LIB or load()
+    shape = q.shape
+    view = _heads(q, "q")
+    tokens, hq, dim = shape
     if dim != cache.head_dim:
         raise ValueError(f"q must have the cache's head_dim {cache.head_dim}")
-    st_q = _heads(q, "q")
-    out = torch.empty(tokens, hq, dim, dtype=torch.bfloat16, device=q.device) if out is None else out
-    if out.shape != q.shape:
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
+        out_at = out.data_ptr()
+    elif out.shape != shape:
         raise ValueError("out must have q's shape")
-    at_cache, st_b = _at(cache._struct), batch._struct
-    need = lib.lora_paged_attention_workspace_bytes(tokens, st_b.n_seqs, hq, at_cache)
-    ws = workspace(need, q.device) if ws is None else ws
-    _check(lib.lora_paged_attention(
-        tokens, hq, _at(st_q), at_cache, _at(st_b), dim ** -0.5 if scale is None else scale, int(causal), window,
-        _dev(out, "out"), None if lse is None else _ints(lse, torch.float32, (tokens, hq), "lse"), ws.data_ptr(),
-        ws.numel(), _stream(q.device)), "lora_paged_attention")
+    else:
+        out_at = _dev(out, "out")
+    lse_at = None if lse is None else _ints(lse, torch.float32, (tokens, hq), "lse")
+    need = lib.lora_paged_attention_workspace_bytes(tokens, batch.n_seqs, hq, cache._at)
+    stream, wp, wn = _call(q, need, ws)
+    _check(lib.lora_paged_attention(tokens, hq, view, cache._at, batch._at, dim ** -0.5 if scale is None else scale,
+                                    int(causal), window, out_at, lse_at, wp, wn, stream), "lora_paged_attention")
     return out

@@ -25,24 +25,19 @@ struct AppendParams {
 };
 
 // The lane's cos and sin by feature, with the sign that the second product takes:
-// y = x cos + partner * ssn.  Lanes past rot_dim pass their features through.
+// y = x cos + partner * ssn.  Features that do not turn have a cleared bit in `turned`.
 struct LaneTurn {
   float c[8], s[8];
-  bool turned[8];
-  int partner;               // half layout, whole pieces: features from this one to its partner's
+  unsigned turned;
 };
 
-// VEC: rot_dim is a multiple of 16, a lane's 8 features have one partner piece.
+// VEC: rot_dim is a multiple of 16, a lane's 8 features turn together or not at all.
 template <bool VEC>
-__device__ __forceinline__ void load_turn(const AppendParams& p, long long m, int f0, LaneTurn& t) {
+__device__ __forceinline__ void load_turn(const AppendParams& p, int at, int f0, LaneTurn& t) {
   const int half = p.rot.half;
-  if (f0 >= 2 * half) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) t.turned[e] = false, t.c[e] = 1.0f, t.s[e] = 0.0f;
-    t.partner = 0;
-    return;
-  }
-  const long long tab = static_cast<long long>(rotary_position(p.rot, m, p.status)) * half;
+  t.turned = 0;
+  if (f0 >= 2 * half) return;
+  const long long tab = static_cast<long long>(checked_position(p.rot, at, p.status)) * half;
   const float* cos = p.rot.cos + tab;
   const float* sin = p.rot.sin + tab;
   if (VEC && !p.interleaved) {
@@ -50,53 +45,53 @@ __device__ __forceinline__ void load_turn(const AppendParams& p, long long m, in
     load8f(cos + (second ? f0 - half : f0), t.c);
     load8f(sin + (second ? f0 - half : f0), t.s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      t.turned[e] = true;
+    for (int e = 0; e < 8; ++e)
       if (!second) t.s[e] = -t.s[e];
-    }
-    t.partner = second ? -half : half;
+    t.turned = 0xFFu;
     return;
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int f = f0 + e;
-    t.turned[e] = f < 2 * half;
-    if (t.turned[e]) {
-      const int col = p.interleaved ? f / 2 : (f < half ? f : f - half);
-      const bool second = p.interleaved ? (f & 1) : f >= half;
-      t.c[e] = __ldg(cos + col);
-      t.s[e] = second ? __ldg(sin + col) : -__ldg(sin + col);
-    } else {
-      t.c[e] = 1.0f;
-      t.s[e] = 0.0f;
-    }
+    if (f >= 2 * half) continue;
+    const int col = p.interleaved ? f / 2 : (f < half ? f : f - half);
+    const bool second = p.interleaved ? (f & 1) : f >= half;
+    t.c[e] = __ldg(cos + col);
+    t.s[e] = second ? __ldg(sin + col) : -__ldg(sin + col);
+    t.turned |= 1u << e;
   }
-  t.partner = 0;
 }
 
-// The lane's 8 features [f0, f0 + 8) of row x, rotated in f32 (not rounded).
+// The lane's 8 features [f0, f0 + 8) of row x (own: as loaded) rotated in f32, not rounded.
+// Whole warps call it: in the half layout a lane's partners come from another lane of the
+// row, `from`.
 template <bool VEC>
-__device__ __forceinline__ void load_row(const AppendParams& p, const bf16* x, int f0, const LaneTurn& t, bool rotate,
-                                         float (&y)[8]) {
-  unpack8(*reinterpret_cast<const uint4*>(x + f0), y);
-  if (!rotate) return;
+__device__ __forceinline__ void turn_piece(const AppendParams& p, uint4 own, const bf16* x, int f0, int from,
+                                           const LaneTurn& t, bool rotate, float (&y)[8]) {
+  unpack8(own, y);
   float o[8];
   if (p.interleaved) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = y[e ^ 1];
   } else if (VEC) {
-    unpack8(*reinterpret_cast<const uint4*>(x + f0 + t.partner), o);
-  } else {
+    uint4 w;
+    w.x = __shfl_sync(0xffffffffu, own.x, from);
+    w.y = __shfl_sync(0xffffffffu, own.y, from);
+    w.z = __shfl_sync(0xffffffffu, own.z, from);
+    w.w = __shfl_sync(0xffffffffu, own.w, from);
+    unpack8(w, o);
+  } else if (rotate) {
     const int half = p.rot.half;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int f = f0 + e;
-      o[e] = t.turned[e] ? __bfloat162float(x[f < half ? f + half : f - half]) : 0.0f;
+      o[e] = (t.turned >> e) & 1u ? __bfloat162float(x[f < half ? f + half : f - half]) : 0.0f;
     }
   }
+  if (!rotate) return;
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    if (t.turned[e]) y[e] = __fadd_rn(__fmul_rn(y[e], t.c[e]), __fmul_rn(o[e], t.s[e]));
+    if ((t.turned >> e) & 1u) y[e] = __fadd_rn(__fmul_rn(y[e], t.c[e]), __fmul_rn(o[e], t.s[e]));
 }
 
 template <int FMT>
@@ -127,7 +122,7 @@ struct Quant<LORA_KV_INT8> {
 };
 
 template <int D, int FMT, bool VEC>
-__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(256, 3) append_kernel(const __grid_constant__ AppendParams p) {
   pdl_wait();
   pdl_launch_dependents();
   constexpr int L = D / 8;                       // lanes of a row
@@ -142,32 +137,44 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
     const long long m = live ? static_cast<long long>(u / static_cast<unsigned>(p.groups)) : 0;
     const int g = live ? static_cast<int>(u - static_cast<unsigned long long>(m) * p.groups) : 0;
     const int h0 = g * p.per_group, h1 = live ? min(h0 + p.per_group, heads) : h0;
-    LaneTurn t;
-    if (p.rotate && live && (h0 < p.hk || h1 > 2 * p.hk)) {
-      load_turn<VEC>(p, m, f0, t);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) t.turned[e] = false, t.c[e] = 1.0f, t.s[e] = 0.0f;
-      t.partner = 0;
-    }
+    // slot and position, the first heads' pieces, then the table entries, which wait for the
+    // position: the loads' latencies overlap
+    const bool turns = p.rotate && live && (h0 < p.hk || h1 > 2 * p.hk);
+    const int at = turns ? __ldg(p.rot.pos + m) : 0;
     long long slot = live ? __ldg(p.slots + m) : -1;
-    const long long page = slot >> p.cache.page_shift;
-    if (slot >= 0 && page >= p.cache.n_pages) {
-      atomicOr(p.status, kStatusInput);
-      slot = -1;
+    const int lane = threadIdx.x & 31, half8 = p.rot.half / 8, c8 = f0 / 8;
+    const int from = c8 < half8 ? lane + half8 : c8 < 2 * half8 ? lane - half8 : lane;
+    LaneTurn t;
+    long long page = 0, off = 0;
+    auto row_of = [&](int h) {
+      return h >= 2 * p.hk ? p.q.x + m * p.q.ts + (h - 2 * p.hk) * p.q.hs
+                           : h >= p.hk ? p.v.x + m * p.v.ts + (h - p.hk) * p.v.hs : p.k.x + m * p.k.ts + h * p.k.hs;
+    };
+    for (int jb = 0; jb < p.per_group; jb += kHeadBatch) {
+    uint4 w[kHeadBatch];
+#pragma unroll
+    for (int i = 0; i < kHeadBatch; ++i) {
+      const int h = h0 + jb + i;
+      w[i] = h < h1 ? *reinterpret_cast<const uint4*>(row_of(h) + f0) : make_uint4(0, 0, 0, 0);
     }
-    const long long off = slot & ((1 << p.cache.page_shift) - 1);
-#pragma unroll 2
-    for (int j = 0; j < p.per_group; ++j) {
-      const int h = h0 + j;
+    if (jb == 0) {
+      t.turned = 0;
+      if (turns) load_turn<VEC>(p, at, f0, t);
+      page = slot >> p.cache.page_shift;
+      if (slot >= 0 && page >= p.cache.n_pages) {
+        atomicOr(p.status, kStatusInput);
+        slot = -1;
+      }
+      off = slot & ((1 << p.cache.page_shift) - 1);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeadBatch; ++i) {
+      const int h = h0 + jb + i;
+      if (jb + i >= p.per_group) break;
       const bool row = h < h1;
       const bool is_q = h >= 2 * p.hk, is_v = !is_q && h >= p.hk;
-      float y[8] = {};
-      if (row) {
-        const bf16* x = is_q ? p.q.x + m * p.q.ts + (h - 2 * p.hk) * p.q.hs
-                             : is_v ? p.v.x + m * p.v.ts + (h - p.hk) * p.v.hs : p.k.x + m * p.k.ts + h * p.k.hs;
-        load_row<VEC>(p, x, f0, t, p.rotate && !is_v, y);
-      }
+      float y[8];
+      turn_piece<VEC>(p, w[i], row ? row_of(h) : p.k.x, f0, from, t, row && p.rotate && !is_v, y);
       // the row's largest magnitude, on the bits: an infinity or NaN is above every number
       unsigned top = 0;
       if (FMT != LORA_KV_BF16) {
@@ -199,6 +206,7 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
         if (f0 == 0) (is_v ? p.cache.vs : p.cache.ks)[r] = scale;
       }
     }
+    }
   }
 }
 
@@ -221,7 +229,7 @@ __device__ __forceinline__ float code_value(uint8_t c, int fmt) {
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadParams p) {
+__global__ void __launch_bounds__(256, 3) read_kernel(const __grid_constant__ ReadParams p) {
   pdl_wait();
   pdl_launch_dependents();
   constexpr int L = D / 8;
@@ -247,28 +255,42 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadP
       page = -1;
     }
     const int h0 = g * p.per_group, h1 = min(h0 + p.per_group, 2 * hk);
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h) {
-      const bool is_v = h >= hk;
-      const int head = is_v ? h - hk : h;
-      bf16* dst = (is_v ? p.v : p.k) + (r * hk + head) * D + f0;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (page >= 0) {
-        const long long src = ((page * hk + head) << p.cache.page_shift) + off;
+    auto dst = [&](int h) { return (h >= hk ? p.v : p.k) + (r * hk + (h >= hk ? h - hk : h)) * D + f0; };
+    if (page < 0) {
+      for (int h = h0; h < h1; ++h) *reinterpret_cast<uint4*>(dst(h)) = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    constexpr int kBatch = 8;
+    for (int hb = h0; hb < h1; hb += kBatch) {
+      uint4 w[kBatch];                 // the codes of 8-bit formats are its first half
+      float scale[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = hb + i;
+        if (h >= h1) break;
+        const bool is_v = h >= hk;
+        const long long src = ((page * hk + (is_v ? h - hk : h)) << p.cache.page_shift) + off;
         const void* base = is_v ? p.cache.v : p.cache.k;
         if constexpr (FMT == LORA_KV_BF16) {
-          w = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(base) + src * D + f0));
+          w[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(base) + src * D + f0));
         } else {
           const uint2 c = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + src * D + f0));
-          const float scale = __ldg((is_v ? p.cache.vs : p.cache.ks) + src);
+          w[i].x = c.x, w[i].y = c.y;
+          scale[i] = __ldg((is_v ? p.cache.vs : p.cache.ks) + src);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (hb + i >= h1) break;
+        if constexpr (FMT != LORA_KV_BF16) {
           float y[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            y[e] = code_value(static_cast<uint8_t>((e < 4 ? c.x : c.y) >> (8 * (e % 4))), FMT) * scale;
-          w = pack8(y);
+            y[e] = code_value(static_cast<uint8_t>((e < 4 ? w[i].x : w[i].y) >> (8 * (e % 4))), FMT) * scale[i];
+          w[i] = pack8(y);
         }
+        *reinterpret_cast<uint4*>(dst(hb + i)) = w[i];
       }
-      *reinterpret_cast<uint4*>(dst) = w;
     }
   }
 }

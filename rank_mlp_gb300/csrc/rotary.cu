@@ -18,6 +18,7 @@ struct RotaryParams {
   RotaryArgs rot;
   float sign;                // -1: the inverse rotation
   int interleaved;
+  int dim;                   // head_dim
   int items;                 // thread items of a head: rotated ones, then passed-through ones
   int turned;                // the rotated ones among them
   int per_group, groups;     // heads a thread walks; such groups of heads
@@ -49,10 +50,17 @@ __device__ __forceinline__ void split_index(const RotaryParams& p, unsigned long
   }
 }
 
-// VEC: rot_dim is a multiple of 16, so that a thread's pairs are whole 16-byte pieces;
-// otherwise it owns one pair (or one passed-through feature) at a time.
-template <bool VEC>
-__global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ RotaryParams p) {
+// How a thread's items look (rot_dim a multiple of 16 but for kScalar):
+//   kHalves       two 16-byte pieces of a head: half a rotation apart, or neighbours that pass
+//   kInterleaved  one piece
+//   kScalar       one pair of features, or one that passes
+enum RotaryMode : int { kHalves = 0, kInterleaved = 1, kScalar = 2 };
+
+// At most 64 registers a thread: the loads in flight come from many resident threads (with
+// the loads of four heads held by twice as many registers the kernel was 1.2 to 1.7 times
+// slower).
+template <int MODE>
+__global__ void __launch_bounds__(256, 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
   pdl_wait();
   pdl_launch_dependents();
   const unsigned long long total = static_cast<unsigned long long>(p.M) * p.groups * p.items;
@@ -62,18 +70,17 @@ __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ Rot
     int g, it;
     split_index(p, idx, m, g, it);
     const int h0 = g * p.per_group, h1 = min(h0 + p.per_group, p.heads);
-    if (it >= p.turned) {
-      const int f = 2 * half + (it - p.turned) * (VEC ? 8 : 1);
-      for (int h = h0; h < h1; ++h) {
-        if (VEC)
-          *reinterpret_cast<uint4*>(row_out(p, m, h) + f) = *reinterpret_cast<const uint4*>(row_in(p, m, h) + f);
-        else
-          row_out(p, m, h)[f] = row_in(p, m, h)[f];
+    const bool turned = it < p.turned;
+    // The position, the first heads' pieces and then the table entries, which wait for the
+    // position: two memory latencies in a row instead of three.
+    const int at = turned ? __ldg(p.rot.pos + m) : 0;
+    if constexpr (MODE == kScalar) {
+      const long long tab = turned ? static_cast<long long>(checked_position(p.rot, at, p.status)) * half : 0;
+      if (!turned) {
+        const int f = 2 * half + it - p.turned;
+        for (int h = h0; h < h1; ++h) row_out(p, m, h)[f] = row_in(p, m, h)[f];
+        continue;
       }
-      continue;
-    }
-    const long long tab = static_cast<long long>(rotary_position(p.rot, m, p.status)) * half;
-    if (!VEC) {
       const float c = __ldg(p.rot.cos + tab + it), s = p.sign * __ldg(p.rot.sin + tab + it);
       const int fa = p.interleaved ? 2 * it : it, fb = p.interleaved ? 2 * it + 1 : it + half;
       for (int h = h0; h < h1; ++h) {
@@ -84,38 +91,78 @@ __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ Rot
         y[fa] = __float2bfloat16_rn(a);
         y[fb] = __float2bfloat16_rn(b);
       }
-    } else if (p.interleaved) {
-      // one piece: features [8 it, 8 it + 8), table columns [4 it, 4 it + 4)
-      const float4 c4 = __ldg(reinterpret_cast<const float4*>(p.rot.cos + tab) + it);
-      const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.rot.sin + tab) + it);
-      const float c[4] = {c4.x, c4.y, c4.z, c4.w};
-      const float s[4] = {p.sign * s4.x, p.sign * s4.y, p.sign * s4.z, p.sign * s4.w};
-#pragma unroll 4
-      for (int h = h0; h < h1; ++h) {
-        float x[8];
-        unpack8(*reinterpret_cast<const uint4*>(row_in(p, m, h) + 8 * it), x);
+    } else if constexpr (MODE == kInterleaved) {
+      // features [8 it, 8 it + 8), table columns [4 it, 4 it + 4)
+      float4 c = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s = c;
+      for (int hb = h0; hb < h1; hb += 4) {
+        uint4 w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) turn(x[2 * e], x[2 * e + 1], c[e], s[e], x[2 * e], x[2 * e + 1]);
-        *reinterpret_cast<uint4*>(row_out(p, m, h) + 8 * it) = pack8(x);
+        for (int i = 0; i < 4; ++i)
+          if (hb + i < h1) w[i] = *reinterpret_cast<const uint4*>(row_in(p, m, hb + i) + 8 * it);
+        if (turned && hb == h0) {
+          const long long tab = static_cast<long long>(checked_position(p.rot, at, p.status)) * half;
+          c = __ldg(reinterpret_cast<const float4*>(p.rot.cos + tab) + it);
+          s = __ldg(reinterpret_cast<const float4*>(p.rot.sin + tab) + it);
+          s.x *= p.sign, s.y *= p.sign, s.z *= p.sign, s.w *= p.sign;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (hb + i >= h1) break;
+          if (turned) {
+            float x[8];
+            unpack8(w[i], x);
+            turn(x[0], x[1], c.x, s.x, x[0], x[1]);
+            turn(x[2], x[3], c.y, s.y, x[2], x[3]);
+            turn(x[4], x[5], c.z, s.z, x[4], x[5]);
+            turn(x[6], x[7], c.w, s.w, x[6], x[7]);
+            w[i] = pack8(x);
+          }
+          *reinterpret_cast<uint4*>(row_out(p, m, hb + i) + 8 * it) = w[i];
+        }
       }
     } else {
-      // two pieces: features [8 it, 8 it + 8) and the same half a rotation on
+      const int fa = turned ? 8 * it : 2 * half + 16 * (it - p.turned);
+      const int fb = turned ? fa + half : fa + 8;
+      const bool two = turned || fb < p.dim;              // the last passed piece may be alone
       float c[8], s[8];
-      load8f(p.rot.cos + tab + 8 * it, c);
-      load8f(p.rot.sin + tab + 8 * it, s);
+      for (int hb = h0; hb < h1; hb += 2) {
+        uint4 wa[2], wb[2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] *= p.sign;
-#pragma unroll 4
-      for (int h = h0; h < h1; ++h) {
-        const bf16* x = row_in(p, m, h) + 8 * it;
-        float a[8], b[8];
-        unpack8(*reinterpret_cast<const uint4*>(x), a);
-        unpack8(*reinterpret_cast<const uint4*>(x + half), b);
+        for (int i = 0; i < 2; ++i) {
+          if (hb + i >= h1) break;
+          const bf16* x = row_in(p, m, hb + i);
+          wa[i] = *reinterpret_cast<const uint4*>(x + fa);
+          if (two) wb[i] = *reinterpret_cast<const uint4*>(x + fb);
+        }
+        if (turned && hb == h0) {
+          const long long tab = static_cast<long long>(checked_position(p.rot, at, p.status)) * half;
+          load8f(p.rot.cos + tab + 8 * it, c);
+          load8f(p.rot.sin + tab + 8 * it, s);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) turn(a[e], b[e], c[e], s[e], a[e], b[e]);
-        bf16* y = row_out(p, m, h) + 8 * it;
-        *reinterpret_cast<uint4*>(y) = pack8(a);
-        *reinterpret_cast<uint4*>(y + half) = pack8(b);
+          for (int e = 0; e < 8; ++e) s[e] *= p.sign;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (hb + i >= h1) break;
+          if (turned) {
+            const uint32_t va[4] = {wa[i].x, wa[i].y, wa[i].z, wa[i].w}, vb[4] = {wb[i].x, wb[i].y, wb[i].z, wb[i].w};
+            uint32_t oa[4], ob[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float a0, a1, b0, b1;
+              turn(__uint_as_float(va[e] << 16), __uint_as_float(vb[e] << 16), c[2 * e], s[2 * e], a0, b0);
+              turn(__uint_as_float(va[e] & 0xFFFF0000u), __uint_as_float(vb[e] & 0xFFFF0000u), c[2 * e + 1], s[2 * e + 1],
+                   a1, b1);
+              oa[e] = pack_bf16x2(a0, a1);
+              ob[e] = pack_bf16x2(b0, b1);
+            }
+            wa[i] = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+            wb[i] = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+          }
+          bf16* y = row_out(p, m, hb + i);
+          *reinterpret_cast<uint4*>(y + fa) = wa[i];
+          if (two) *reinterpret_cast<uint4*>(y + fb) = wb[i];
+        }
       }
     }
   }
@@ -213,17 +260,19 @@ extern "C" lora_status_t lora_rotary(int64_t M, int head_dim, const lora_heads_t
   p.sign = inverse ? -1.0f : 1.0f;
   p.interleaved = rot->layout == LORA_ROTARY_INTERLEAVED;
   const bool vec = rot->rot_dim % 16 == 0;
+  const int passed = head_dim - rot->rot_dim;
+  p.dim = head_dim;
   p.turned = !vec ? rot->rot_dim / 2 : p.interleaved ? rot->rot_dim / 8 : rot->rot_dim / 16;
-  const int passed = (head_dim - rot->rot_dim) / (vec ? 8 : 1);
-  p.items = p.turned + (in_place ? 0 : passed);
+  p.items = p.turned;
+  if (!in_place) p.items += static_cast<int>(!vec ? passed : p.interleaved ? passed / 8 : ceil_div(passed, 16));
   p.per_group = heads_per_group(M, p.items, p.heads);
   p.groups = static_cast<int>(ceil_div(p.heads, p.per_group));
   p.status = static_cast<unsigned*>(ws);
   // M, groups and items are below 2^31, 2^17 and 2^10: the product fits 64 bits
   const int64_t blocks = ceil_div(M * p.groups * p.items, 256);
   const unsigned grid = static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30));
-  return launch_counted(vec ? rotary_kernel<true> : rotary_kernel<false>, dim3(grid), dim3(256), 0, LORA_KIND_ROPE,
-                        stream, p);
+  return launch_counted(!vec ? rotary_kernel<kScalar> : p.interleaved ? rotary_kernel<kInterleaved> : rotary_kernel<kHalves>,
+                        dim3(grid), dim3(256), 0, LORA_KIND_ROPE, stream, p);
 }
 
 extern "C" lora_status_t lora_rope_table_scaled(float* cos, float* sin, int64_t n_pos, int rot_dim, double base,

@@ -84,11 +84,13 @@ inline CacheArgs cache_args(const lora_kv_cache_t* c) {
   return CacheArgs{c->k, c->v, c->k_scale, c->v_scale, c->n_pages, shift, c->heads};
 }
 
-// Heads each thread group walks one after the other: as many as leave the GPU enough
-// groups (a group of `lanes` threads) to hide its loads; the table entries of a token
-// are loaded once for them.
+// Heads each thread group (of `lanes` threads) walks: up to eight, as many as leave the GPU
+// some two rounds of its resident threads, so that the last round's idle part is small;
+// the table entries of a token are loaded once for them.  kHeadBatch: heads whose loads the
+// cache kernels issue together.
+constexpr int kHeadBatch = 4;
 inline int heads_per_group(int64_t M, int lanes, int heads) {
-  const int64_t want = static_cast<int64_t>(num_sms()) * 1024;     // threads
+  const int64_t want = static_cast<int64_t>(num_sms()) * 2048 * 2;     // threads
   int hp = 8;
   while (hp > 1 && M * lanes * ceil_div(heads, hp) < want) hp >>= 1;
   return hp;
@@ -96,8 +98,7 @@ inline int heads_per_group(int64_t M, int lanes, int heads) {
 
 // ---------------------------------------------------------------- device arithmetic
 
-__device__ __forceinline__ int rotary_position(const RotaryArgs& r, long long m, unsigned* status) {
-  const int pos = __ldg(r.pos + m);
+__device__ __forceinline__ int checked_position(const RotaryArgs& r, int pos, unsigned* status) {
   if (pos >= 0 && pos < r.npos) return pos;
   atomicOr(status, kStatusInput);
   return 0;
