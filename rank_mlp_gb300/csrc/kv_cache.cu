@@ -88,10 +88,11 @@ __device__ __forceinline__ void turn_piece(const AppendParams& p, uint4 own, con
       o[e] = (t.turned >> e) & 1u ? __bfloat162float(x[f < half ? f + half : f - half]) : 0.0f;
     }
   }
-  if (!rotate) return;
+  if (!rotate || !t.turned) return;
+  // (scalar on purpose: as packed f32x2 operations the compiler joins the product and the sum)
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    if ((t.turned >> e) & 1u) y[e] = __fadd_rn(__fmul_rn(y[e], t.c[e]), __fmul_rn(o[e], t.s[e]));
+    if (VEC || ((t.turned >> e) & 1u)) y[e] = __fadd_rn(__fmul_rn(y[e], t.c[e]), __fmul_rn(o[e], t.s[e]));
 }
 
 template <int FMT>
@@ -104,38 +105,50 @@ struct Quant<LORA_KV_FP8> {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       w[e] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * e], y[2 * e + 1]), __NV_SATFINITE, __NV_E4M3);
-    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
   }
 };
 template <>
 struct Quant<LORA_KV_INT8> {
   static constexpr float kTop = 127.0f;
+  // |y| is at most 127 (1 + 2^-22): adding 1.5 * 2^23 rounds it to a whole number, ties to
+  // even, whose two's complement is the sum's low byte
   static __device__ __forceinline__ uint2 codes(const float (&y)[8]) {
-    uint32_t w[2] = {0, 0};
+    uint32_t w[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = max(-127, min(127, __float2int_rn(y[e])));
-      w[e / 4] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * (e % 4));
-    }
-    return make_uint2(w[0], w[1]);
+    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__fadd_rn(y[e], 12582912.0f));
+    return make_uint2(__byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410));
   }
 };
 
+// The larger of |a| and |b|; a NaN if either is one.
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+  float y;
+  asm("{\n\t.reg .f32 a, b;\n\tabs.f32 a, %1;\n\tabs.f32 b, %2;\n\tmax.NaN.f32 %0, a, b;\n\t}" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+constexpr int kAppendThreads = 128;
+
 template <int D, int FMT, bool VEC>
-__global__ void __launch_bounds__(256, 3) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_constant__ AppendParams p) {
   pdl_wait();
   pdl_launch_dependents();
   constexpr int L = D / 8;                       // lanes of a row
   const int f0 = (threadIdx.x % L) * 8;
   const int heads = 2 * p.hk + p.hq;
   const unsigned long long units = static_cast<unsigned long long>(p.M) * p.groups;
-  const unsigned long long step = static_cast<unsigned long long>(gridDim.x) * (256 / L);
+  const unsigned long long step = static_cast<unsigned long long>(gridDim.x) * (kAppendThreads / L);
   // the warp's lane groups run the same number of steps: the shuffles take whole warps
-  for (unsigned long long base = static_cast<unsigned long long>(blockIdx.x) * (256 / L); base < units; base += step) {
+  for (unsigned long long base = static_cast<unsigned long long>(blockIdx.x) * (kAppendThreads / L); base < units; base += step) {
     const unsigned long long u = base + threadIdx.x / L;
     const bool live = u < units;
-    const long long m = live ? static_cast<long long>(u / static_cast<unsigned>(p.groups)) : 0;
-    const int g = live ? static_cast<int>(u - static_cast<unsigned long long>(m) * p.groups) : 0;
+    // neighbouring lane groups take neighbouring tokens and the same heads, so that a warp's
+    // rows go the same way (k, v or q)
+    const int g = !live ? 0 : units <= 0xffffffffull ? static_cast<int>(static_cast<unsigned>(u) / static_cast<unsigned>(p.M))
+                                                     : static_cast<int>(u / static_cast<unsigned long long>(p.M));
+    const long long m = live ? static_cast<long long>(u) - g * p.M : 0;
     const int h0 = g * p.per_group, h1 = live ? min(h0 + p.per_group, heads) : h0;
     // slot and position, the first heads' pieces, then the table entries, which wait for the
     // position: the loads' latencies overlap
@@ -145,10 +158,13 @@ __global__ void __launch_bounds__(256, 3) append_kernel(const __grid_constant__ 
     const int lane = threadIdx.x & 31, half8 = p.rot.half / 8, c8 = f0 / 8;
     const int from = c8 < half8 ? lane + half8 : c8 < 2 * half8 ? lane - half8 : lane;
     LaneTurn t;
-    long long page = 0, off = 0;
+    long long row0 = 0;        // the slot's row of head 0
+    const bf16* k_row = p.k.x + m * p.k.ts;
+    const bf16* v_row = p.v.x + m * p.v.ts - p.hk * p.v.hs;
+    const bf16* q_row = p.q.x + m * p.q.ts - 2 * p.hk * p.q.hs;
     auto row_of = [&](int h) {
-      return h >= 2 * p.hk ? p.q.x + m * p.q.ts + (h - 2 * p.hk) * p.q.hs
-                           : h >= p.hk ? p.v.x + m * p.v.ts + (h - p.hk) * p.v.hs : p.k.x + m * p.k.ts + h * p.k.hs;
+      const bf16* base = h >= 2 * p.hk ? q_row : h >= p.hk ? v_row : k_row;
+      return base + h * (h >= 2 * p.hk ? p.q.hs : h >= p.hk ? p.v.hs : p.k.hs);
     };
     for (int jb = 0; jb < p.per_group; jb += kHeadBatch) {
     uint4 w[kHeadBatch];
@@ -160,12 +176,12 @@ __global__ void __launch_bounds__(256, 3) append_kernel(const __grid_constant__ 
     if (jb == 0) {
       t.turned = 0;
       if (turns) load_turn<VEC>(p, at, f0, t);
-      page = slot >> p.cache.page_shift;
+      const long long page = slot >> p.cache.page_shift;
       if (slot >= 0 && page >= p.cache.n_pages) {
         atomicOr(p.status, kStatusInput);
         slot = -1;
       }
-      off = slot & ((1 << p.cache.page_shift) - 1);
+      row0 = (page * p.cache.heads << p.cache.page_shift) + (slot & ((1 << p.cache.page_shift) - 1));
     }
 #pragma unroll
     for (int i = 0; i < kHeadBatch; ++i) {
@@ -175,15 +191,15 @@ __global__ void __launch_bounds__(256, 3) append_kernel(const __grid_constant__ 
       const bool is_q = h >= 2 * p.hk, is_v = !is_q && h >= p.hk;
       float y[8];
       turn_piece<VEC>(p, w[i], row ? row_of(h) : p.k.x, f0, from, t, row && p.rotate && !is_v, y);
-      // the row's largest magnitude, on the bits: an infinity or NaN is above every number
-      unsigned top = 0;
-      if (FMT != LORA_KV_BF16) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int d = L / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-      } else {
+      // the row's largest magnitude (a NaN if it holds one)
+      float top = 0.0f;
+      if (FMT == LORA_KV_BF16) {
         __syncwarp();          // every lane of the row has read it (yq may be q)
+      } else if (__any_sync(0xffffffffu, row && !is_q)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max_abs_nan(top, y[e]);
+#pragma unroll
+        for (int d = L / 2; d > 0; d >>= 1) top = max_abs_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
       }
       if (!row) continue;
       if (is_q) {
@@ -191,18 +207,18 @@ __global__ void __launch_bounds__(256, 3) append_kernel(const __grid_constant__ 
         continue;
       }
       if (slot < 0) continue;
-      const long long r = ((page * p.cache.heads + (is_v ? h - p.hk : h)) << p.cache.page_shift) + off;
-      void* dst = is_v ? p.cache.v : p.cache.k;
+      const long long r = row0 + (static_cast<long long>(is_v ? h - p.hk : h) << p.cache.page_shift);
       if constexpr (FMT == LORA_KV_BF16) {
-        *reinterpret_cast<uint4*>(static_cast<bf16*>(dst) + r * D + f0) = pack8(y);
+        *reinterpret_cast<uint4*>(static_cast<bf16*>(is_v ? p.cache.v : p.cache.k) + r * D + f0) = pack8(y);
       } else {
-        const bool fine = top < 0x7F800000u;
-        const float scale = fine ? fmaxf(__fmul_rn(__uint_as_float(top), 1.0f / Quant<FMT>::kTop), 1.17549435e-38f)
-                                 : __uint_as_float(0x7FC00000u);
+        const bool fine = top < INFINITY;
+        const float scale = fine ? fmaxf(__fmul_rn(top, 1.0f / Quant<FMT>::kTop), 1.17549435e-38f) : __uint_as_float(0x7FC00000u);
         const float inv = __frcp_rn(scale);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = fine ? __fmul_rn(y[e], inv) : 0.0f;
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(dst) + r * D + f0) = Quant<FMT>::codes(y);
+        for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(y[e], inv);
+        uint2 c = Quant<FMT>::codes(y);
+        if (!fine) c = make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? p.cache.v : p.cache.k) + r * D + f0) = c;
         if (f0 == 0) (is_v ? p.cache.vs : p.cache.ks)[r] = scale;
       }
     }
@@ -361,8 +377,8 @@ extern "C" lora_status_t lora_kv_append(int64_t M, const lora_kv_cache_t* cache,
   const bool vec = rot == nullptr || rot->rot_dim % 16 == 0;
   const AppendKernel f = D == 64 ? append_of<64>(cache->format, vec)
                                  : D == 128 ? append_of<128>(cache->format, vec) : append_of<256>(cache->format, vec);
-  const int64_t blocks = ceil_div(M * p.groups, 256 / (D / 8));
-  return launch_counted(f, dim3(static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30))), dim3(256), 0,
+  const int64_t blocks = ceil_div(M * p.groups, kAppendThreads / (D / 8));
+  return launch_counted(f, dim3(static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30))), dim3(kAppendThreads), 0,
                         LORA_KIND_CACHE, stream, p);
 }
 
