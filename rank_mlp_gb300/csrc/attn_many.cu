@@ -16,9 +16,16 @@
 // the next tile's scores.  An accumulator is rescaled, in tensor memory, only when a row's
 // maximum rises by more than 2^8 (kMaxSlack).
 //
-// 8-bit caches: the ring's raw tiles are turned into bf16 tiles by four more warps, once
-// for all the tile's rows (both formats' codes are bf16 numbers); a position's K scale
-// multiplies its score and its V scale its weight, in f32.
+// 8-bit caches run in f16, which holds both formats' codes exactly: four more warps turn
+// the ring's raw tiles into f16 tiles, once for all the tile's rows (to bf16 it takes up to
+// five instructions for two codes, to f16 one or two, and these conversions set the pace).
+// The softmax warps turn their rows of Q, scaled by a power of two to f16's upper range
+// (exact for features down to 2^-29 of the row's largest).  A position's K scale multiplies
+// its score and its V scale its weight, in f32; weights and sums carry a factor 2^-E, E the
+// exponent of the largest V scale so far, which keeps the f16 products in range (a weight
+// times scale below 2^-24 of that largest scale is lost).
+#include <type_traits>
+
 #include "paged_attn.cuh"
 #include "codes.cuh"
 
@@ -62,7 +69,7 @@ struct ManyCfg {
   static constexpr int kOutCols = kRaw && D >= 128 ? 32 : 64;
   static constexpr int kOffOut = kOffScales + (kRaw ? kScaleSlots * 2 * KT * 4 : 0);
   static constexpr int kOffBars = kOffOut + (kStaged ? kSoftWarps * 32 * kOutCols * 2 : 0);
-  static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 6 + 5 * NQ + (kRaw ? kScaleSlots : 0);
+  static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 6 + 5 * NQ + (kRaw ? kScaleSlots + NQ : 0);
   static constexpr int kOffPlan = kOffBars + kNumBars * 8 + 8;
   static constexpr int kSmem = kOffPlan + static_cast<int>(sizeof(PlanScratch<kThreads>)) + 1024;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -98,7 +105,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto& scratch = *reinterpret_cast<PlanScratch<C::kThreads>*>(smem + C::kOffPlan);
   const uint32_t bar0 = smem_u32(bars);
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };                          // a bf16 tile is in the ring
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };                          // a 16-bit tile is in the ring
   auto empty_bar = [&](int s) { return bar0 + 8u * (ST + s); };
   auto rfull_bar = [&](int s) { return bar0 + 8u * (2 * ST + s); };              // a raw tile
   auto rempty_bar = [&](int s) { return bar0 + 8u * (2 * ST + RS + s); };
@@ -112,6 +119,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
   auto qfree_bar = [&](int q) { return bar0 + 8u * (kB + 6 + 2 * C::NQ + q); };  // its last scores are done
   auto drain_bar = [&](int q) { return bar0 + 8u * (kB + 6 + 3 * C::NQ + q); };
   auto scale_bar = [&](int s) { return bar0 + 8u * (kB + 6 + 5 * C::NQ + s); };  // a tile's scales are in slot s
+  auto qraw_bar = [&](int q) { return bar0 + 8u * (kB + 6 + 5 * C::NQ + C::kScaleSlots + q); };   // 8-bit: Q as bf16
   auto turn_bar = [&](int q) { return bar0 + 8u * (kB + 6 + 4 * C::NQ + q); };   // half q's lane may issue
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -133,7 +141,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
     }
     for (int q = 0; q < C::NQ; ++q) {
       mbar_init(odone_bar(q), 1);
-      mbar_init(qready_bar(q), 1);
+      mbar_init(qready_bar(q), C::kRaw ? 4 : 1);
+      if (C::kRaw) mbar_init(qraw_bar(q), 1);
       mbar_init(qfree_bar(q), 1);
       mbar_init(drain_bar(q), 1);
       mbar_init(turn_bar(q), 1);
@@ -244,9 +253,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
     // it from a diverged lane took longer).
     {
       const int q = __shfl_sync(0xffffffffu, warp - 1, 0);
-      constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, 0, 1);
+      // (f16 operands: the format fields of A and B, bits 7 and 10, are 0)
+      constexpr uint32_t kTypes = C::kRaw ? ~((1u << 7) | (1u << 10)) : ~0u;
+      constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, 0, 1) & kTypes;
       // a negative scale negates Q as it is read (bit 13)
-      const uint32_t idesc_s = idesc_bf16_f32(128, KT, 0, 0) | (p.scale_log2 < 0.0f ? 1u << 13 : 0u);
+      const uint32_t idesc_s = (idesc_bf16_f32(128, KT, 0, 0) & kTypes) | (p.scale_log2 < 0.0f ? 1u << 13 : 0u);
       const uint64_t qdesc = smem_desc_sw128(sbase + q * C::kQBytes, 16u, 1024u);
       const uint64_t kdesc0 = smem_desc_sw128(ring, 16u, 1024u);
       const uint64_t vdesc0 = smem_desc_sw128(ring, KT * 128u, 1024u);
@@ -414,6 +425,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
     if (lane == 0) {
       uint32_t used[2] = {0, 0};          // items of each half so far
       bool ok = true;
+      auto qbar = [&](int q) { return C::kRaw ? qraw_bar(q) : qready_bar(q); };
       while (ok && walk.next(p, w)) {
         const int nq = halves_of<C>(p, w), kvh = w.slice / p.spg;
         const int head = kvh * p.group + (w.slice - kvh * p.spg) * p.hs;
@@ -422,16 +434,16 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           if (used[q] > 0) ok = attn_wait(qfree_bar(q), (used[q] - 1u) & 1u, abort_flag, p);
           if (!ok) break;
           ++used[q];
-          mbar_arrive_expect_tx(qready_bar(q), static_cast<uint32_t>(p.th * p.hs * D * 2));
+          mbar_arrive_expect_tx(qbar(q), static_cast<uint32_t>(p.th * p.hs * D * 2));
 #pragma unroll
           for (int x = 0; x < C::kHalves; ++x)
-            tma_load_3d(sbase + q * C::kQBytes + x * (128 * 128), &p.qmap, qready_bar(q), 64 * x, head,
+            tma_load_3d(sbase + q * C::kQBytes + x * (128 * 128), &p.qmap, qbar(q), 64 * x, head,
                         w.s.q0 + w.rt * p.tt + q * p.th);
         }
       }
       if (!ok)                            // copies in flight land before the block ends
         for (int q = 0; q < C::NQ; ++q)
-          if (used[q] > 0) attn_wait_drain(qready_bar(q), (used[q] - 1u) & 1u, p);
+          if (used[q] > 0) attn_wait_drain(qbar(q), (used[q] - 1u) & 1u, p);
     }
   }
   } else if (warp < 4 + C::kSoftWarps) {
@@ -444,7 +456,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
     const uint32_t o_tmem = tmem + lanes + C::kOCol0 + q * D;
     // (a scale of 0 becomes the smallest normal one: finite scores weigh the same, and a
     // hidden score stays -inf)
-    const float c = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
+    const float scale = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
+    float c = scale;
+    uint32_t qphase = 0;
     const bool out_v8 = rows_v8_aligned(p.out, 16);
     uint32_t T = 0, tile = 0;                     // position tiles, ring tiles before this item
     uint32_t done = 0;                            // O += P V steps of this half so far
@@ -461,7 +475,36 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
       const bool own = row_owner(p, w.s, w.slice, w.rt, q, r, tok, head);
       if (own) row_range(p, w.s, tok, lo, hi); else lo = 0, hi = 0x7fffffff;
       const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
-      float top = -INFINITY;
+      if constexpr (C::kRaw) {
+        ok = attn_wait(qraw_bar(q), qphase, abort_flag, p);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        qphase ^= 1u;
+        const uint32_t line = sbase + q * C::kQBytes + r * 128;
+        auto piece = [&](int e) { return line + (e >> 3) * (128 * 128) + (((e & 7) ^ (r & 7)) << 4); };
+        unsigned big = 0;
+#pragma unroll 8
+        for (int e = 0; e < D / 8; ++e) {
+          const uint4 v = ld_shared_v4(piece(e));
+          big = max(max(big, max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu)), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu));
+          big = max(max(big, max(v.z & 0x7FFFu, (v.z >> 16) & 0x7FFFu)), max(v.w & 0x7FFFu, (v.w >> 16) & 0x7FFFu));
+        }
+        // the row times 2^(14 - exponent of its largest), and the score scale without it
+        const float f = __uint_as_float(static_cast<unsigned>(min(254, 268 - static_cast<int>(big >> 7))) << 23);
+        c = scale / f;
+        auto turn2 = [&](uint32_t u) { return pack_f16x2(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xFFFF0000u) * f); };
+#pragma unroll 4
+        for (int e = 0; e < D / 8; ++e) {
+          const uint4 v = ld_shared_v4(piece(e));
+          st_shared_v4(piece(e), make_uint4(turn2(v.x), turn2(v.y), turn2(v.z), turn2(v.w)));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qready_bar(q));
+      }
+      // top: the row's running maximum (scaled, log2); ref = top + exponent: what weights and
+      // sums are relative to
+      float top = -INFINITY, ref = -INFINITY;
+      int exponent = C::kRaw ? -90 : 0;
       float2 sum = make_float2(0.0f, 0.0f);          // two partial sums
       for (int i = 0; i < n; ++i) {
         const uint32_t buf = C::NQ == 2 ? q : (T + i) & 1u;
@@ -482,9 +525,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         }
         tc_fence_after_sync();
         const bool edge = k0 < lo_max || k0 + KT > hi_min;
-        // the row's scores, read once and held in registers, 32 columns on their way while
-        // the 32 before are worked on
-        uint32_t v[KT / 32][32];
+        // compiled twice: for tiles that all of the warp's rows see whole (nearly all), and for
+        // the others
+        auto softmax = [&](auto at_edge) {
+        constexpr bool kEdge = decltype(at_edge)::value;
+        // The row's scores, 32 columns on their way while the 32 before are worked on.  16-bit
+        // caches read them once and hold them in registers; 8-bit ones, whose warps have fewer
+        // registers, read them again for the second pass (holding them spilled, and was slower).
+        constexpr bool kHold = !C::kRaw;
+        uint32_t v[kHold ? KT / 32 : 2][32];
         // scores of columns [x, x + 32): K scales, mask
         auto finish = [&](uint32_t (&v)[32], int x) {
           if (C::kRaw) {
@@ -497,7 +546,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
               v[e + 2] = __float_as_uint(b.x), v[e + 3] = __float_as_uint(b.y);
             }
           }
-          if (edge) {
+          if (kEdge) {
             const int key = k0 + x;
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = key + e >= lo && key + e < hi ? v[e] : 0xFF800000u;   // -inf
@@ -513,23 +562,50 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           }
         };
         tmem_ld32(s_tmem, v[0]);
+        if constexpr (kHold) {
 #pragma unroll
-        for (int x = 0; x < KT / 32; ++x) {
-          tmem_ld_wait_for(v[x]);
-          if (x + 1 < KT / 32) tmem_ld32(s_tmem + 32 * (x + 1), v[x + 1]);
-          finish(v[x], 32 * x);
-          maxima(v[x]);
+          for (int x = 0; x < KT / 32; ++x) {
+            tmem_ld_wait_for(v[x]);
+            if (x + 1 < KT / 32) tmem_ld32(s_tmem + 32 * (x + 1), v[x + 1]);
+            finish(v[x], 32 * x);
+            maxima(v[x]);
+          }
+        } else {
+#pragma unroll 1
+          for (int x = 0; x < KT; x += 64) {
+            tmem_ld_wait_for(v[0]);
+            tmem_ld32(s_tmem + x + 32, v[1]);
+            finish(v[0], x);
+            maxima(v[0]);
+            tmem_ld_wait_for(v[1]);
+            tmem_ld32(s_tmem + (x + 64 < KT ? x + 64 : 0), v[0]);       // at the end: for the second pass
+            finish(v[1], x + 32);
+            maxima(v[1]);
+          }
         }
         const float cand = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
-        if (__any_sync(0xffffffffu, cand > top + kMaxSlack)) {
-          const float next = fmaxf(top, cand);
-          const float f = next == -INFINITY ? 1.0f : exp2_approx(top - next);
-          top = next;
+        int larger = exponent;
+        if (C::kRaw) {
+          // exponent of the largest V scale of the tile's positions (a NaN, a broken row's, aside)
+          unsigned big = 0;
+#pragma unroll
+          for (int e = 0; e < KT / 32; ++e) {
+            const unsigned bits = __float_as_uint(vs[32 * e + lane]);
+            if (k0 + 32 * e + lane < w.s.kv && bits < 0x7F800000u) big = max(big, bits);
+          }
+          larger = max(larger, min(110, static_cast<int>(__reduce_max_sync(0xffffffffu, big) >> 23) - 126));
+        }
+        if (__any_sync(0xffffffffu, cand > top + kMaxSlack || larger > exponent)) {
+          top = fmaxf(top, cand);
+          exponent = larger;
+          const float next = top + exponent;
+          const float f = next == -INFINITY ? 1.0f : exp2_approx(ref - next);
+          ref = next;
           sum.x *= f;
           sum.y *= f;
           if (i > 0) {
             ok = attn_wait(odone_bar(q), (done - 1u) & 1u, abort_flag, p);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, ok)) return false;
             tc_fence_after_sync();
 #pragma unroll 1
             for (int x = 0; x < D; x += 16) {
@@ -543,8 +619,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             tmem_st_wait();
           }
         }
-        const float ref = top == -INFINITY ? 0.0f : top;
-        const float2 c2 = make_float2(c, c), ref2 = make_float2(-ref, -ref);
+        const float base = ref == -INFINITY ? 0.0f : -ref;
+        const float2 c2 = make_float2(c, c), ref2 = make_float2(base, base);
         float2 l[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         auto weights = [&](const uint32_t (&v)[32], int x) {
           uint32_t u[16];
@@ -562,7 +638,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
               const float4 f = *reinterpret_cast<const float4*>(vs + x + e);
               y[0] = mul_f32x2(y[0], make_float2(f.x, f.y));
               y[1] = mul_f32x2(y[1], make_float2(f.z, f.w));
-              if (edge) {                 // a hidden position's scale may be anything
+              if (kEdge) {                 // a hidden position's scale may be anything
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                   if (v[e + 2 * k] == 0xFF800000u) y[k].x = 0.0f;
@@ -570,8 +646,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
                 }
               }
             }
-            u[e / 2] = pack_bf16x2(y[0].x, y[0].y);
-            u[e / 2 + 1] = pack_bf16x2(y[1].x, y[1].y);
+            u[e / 2] = C::kRaw ? pack_f16x2(y[0].x, y[0].y) : pack_bf16x2(y[0].x, y[0].y);
+            u[e / 2 + 1] = C::kRaw ? pack_f16x2(y[1].x, y[1].y) : pack_bf16x2(y[1].x, y[1].y);
           }
           tmem_st16(s_tmem + x / 2, u);
         };
@@ -580,7 +656,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           // NaN: they are cleared before the first weights are handed over (both halves'
           // warps may, with the same zeros)
           ok = attn_wait(full_bar(vidx % ST), (vidx / ST) & 1u, abort_flag, p);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          if (!__all_sync(0xffffffffu, ok)) return false;
           const uint32_t vt = ring + (vidx % ST) * C::kTile;
           for (int row = max(w.s.kv - k0, 0) + quarter; row < KT; row += 4)
             for (int e = lane; e < D / 8; e += 32)
@@ -588,17 +664,41 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           fence_proxy_async_smem();
         }
         // half of a tile's weights are handed over while the other half is made
-#pragma unroll
-        for (int x = 0; x < KT / 32; ++x) {
-          weights(v[x], 32 * x);
-          if (x != KT / 64 - 1 && x != KT / 32 - 1) continue;
+        auto hand_over = [&](int half) {
           tmem_st_wait();
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(pready_bar(buf, x == KT / 32 - 1 ? 1 : 0));
+          if (lane == 0) mbar_arrive(pready_bar(buf, half));
+        };
+        if constexpr (kHold) {
+#pragma unroll
+          for (int x = 0; x < KT / 32; ++x) {
+            weights(v[x], 32 * x);
+            if (x == KT / 64 - 1) hand_over(0);
+            if (x == KT / 32 - 1) hand_over(1);
+          }
+        } else {
+          // (weights of columns [x, x + 32) overwrite scores [x / 2, x / 2 + 16), long read)
+#pragma unroll 1
+          for (int x = 0; x < KT; x += 64) {
+            tmem_ld_wait_for(v[0]);
+            tmem_ld32(s_tmem + x + 32, v[1]);
+            finish(v[0], x);
+            weights(v[0], x);
+            if (KT == 64) hand_over(0);
+            tmem_ld_wait_for(v[1]);
+            if (x + 64 < KT) tmem_ld32(s_tmem + x + 64, v[0]);
+            finish(v[1], x + 32);
+            weights(v[1], x + 32);
+            hand_over(KT == 64 || x + 64 == KT ? 1 : 0);
+          }
         }
         l[0] = add_f32x2(l[0], l[1]);
         sum = add_f32x2(sum, l[0]);
+        return true;
+        };
+        ok = edge ? softmax(std::true_type{}) : softmax(std::false_type{});
+        if (!ok) break;
         ++done;
       }
       T += n;
@@ -687,9 +787,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
       }
       if (own) {
         if (!whole)
-          p.part_ml[prow] = make_float2(top, all);
+          p.part_ml[prow] = make_float2(ref, all);
         else if (p.lse != nullptr)
-          p.lse[orow] = none ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+          p.lse[orow] = none ? -INFINITY : (ref + log2f(all)) * 0.6931471805599453f;
       }
       tc_fence_before_sync();
       __syncwarp();
@@ -730,21 +830,26 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             }
             // four 16-byte pieces (64 codes) of eight rows a step; of eight lanes four take
             // row r and four row r ^ 5, which keeps both the raw pieces they read and the
-            // (even or odd) bf16 pieces they write in eight different bank groups
+            // (even or odd) f16 pieces they write in eight different bank groups
             const uint32_t src = sbase + C::kOffRaw + rs * C::kRawTile + src_at, dst = ring + st * C::kTile;
             constexpr int kSteps = KT / 8 * C::kHalves / 4, kBatch = 4;
+            const int live = w.s.kv - j * KT;
 #pragma unroll
             for (int k0 = 0; k0 < kSteps; k0 += kBatch) {
               uint4 v[kBatch];
 #pragma unroll
-              for (int k = 0; k < kBatch; ++k) v[k] = ld_shared_v4(src + (k0 + k) * kStepRows * C::kRawBox);
+              for (int k = 0; k < kBatch; ++k) {
+                v[k] = ld_shared_v4(src + (k0 + k) * kStepRows * C::kRawBox);
+                // rows of V past the sequence may hold e4m3's NaN, which zero weights do not silence
+                if (kv == 1 && row + (k0 + k) * kStepRows >= live) v[k] = make_uint4(0, 0, 0, 0);
+              }
 #pragma unroll
               for (int k = 0; k < kBatch; ++k) {
                 const uint32_t to = dst + (k0 + k) * kStepRows * 128;
-                st_shared_v4(to + dst_at0, make_uint4(codes01_to_bf16x2<C::FMT>(v[k].x), codes23_to_bf16x2<C::FMT>(v[k].x),
-                                                      codes01_to_bf16x2<C::FMT>(v[k].y), codes23_to_bf16x2<C::FMT>(v[k].y)));
-                st_shared_v4(to + dst_at1, make_uint4(codes01_to_bf16x2<C::FMT>(v[k].z), codes23_to_bf16x2<C::FMT>(v[k].z),
-                                                      codes01_to_bf16x2<C::FMT>(v[k].w), codes23_to_bf16x2<C::FMT>(v[k].w)));
+                st_shared_v4(to + dst_at0, make_uint4(codes01_to_f16x2<C::FMT>(v[k].x), codes23_to_f16x2<C::FMT>(v[k].x),
+                                                      codes01_to_f16x2<C::FMT>(v[k].y), codes23_to_f16x2<C::FMT>(v[k].y)));
+                st_shared_v4(to + dst_at1, make_uint4(codes01_to_f16x2<C::FMT>(v[k].z), codes23_to_f16x2<C::FMT>(v[k].z),
+                                                      codes01_to_f16x2<C::FMT>(v[k].w), codes23_to_f16x2<C::FMT>(v[k].w)));
               }
             }
             fence_proxy_async_smem();
