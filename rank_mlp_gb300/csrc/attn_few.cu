@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
         big[h] = max(big[h], __shfl_xor_sync(0xffffffffu, big[h], 2));
         // the row times 2^(14 - exponent of its largest), and the score scale without it
         const float f = __uint_as_float(static_cast<unsigned>(min(254, 268 - static_cast<int>(big[h] >> 7))) << 23);
-        c[h] = scale / f;
+        c[h] = fmaxf(scale / f, 1.17549435e-38f);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
 #pragma unroll

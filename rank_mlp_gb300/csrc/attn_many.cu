@@ -16,14 +16,15 @@
 // the next tile's scores.  An accumulator is rescaled, in tensor memory, only when a row's
 // maximum rises by more than 2^8 (kMaxSlack).
 //
-// 8-bit caches run in f16, which holds both formats' codes exactly: four more warps turn
-// the ring's raw tiles into f16 tiles, once for all the tile's rows (to bf16 it takes up to
-// five instructions for two codes, to f16 one or two, and these conversions set the pace).
-// The softmax warps turn their rows of Q, scaled by a power of two to f16's upper range
-// (exact for features down to 2^-29 of the row's largest).  A position's K scale multiplies
-// its score and its V scale its weight, in f32; weights and sums carry a factor 2^-E, E the
-// exponent of the largest V scale so far, which keeps the f16 products in range (a weight
-// times scale below 2^-24 of that largest scale is lost).
+// 8-bit caches run in f16: four more warps turn the ring's raw tiles into f16 tiles once for
+// all the tile's rows.  K tiles hold the codes, which f16 holds exactly, and a position's K
+// scale multiplies its score in f32.  V tiles hold a code times its row's scale over a power
+// of two 2^eV that brings the tile's largest scale to (1/2, 1], rounded to f16's 11 bits,
+// eight times finer than the bf16 rows that went into the cache; the weights carry 2^(eV -
+// E), E the largest eV so far, and so do the sums (a scale per position in the weights, too,
+// cost a sixth of the time).  The softmax warps turn their rows of Q, scaled by a power of
+// two to f16's upper range (exact for features down to 2^-29 of the row's largest).  What is
+// lost are products below 2^-24 of the largest V scale so far.
 #include <type_traits>
 
 #include "paged_attn.cuh"
@@ -67,7 +68,9 @@ struct ManyCfg {
   // (mixed batch of 24: 141 us against 152 us with four stages and staged rows).
   static constexpr bool kStaged = kRaw || D < 256;
   static constexpr int kOutCols = kRaw && D >= 128 ? 32 : 64;
-  static constexpr int kOffOut = kOffScales + (kRaw ? kScaleSlots * 2 * KT * 4 : 0);
+  // (a slot: the tile's KT K scales, then eV)
+  static constexpr int kSlotBytes = KT * 4 + 16;
+  static constexpr int kOffOut = (kOffScales + (kRaw ? kScaleSlots * kSlotBytes : 0) + 127) & ~127;
   static constexpr int kOffBars = kOffOut + (kStaged ? kSoftWarps * 32 * kOutCols * 2 : 0);
   static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 6 + 5 * NQ + (kRaw ? kScaleSlots + NQ : 0);
   static constexpr int kOffPlan = kOffBars + kNumBars * 8 + 8;
@@ -86,6 +89,12 @@ __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+
+// 2^e of a normal exponent.
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<unsigned>(127 + e) << 23); }
+// The e with 2^(e - 1) <= x < 2^e of a scale's bits, kept where weights and sums over it stay
+// inside f32.
+__device__ __forceinline__ int scale_exponent(unsigned bits) { return max(-90, min(110, static_cast<int>(bits >> 23) - 126)); }
 
 // Row halves of an item that hold rows of the sequence.
 template <class C>
@@ -369,7 +378,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           }
         }
       } else {
-        // the scores of tile t + 1 (the next item's too) are issued before tile t's O += P V
+        // The scores of tile t + 1 are issued before tile t's O += P V.  So are the next item's
+        // first ones with a bf16 cache; with an 8-bit one its Q is turned to f16 by the softmax
+        // warps, which come to it only after this item's last O += P V.
         uint32_t T = 0;                   // tiles so far: score buffer T & 1
         auto next_scores = [&](bool new_item, bool last) {
           if (new_item) {
@@ -395,11 +406,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           const int vst = st;
           const uint32_t vph = ph, buf = (T - 1u) & 1u;
           step(st, ph);
+          bool fresh = false;
           if (++j == w.jb) {
             more = next_item();
             if (more) {
               j = w.ja;
-              ok = next_scores(true, w.ja + 1 == w.jb);
+              fresh = true;
+              if (!C::kRaw) ok = next_scores(true, w.ja + 1 == w.jb);
             }
           } else {
             ok = next_scores(false, j + 1 == w.jb);
@@ -410,6 +423,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           pphase ^= 1u << buf;
           commit(odone_bar(0));
           commit(empty_bar(vst));
+          if (C::kRaw && fresh) ok = next_scores(true, w.ja + 1 == w.jb);
         }
       }
       if (!ok) {
@@ -490,7 +504,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         }
         // the row times 2^(14 - exponent of its largest), and the score scale without it
         const float f = __uint_as_float(static_cast<unsigned>(min(254, 268 - static_cast<int>(big >> 7))) << 23);
-        c = scale / f;
+        c = fmaxf(scale / f, 1.17549435e-38f);
         auto turn2 = [&](uint32_t u) { return pack_f16x2(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xFFFF0000u) * f); };
 #pragma unroll 4
         for (int e = 0; e < D / 8; ++e) {
@@ -511,8 +525,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         const int k0 = (w.ja + i) * KT;
         const uint32_t s_tmem = tmem + lanes + C::kSCol0 + buf * C::kSCols;
         const uint32_t vidx = tile + 2u * i + 1u;
-        const float* ks = nullptr;
-        const float* vs = nullptr;
+        int ev = 0;                               // 8-bit: exponent of the tile's V scales
+        const float* ks = nullptr;                // and its K scales
         ok = attn_wait(sfull_bar(buf), (sphase >> buf) & 1u, abort_flag, p);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         sphase ^= 1u << buf;
@@ -520,8 +534,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           const uint32_t sc = (vidx >> 1) % C::kScaleSlots;
           ok = attn_wait(scale_bar(sc), ((vidx >> 1) / C::kScaleSlots) & 1u, abort_flag, p);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          ks = reinterpret_cast<const float*>(smem + C::kOffScales) + sc * 2 * KT;
-          vs = ks + KT;
+          ks = reinterpret_cast<const float*>(smem + C::kOffScales + sc * C::kSlotBytes);
+          ev = __float_as_int(ks[KT]);
         }
         tc_fence_after_sync();
         const bool edge = k0 < lo_max || k0 + KT > hi_min;
@@ -529,11 +543,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         // the others
         auto softmax = [&](auto at_edge) {
         constexpr bool kEdge = decltype(at_edge)::value;
-        // The row's scores, 32 columns on their way while the 32 before are worked on.  16-bit
-        // caches read them once and hold them in registers; 8-bit ones, whose warps have fewer
-        // registers, read them again for the second pass (holding them spilled, and was slower).
-        constexpr bool kHold = !C::kRaw;
-        uint32_t v[kHold ? KT / 32 : 2][32];
+        // the row's scores, read once and held in registers, 32 columns on their way while the
+        // 32 before are worked on
+        uint32_t v[KT / 32][32];
         // scores of columns [x, x + 32): K scales, mask
         auto finish = [&](uint32_t (&v)[32], int x) {
           if (C::kRaw) {
@@ -562,40 +574,17 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           }
         };
         tmem_ld32(s_tmem, v[0]);
-        if constexpr (kHold) {
 #pragma unroll
-          for (int x = 0; x < KT / 32; ++x) {
-            tmem_ld_wait_for(v[x]);
-            if (x + 1 < KT / 32) tmem_ld32(s_tmem + 32 * (x + 1), v[x + 1]);
-            finish(v[x], 32 * x);
-            maxima(v[x]);
-          }
-        } else {
-#pragma unroll 1
-          for (int x = 0; x < KT; x += 64) {
-            tmem_ld_wait_for(v[0]);
-            tmem_ld32(s_tmem + x + 32, v[1]);
-            finish(v[0], x);
-            maxima(v[0]);
-            tmem_ld_wait_for(v[1]);
-            tmem_ld32(s_tmem + (x + 64 < KT ? x + 64 : 0), v[0]);       // at the end: for the second pass
-            finish(v[1], x + 32);
-            maxima(v[1]);
-          }
+        for (int x = 0; x < KT / 32; ++x) {
+          tmem_ld_wait_for(v[x]);
+          if (x + 1 < KT / 32) tmem_ld32(s_tmem + 32 * (x + 1), v[x + 1]);
+          finish(v[x], 32 * x);
+          maxima(v[x]);
         }
         const float cand = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
-        int larger = exponent;
-        if (C::kRaw) {
-          // exponent of the largest V scale of the tile's positions (a NaN, a broken row's, aside)
-          unsigned big = 0;
-#pragma unroll
-          for (int e = 0; e < KT / 32; ++e) {
-            const unsigned bits = __float_as_uint(vs[32 * e + lane]);
-            if (k0 + 32 * e + lane < w.s.kv && bits < 0x7F800000u) big = max(big, bits);
-          }
-          larger = max(larger, min(110, static_cast<int>(__reduce_max_sync(0xffffffffu, big) >> 23) - 126));
-        }
-        if (__any_sync(0xffffffffu, cand > top + kMaxSlack || larger > exponent)) {
+        const int larger = C::kRaw ? max(exponent, ev) : 0;
+        // (rows that are nobody's hold any numbers: they have no say)
+        if (__any_sync(0xffffffffu, own && (cand > top + kMaxSlack || larger > exponent))) {
           top = fmaxf(top, cand);
           exponent = larger;
           const float next = top + exponent;
@@ -619,7 +608,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             tmem_st_wait();
           }
         }
-        const float base = ref == -INFINITY ? 0.0f : -ref;
+        const float base = ref == -INFINITY ? 0.0f : static_cast<float>(ev) - ref;
         const float2 c2 = make_float2(c, c), ref2 = make_float2(base, base);
         float2 l[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         auto weights = [&](const uint32_t (&v)[32], int x) {
@@ -633,18 +622,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
               y[k].x = exp2_approx(y[k].x);
               y[k].y = exp2_approx(y[k].y);
               l[k] = add_f32x2(l[k], y[k]);
-            }
-            if (C::kRaw) {
-              const float4 f = *reinterpret_cast<const float4*>(vs + x + e);
-              y[0] = mul_f32x2(y[0], make_float2(f.x, f.y));
-              y[1] = mul_f32x2(y[1], make_float2(f.z, f.w));
-              if (kEdge) {                 // a hidden position's scale may be anything
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  if (v[e + 2 * k] == 0xFF800000u) y[k].x = 0.0f;
-                  if (v[e + 2 * k + 1] == 0xFF800000u) y[k].y = 0.0f;
-                }
-              }
             }
             u[e / 2] = C::kRaw ? pack_f16x2(y[0].x, y[0].y) : pack_bf16x2(y[0].x, y[0].y);
             u[e / 2 + 1] = C::kRaw ? pack_f16x2(y[1].x, y[1].y) : pack_bf16x2(y[1].x, y[1].y);
@@ -670,30 +647,21 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           __syncwarp();
           if (lane == 0) mbar_arrive(pready_bar(buf, half));
         };
-        if constexpr (kHold) {
 #pragma unroll
-          for (int x = 0; x < KT / 32; ++x) {
-            weights(v[x], 32 * x);
-            if (x == KT / 64 - 1) hand_over(0);
-            if (x == KT / 32 - 1) hand_over(1);
+        for (int x = 0; x < KT / 32; ++x) {
+          weights(v[x], 32 * x);
+          if (C::NQ == 1 && x == KT / 32 - 1 && i > 0 && i + 1 == n) {
+            // With one half the last scores do not wait for the O += P V before theirs; it has to
+            // be seen done before these weights go out, or the wait for the last one below
+            // could take its phase for the one before.
+            ok = attn_wait(odone_bar(q), (done - 1u) & 1u, abort_flag, p);
+            if (!__all_sync(0xffffffffu, ok)) return false;
           }
-        } else {
-          // (weights of columns [x, x + 32) overwrite scores [x / 2, x / 2 + 16), long read)
-#pragma unroll 1
-          for (int x = 0; x < KT; x += 64) {
-            tmem_ld_wait_for(v[0]);
-            tmem_ld32(s_tmem + x + 32, v[1]);
-            finish(v[0], x);
-            weights(v[0], x);
-            if (KT == 64) hand_over(0);
-            tmem_ld_wait_for(v[1]);
-            if (x + 64 < KT) tmem_ld32(s_tmem + x + 64, v[0]);
-            finish(v[1], x + 32);
-            weights(v[1], x + 32);
-            hand_over(KT == 64 || x + 64 == KT ? 1 : 0);
-          }
+          if (x == KT / 64 - 1) hand_over(0);
+          if (x == KT / 32 - 1) hand_over(1);
         }
         l[0] = add_f32x2(l[0], l[1]);
+        if (C::kRaw) l[0] = mul_f32x2(l[0], make_float2(exp2_int(-ev), exp2_int(-ev)));
         sum = add_f32x2(sum, l[0]);
         return true;
         };
@@ -800,6 +768,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
       if constexpr (C::kSplitRegs) regs_lower<C::kConvRegs>();
       const int cw = warp - 4 - C::kSoftWarps, tid = cw * 32 + lane;
       constexpr int kStepRows = 8 * 4 / C::kHalves;       // rows between a warp's steps
+      constexpr int kSteps = KT / 8 * C::kHalves / 4, kBatch = 4;
+      float vscale[kSteps];
+      int ev = 0;
       const int half = cw % C::kHalves, x = lane & 3, r7 = (lane >> 3) ^ (((lane >> 2) & 1) * 5);
       const int row = cw / C::kHalves * 8 + r7;
       const uint32_t src_at = C::kRawBox == 128
@@ -818,38 +789,60 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             if (ok) ok = attn_wait(empty_bar(st), ((idx / ST) & 1u) ^ 1u, abort_flag, p);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            // scales of position tile idx / 2, both tiles': the slot was last read by the
-            // softmax of kScaleSlots tiles before, whose V tile has left the ring
+            const int live = w.s.kv - j * KT;        // positions of the sequence from the tile's first on
+            const float* scales = reinterpret_cast<const float*>(smem + C::kOffRawScales) + rs * 2 * KT;
             if (kv == 0) {
+              // The K scales and eV (broken rows' NaN aside) for the softmax, and this thread's
+              // rows' V scales.  The slot was last read by the softmax of kScaleSlots tiles
+              // before, whose V tile has left the ring.
               const uint32_t sc = (idx >> 1) % C::kScaleSlots;
-              for (int e = tid; e < 2 * KT; e += 128)
-                reinterpret_cast<float*>(smem + C::kOffScales)[sc * 2 * KT + e] =
-                    reinterpret_cast<const float*>(smem + C::kOffRawScales)[rs * 2 * KT + e];
+              float* slot = reinterpret_cast<float*>(smem + C::kOffScales + sc * C::kSlotBytes);
+              unsigned big = 0;
+#pragma unroll
+              for (int x = 0; x < KT / 32; ++x) {
+                const unsigned bits = __float_as_uint(scales[KT + 32 * x + lane]);
+                if (32 * x + lane < live && bits < 0x7F800000u) big = max(big, bits);
+              }
+              ev = scale_exponent(__reduce_max_sync(0xffffffffu, big));
+              if (tid < KT) slot[tid] = scales[tid];
+              if (tid == 0) slot[KT] = __int_as_float(ev);
               __syncwarp();
               if (lane == 0) mbar_arrive(scale_bar(sc));
+#pragma unroll
+              for (int k = 0; k < kSteps; ++k) vscale[k] = scales[KT + row + k * kStepRows];
             }
+            const float unit = exp2_int(-ev);
             // four 16-byte pieces (64 codes) of eight rows a step; of eight lanes four take
             // row r and four row r ^ 5, which keeps both the raw pieces they read and the
             // (even or odd) f16 pieces they write in eight different bank groups
             const uint32_t src = sbase + C::kOffRaw + rs * C::kRawTile + src_at, dst = ring + st * C::kTile;
-            constexpr int kSteps = KT / 8 * C::kHalves / 4, kBatch = 4;
-            const int live = w.s.kv - j * KT;
 #pragma unroll
             for (int k0 = 0; k0 < kSteps; k0 += kBatch) {
               uint4 v[kBatch];
 #pragma unroll
               for (int k = 0; k < kBatch; ++k) {
                 v[k] = ld_shared_v4(src + (k0 + k) * kStepRows * C::kRawBox);
-                // rows of V past the sequence may hold e4m3's NaN, which zero weights do not silence
-                if (kv == 1 && row + (k0 + k) * kStepRows >= live) v[k] = make_uint4(0, 0, 0, 0);
               }
 #pragma unroll
               for (int k = 0; k < kBatch; ++k) {
                 const uint32_t to = dst + (k0 + k) * kStepRows * 128;
-                st_shared_v4(to + dst_at0, make_uint4(codes01_to_f16x2<C::FMT>(v[k].x), codes23_to_f16x2<C::FMT>(v[k].x),
-                                                      codes01_to_f16x2<C::FMT>(v[k].y), codes23_to_f16x2<C::FMT>(v[k].y)));
-                st_shared_v4(to + dst_at1, make_uint4(codes01_to_f16x2<C::FMT>(v[k].z), codes23_to_f16x2<C::FMT>(v[k].z),
-                                                      codes01_to_f16x2<C::FMT>(v[k].w), codes23_to_f16x2<C::FMT>(v[k].w)));
+                // (rows past the sequence hold anything: a NaN is not silenced by a zero weight)
+                const bool past = row + (k0 + k) * kStepRows >= live;
+                if (past) v[k] = make_uint4(0, 0, 0, 0);
+                // the row's factor as a sum of two f16 numbers, so that a product is rounded once
+                const float f = past ? 0.0f : vscale[k0 + k] * unit;
+                const __half hi = __float2half_rn(f);
+                const __half2 f1 = __half2half2(hi), f0 = __half2half2(__float2half_rn(f - __half2float(hi)));
+                auto two = [&](uint32_t codes) {
+                  if (kv == 0) return codes;
+                  const __half2 x = *reinterpret_cast<const __half2*>(&codes);
+                  const __half2 y = __hfma2(x, f1, __hmul2(x, f0));
+                  return *reinterpret_cast<const uint32_t*>(&y);
+                };
+                st_shared_v4(to + dst_at0, make_uint4(two(codes01_to_f16x2<C::FMT>(v[k].x)), two(codes23_to_f16x2<C::FMT>(v[k].x)),
+                                                      two(codes01_to_f16x2<C::FMT>(v[k].y)), two(codes23_to_f16x2<C::FMT>(v[k].y))));
+                st_shared_v4(to + dst_at1, make_uint4(two(codes01_to_f16x2<C::FMT>(v[k].z)), two(codes23_to_f16x2<C::FMT>(v[k].z)),
+                                                      two(codes01_to_f16x2<C::FMT>(v[k].w)), two(codes23_to_f16x2<C::FMT>(v[k].w))));
               }
             }
             fence_proxy_async_smem();

@@ -383,6 +383,23 @@ def test_ragged_batch_of_everything(lib):
         p.check(out)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("hq,hk,dim,new", [(16, 8, 64, (1, 90)), (16, 8, 128, (1, 90)), (32, 4, 64, (1, 90)),
+                                           (32, 4, 128, (1, 90)), (8, 8, 256, (1, 200)), (16, 2, 256, (1, 40)),
+                                           (16, 8, 128, (1, 3)), (8, 8, 256, (1, 3))])
+def test_many_items_for_each_block(lib, hq, hk, dim, new, fmt):
+    """More (sequence, head, row tile) items than the GPU has blocks, in every kernel: blocks go
+    from one item to the next, with one and with two row halves, whole items and cut ones."""
+    g = torch.Generator().manual_seed(dim + hq)
+    kv = torch.randint(1, 700, (120,), generator=g).tolist()
+    n = torch.randint(new[0], new[1] + 1, (120,), generator=g).tolist()
+    p = Paged(lib, [(min(a, b), b) for a, b in zip(n, kv)], hq, hk, dim, 32, fmt, seed=hq)
+    lse = torch.empty(p.q.shape[:2], device=DEV)
+    out = lib.paged_attention(p.q, p.cache, p.batch, lse=lse)
+    assert lib.poll_status() == 0
+    p.check(out, lse)
+
+
 def test_repeated_calls_and_graph_replays_give_the_same_bits(lib):
     p = Paged(lib, [(1, 3000), (1, 7), (90, 1000)], 8, 2, 128, 64, "int8")
     first = lib.paged_attention(p.q, p.cache, p.batch)
