@@ -383,12 +383,13 @@ typedef struct {
  * p < 0) gets out 0 and lse -inf.  Rows of M that no sequence owns are not written.
  * q is a view (of strides above 0); heads_q is a multiple of the cache's heads, and M * heads_q at most 2^31 - 1.
  * Scores, maxima, sums and the accumulated output are f32; the weights e^(...) are
- * rounded to bf16 before they multiply V (as the matrix units take them), and the
- * result is rounded once.  What lies past kv_len in a page is not looked at, whatever
- * bits it holds; a page outside the cache is read as page 0, and a length past the
- * table or a query range outside M is cut to it, each reported by lora_poll_status
- * (LORA_ERR_DEVICE_INPUT).  With a bf16 cache, an infinity or NaN inside a sequence's
- * own V may also reach its tokens that do not see that position.
+ * rounded to the matrix units' 16 bits before they multiply V (bf16 with a bf16 cache, f16
+ * with an 8-bit one, where the many-row kernel also rounds V, code times scale, to f16's 11
+ * bits), and the result is rounded once.  What lies past kv_len in a page is not looked at,
+ * whatever bits it holds; a page outside the cache is read as page 0, and a length past
+ * the table or a query range outside M is cut to it, each reported by lora_poll_status
+ * (LORA_ERR_DEVICE_INPUT).  An infinity or NaN in a position of a sequence's own V
+ * (kv_len's inside) may also reach tokens of that sequence that do not see the position.
  * ws: lora_paged_attention_workspace_bytes. */
 size_t lora_paged_attention_workspace_bytes(int64_t M, int64_t n_seqs, int heads_q, const lora_kv_cache_t* cache);
 lora_status_t lora_paged_attention(int64_t M, int heads_q, const lora_heads_t* q, const lora_kv_cache_t* cache,
