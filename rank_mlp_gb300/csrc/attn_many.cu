@@ -38,14 +38,16 @@ struct ManyCfg {
   static constexpr bool kRaw = FMT != LORA_KV_BF16;
   static constexpr int R = 128 * NQ;
   static constexpr int KT = D == 256 ? 64 : 128;
-  static constexpr int kItem = 2;                            // an item's own cost, in tiles
+  // An item's own cost, in tiles: measured 1, 2, 3, 4, 6 at 176, 167, 161, 163, 167 us for the
+  // first prefill of 4 x 2048 tokens.
+  static constexpr int kItem = 3;
   static constexpr int kHalves = D / 64;                     // 128-byte columns of a bf16 row
   static constexpr int kTile = KT * D * 2;                   // one bf16 K or V tile
   static constexpr int kQBytes = 128 * D * 2;                // one row half of Q
   static constexpr int kRawRow = D, kRawBox = D < 128 ? D : 128, kRawBoxes = D / kRawBox;
   static constexpr int kRawTile = kRaw ? KT * D : 0;
-  static constexpr int kRawStages = !kRaw ? 0 : D == 128 && NQ == 2 ? 2 : 3;
-  static constexpr int kStages = kRaw ? (D == 64 ? 6 : NQ == 1 && D == 128 ? 4 : 3) : (D == 64 ? 8 : D == 128 ? 4 : 5);
+  static constexpr int kRawStages = kRaw ? 3 : 0;
+  static constexpr int kStages = kRaw ? (D == 64 ? 6 : NQ == 1 && D == 128 ? 4 : 3) : (D == 64 ? 8 : D == 128 && NQ == 1 ? 6 : 5);
   static constexpr int kScaleSlots = (kStages + 2) / 2;      // see the converting warps
   static constexpr int kConvWarps = kRaw ? 4 : 0;
   static constexpr int kSoftWarps = 4 * NQ;
@@ -63,15 +65,9 @@ struct ManyCfg {
   static constexpr int kOffRaw = kOffRing + kStages * kTile;
   static constexpr int kOffRawScales = kOffRaw + kRawStages * kRawTile;
   static constexpr int kOffScales = kOffRawScales + (kRaw ? kRawStages * 2 * KT * 4 : 0);
-  // Output staging: kOutCols bf16 (or half as many f32) columns of a warp's 32 rows.  At
-  // head_dim 256 bf16 tiles leave no room for it, and the fifth ring stage is worth more
-  // (mixed batch of 24: 141 us against 152 us with four stages and staged rows).
-  static constexpr bool kStaged = kRaw || D < 256;
-  static constexpr int kOutCols = kRaw && D >= 128 ? 32 : 64;
   // (a slot: the tile's KT K scales, then eV)
   static constexpr int kSlotBytes = KT * 4 + 16;
-  static constexpr int kOffOut = (kOffScales + (kRaw ? kScaleSlots * kSlotBytes : 0) + 127) & ~127;
-  static constexpr int kOffBars = kOffOut + (kStaged ? kSoftWarps * 32 * kOutCols * 2 : 0);
+  static constexpr int kOffBars = (kOffScales + (kRaw ? kScaleSlots * kSlotBytes : 0) + 127) & ~127;
   static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 6 + 5 * NQ + (kRaw ? kScaleSlots + NQ : 0);
   static constexpr int kOffPlan = kOffBars + kNumBars * 8 + 8;
   static constexpr int kSmem = kOffPlan + static_cast<int>(sizeof(PlanScratch<kThreads>)) + 1024;
@@ -682,75 +678,25 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
       const float inv = none ? 0.0f : 1.0f / all;
       const int orow = own ? (w.s.q0 + tok) * p.hq + head : -1;       // below 2^31
       const long long prow = slot * R + q * 128 + r;
-      if constexpr (C::kStaged) {
-        // Out through shared memory, a warp's own 32 rows at a time: a store instruction then
-        // writes whole lines of a few rows (a row per lane would touch 32 lines and keep the
-        // load/store unit busy four times as long).
-        const uint32_t buf = sbase + C::kOffOut + (warp - 4) * (32 * C::kOutCols * 2);
-        constexpr int kRowBytes = C::kOutCols * 2, kPieces = kRowBytes / 16;    // of the staging
-        auto piece = [&](int row, int e) { return buf + row * kRowBytes + ((e ^ (kPieces == 8 ? row & 7 : (row >> 1) & 3)) << 4); };
-        const int cols = whole ? C::kOutCols : C::kOutCols / 2;
+      // A thread writes its row's whole sectors straight away.  (Rows through shared memory, so
+      // that a store touches whole lines of few rows, write faster; but the room is worth more
+      // as a ring stage: first prefill of 4 x 2048 tokens 150 us against 167 us.)
 #pragma unroll 1
-        for (int x = 0; x < D; x += cols) {
-          uint32_t v[C::kOutCols];
-          __syncwarp();
-          if (C::kOutCols == 32 && !whole)            // 16 columns: never past the accumulator
-            tmem_ld16(o_tmem + x, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
-          else
-            tmem_ld32(o_tmem + x, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-          if (C::kOutCols == 64 && whole) tmem_ld32(o_tmem + x + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[C::kOutCols - 32]));
-          tmem_ld_wait();
-          if (whole) {
+      for (int x = 0; x < D; x += 32) {
+        uint32_t v[32];
+        __syncwarp();
+        tmem_ld32(o_tmem + x, v);
+        tmem_ld_wait();
+        if (!own) continue;
+        if (whole) {
+          uint32_t u[16];
 #pragma unroll
-            for (int e = 0; e < kPieces; ++e) {
-              uint32_t u[4];
+          for (int e = 0; e < 16; ++e)
+            u[e] = none ? 0u : pack_bf16x2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
+          store_row32_bf16(p.out + static_cast<long long>(orow) * D + x, u, 0, 32, out_v8);
+        } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                u[k] = none ? 0u : pack_bf16x2(__uint_as_float(v[8 * e + 2 * k]) * inv, __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
-              st_shared_v4(piece(lane, e), make_uint4(u[0], u[1], u[2], u[3]));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < kPieces; ++e)
-              st_shared_v4(piece(lane, e), make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
-          }
-          __syncwarp();
-          uint4 u[kPieces];
-          int to[kPieces];
-#pragma unroll
-          for (int i = 0; i < kPieces; ++i) {
-            const int row = (i * 32 + lane) / kPieces;
-            to[i] = __shfl_sync(0xffffffffu, orow, row);
-            u[i] = ld_shared_v4(piece(row, lane % kPieces));
-          }
-#pragma unroll
-          for (int i = 0; i < kPieces; ++i) {
-            const int row = (i * 32 + lane) / kPieces, e = lane % kPieces;
-            if (to[i] < 0) continue;
-            if (whole)
-              *reinterpret_cast<uint4*>(p.out + static_cast<long long>(to[i]) * D + x + 8 * e) = u[i];
-            else
-              *reinterpret_cast<uint4*>(p.part_o + (slot * R + q * 128 + quarter * 32 + row) * D + x + 4 * e) = u[i];
-          }
-        }
-      } else {
-#pragma unroll 1
-        for (int x = 0; x < D; x += 32) {
-          uint32_t v[32];
-          __syncwarp();
-          tmem_ld32(o_tmem + x, v);
-          tmem_ld_wait();
-          if (!own) continue;
-          if (whole) {
-            uint32_t u[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              u[e] = none ? 0u : pack_bf16x2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
-            store_row32_bf16(p.out + static_cast<long long>(orow) * D + x, u, 0, 32, out_v8);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) st_global_v8(p.part_o + prow * D + x + e, v + e);
-          }
+          for (int e = 0; e < 32; e += 8) st_global_v8(p.part_o + prow * D + x + e, v + e);
         }
       }
       if (own) {
