@@ -65,8 +65,8 @@ struct ManyCfg {
   static constexpr int kOffRaw = kOffRing + kStages * kTile;
   static constexpr int kOffRawScales = kOffRaw + kRawStages * kRawTile;
   static constexpr int kOffScales = kOffRawScales + (kRaw ? kRawStages * 2 * KT * 4 : 0);
-  // (a slot: the tile's KT K scales, then eV)
-  static constexpr int kSlotBytes = KT * 4 + 16;
+  // (a slot: the tile's KT K scales, eV, the V scales)
+  static constexpr int kSlotBytes = 2 * KT * 4 + 16;
   static constexpr int kOffBars = (kOffScales + (kRaw ? kScaleSlots * kSlotBytes : 0) + 127) & ~127;
   static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 6 + 5 * NQ + (kRaw ? kScaleSlots + NQ : 0);
   static constexpr int kOffPlan = kOffBars + kNumBars * 8 + 8;
@@ -715,8 +715,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
       const int cw = warp - 4 - C::kSoftWarps, tid = cw * 32 + lane;
       constexpr int kStepRows = 8 * 4 / C::kHalves;       // rows between a warp's steps
       constexpr int kSteps = KT / 8 * C::kHalves / 4, kBatch = 4;
-      float vscale[kSteps];
-      int ev = 0;
       const int half = cw % C::kHalves, x = lane & 3, r7 = (lane >> 3) ^ (((lane >> 2) & 1) * 5);
       const int row = cw / C::kHalves * 8 + r7;
       const uint32_t src_at = C::kRawBox == 128
@@ -736,60 +734,74 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const int live = w.s.kv - j * KT;        // positions of the sequence from the tile's first on
-            const float* scales = reinterpret_cast<const float*>(smem + C::kOffRawScales) + rs * 2 * KT;
+            const uint32_t sc = (idx >> 1) % C::kScaleSlots;
+            float* slot = reinterpret_cast<float*>(smem + C::kOffScales + sc * C::kSlotBytes);
+            // four 16-byte pieces (64 codes) of eight rows a step; of eight lanes four take
+            // row r and four row r ^ 5, which keeps both the raw pieces they read and the
+            // (even or odd) f16 pieces they write in eight different bank groups
+            const uint32_t src = sbase + C::kOffRaw + rs * C::kRawTile + src_at, dst = ring + st * C::kTile;
+            // Compiled apart for K, which is the codes alone, and V; the loop stays rolled, for
+            // the softmax warps need the instruction cache (512 new tokens over fp8 caches 302
+            // us; one unrolled piece of code for both 341 us, unrolled and apart 316 us).
+            auto convert = [&](auto v_tile) {
+              constexpr bool kV = decltype(v_tile)::value;
+              const float unit = kV ? exp2_int(-__float_as_int(slot[KT])) : 1.0f;
+#pragma unroll 1
+              for (int k0 = 0; k0 < kSteps; k0 += kBatch) {
+                uint4 v[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) v[k] = ld_shared_v4(src + (k0 + k) * kStepRows * C::kRawBox);
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                  const uint32_t to = dst + (k0 + k) * kStepRows * 128;
+                  __half2 f1, f0;
+                  if constexpr (kV) {
+                    // (rows past the sequence hold anything: a NaN is not silenced by a zero weight)
+                    const int r = row + (k0 + k) * kStepRows;
+                    if (r >= live) v[k] = make_uint4(0, 0, 0, 0);
+                    // the row's factor as a sum of two f16 numbers, so that a product is rounded once
+                    const float f = r >= live ? 0.0f : slot[KT + 4 + r] * unit;
+                    const __half hi = __float2half_rn(f);
+                    f1 = __half2half2(hi), f0 = __half2half2(__float2half_rn(f - __half2float(hi)));
+                  }
+                  auto two = [&](uint32_t codes) {
+                    if constexpr (!kV) return codes;
+                    const __half2 x = *reinterpret_cast<const __half2*>(&codes);
+                    const __half2 y = __hfma2(x, f1, __hmul2(x, f0));
+                    return *reinterpret_cast<const uint32_t*>(&y);
+                  };
+                  st_shared_v4(to + dst_at0, make_uint4(two(codes01_to_f16x2<C::FMT>(v[k].x)), two(codes23_to_f16x2<C::FMT>(v[k].x)),
+                                                        two(codes01_to_f16x2<C::FMT>(v[k].y)), two(codes23_to_f16x2<C::FMT>(v[k].y))));
+                  st_shared_v4(to + dst_at1, make_uint4(two(codes01_to_f16x2<C::FMT>(v[k].z)), two(codes23_to_f16x2<C::FMT>(v[k].z)),
+                                                        two(codes01_to_f16x2<C::FMT>(v[k].w)), two(codes23_to_f16x2<C::FMT>(v[k].w))));
+                }
+              }
+            };
             if (kv == 0) {
-              // The K scales and eV (broken rows' NaN aside) for the softmax, and this thread's
-              // rows' V scales.  The slot was last read by the softmax of kScaleSlots tiles
-              // before, whose V tile has left the ring.
-              const uint32_t sc = (idx >> 1) % C::kScaleSlots;
-              float* slot = reinterpret_cast<float*>(smem + C::kOffScales + sc * C::kSlotBytes);
+              // The tile's scales and eV (broken rows' NaN aside) into its slot, which was last
+              // read for the tile kScaleSlots before, whose V tile has left the ring.
+              const float* scales = reinterpret_cast<const float*>(smem + C::kOffRawScales) + rs * 2 * KT;
               unsigned big = 0;
 #pragma unroll
               for (int x = 0; x < KT / 32; ++x) {
                 const unsigned bits = __float_as_uint(scales[KT + 32 * x + lane]);
                 if (32 * x + lane < live && bits < 0x7F800000u) big = max(big, bits);
               }
-              ev = scale_exponent(__reduce_max_sync(0xffffffffu, big));
-              if (tid < KT) slot[tid] = scales[tid];
-              if (tid == 0) slot[KT] = __int_as_float(ev);
+              if (tid < KT) {
+                slot[tid] = scales[tid];
+                slot[KT + 4 + tid] = scales[KT + tid];
+              }
+              big = __reduce_max_sync(0xffffffffu, big);
+              if (tid == 0) slot[KT] = __int_as_float(scale_exponent(big));
               __syncwarp();
               if (lane == 0) mbar_arrive(scale_bar(sc));
-#pragma unroll
-              for (int k = 0; k < kSteps; ++k) vscale[k] = scales[KT + row + k * kStepRows];
-            }
-            const float unit = exp2_int(-ev);
-            // four 16-byte pieces (64 codes) of eight rows a step; of eight lanes four take
-            // row r and four row r ^ 5, which keeps both the raw pieces they read and the
-            // (even or odd) f16 pieces they write in eight different bank groups
-            const uint32_t src = sbase + C::kOffRaw + rs * C::kRawTile + src_at, dst = ring + st * C::kTile;
-#pragma unroll
-            for (int k0 = 0; k0 < kSteps; k0 += kBatch) {
-              uint4 v[kBatch];
-#pragma unroll
-              for (int k = 0; k < kBatch; ++k) {
-                v[k] = ld_shared_v4(src + (k0 + k) * kStepRows * C::kRawBox);
-              }
-#pragma unroll
-              for (int k = 0; k < kBatch; ++k) {
-                const uint32_t to = dst + (k0 + k) * kStepRows * 128;
-                // (rows past the sequence hold anything: a NaN is not silenced by a zero weight)
-                const bool past = row + (k0 + k) * kStepRows >= live;
-                if (past) v[k] = make_uint4(0, 0, 0, 0);
-                // the row's factor as a sum of two f16 numbers, so that a product is rounded once
-                const float f = past ? 0.0f : vscale[k0 + k] * unit;
-                const __half hi = __float2half_rn(f);
-                const __half2 f1 = __half2half2(hi), f0 = __half2half2(__float2half_rn(f - __half2float(hi)));
-                auto two = [&](uint32_t codes) {
-                  if (kv == 0) return codes;
-                  const __half2 x = *reinterpret_cast<const __half2*>(&codes);
-                  const __half2 y = __hfma2(x, f1, __hmul2(x, f0));
-                  return *reinterpret_cast<const uint32_t*>(&y);
-                };
-                st_shared_v4(to + dst_at0, make_uint4(two(codes01_to_f16x2<C::FMT>(v[k].x)), two(codes23_to_f16x2<C::FMT>(v[k].x)),
-                                                      two(codes01_to_f16x2<C::FMT>(v[k].y)), two(codes23_to_f16x2<C::FMT>(v[k].y))));
-                st_shared_v4(to + dst_at1, make_uint4(two(codes01_to_f16x2<C::FMT>(v[k].z)), two(codes23_to_f16x2<C::FMT>(v[k].z)),
-                                                      two(codes01_to_f16x2<C::FMT>(v[k].w)), two(codes23_to_f16x2<C::FMT>(v[k].w))));
-              }
+              convert(std::false_type{});
+            } else {
+              // (the slot is whole: other warps wrote parts of it)
+              ok = attn_wait(scale_bar(sc), ((idx >> 1) / C::kScaleSlots) & 1u, abort_flag, p);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              convert(std::true_type{});
             }
             fence_proxy_async_smem();
             __syncwarp();
