@@ -6,10 +6,12 @@
 // A CTA: one producer warp fills a ring of K/V tiles of 64 or 128 positions by TMA (128- or
 // 64-byte swizzle, one box per page), four warps take a quarter of each tile's positions
 // and keep a running maximum, sum and output of their own in registers, merged when the
-// item's part ends.
+// item's part ends.  Measured: one token of four sequences of 50,000 to 65,536 positions, 8
+// cache heads of 128 features: 948 MB in 148 us (6.4 TB/s, 94% of a copy's rate).
 //
 // 8-bit caches run in f16, which holds both formats' codes exactly and to which they turn
-// in fewer instructions than to bf16 (the conversions, not memory, set the pace).  A row of
+// in fewer instructions than to bf16 (the conversions, not memory, set the pace: 64
+// sequences of 200 to 8192 int8 positions, 569 MB in 131 us, 4.3 TB/s).  A row of
 // Q is scaled by a power of two to f16's upper range (exact for features down to 2^-29 of
 // the row's largest).  A position's K scale multiplies its score in f32; its V scale joins
 // the weight as an exponent, 2^(s + log2 vs - m'), with a running maximum m' of its own, so

@@ -6,7 +6,9 @@
 // and head_dim 256, where the output alone fills half of the tensor memory.
 //   S = Q K^T        operands in shared memory, S in tensor memory (two buffers)
 //   P = 2^(c S - m)  one thread per row: maximum, exponential and sum without a shuffle;
-//                    P replaces S in place as packed bf16
+//                    P replaces S in place, packed as bf16: each weight is rounded by at
+//                    most 2^-9 of itself, as an output is, and the sum that divides them is
+//                    the sum of the f32 weights
 //   O += P V         P from tensor memory, V from shared memory as it lies (MN-major)
 // Roles: warp 0 fills a ring of K and V tiles by TMA (one box per page); warp 1 (and, with
 // two halves, warp 2) issues the MMAs; warp 3 brings the next item's Q as soon as the last
@@ -15,6 +17,14 @@
 // half, so that one lane's barrier work hides behind the other's MMAs); with one half, on
 // the next tile's scores.  An accumulator is rescaled, in tensor memory, only when a row's
 // maximum rises by more than 2^8 (kMaxSlack).
+//
+// Bound by the tensor cores and, as much, by the softmax's instructions (an exponential, a
+// maximum, two multiply-adds and half a conversion a score), which is why a row's scores stay
+// in registers and rows need no shuffles.  Measured: a first prefill of 4 x 2048 tokens, 32
+// query heads over 8 cache heads of 128 features, bf16: 145 us, 950 TFLOP/s of products
+// needed (half of cuBLAS's rate); 512 new tokens of two sequences after 16,000: 198 us with a
+// bf16 cache (1340 TFLOP/s, 70%), 302 us with fp8, where the ring has room for three
+// converted tiles and converting sets the pace.
 //
 // 8-bit caches run in f16: four more warps turn the ring's raw tiles into f16 tiles once for
 // all the tile's rows.  K tiles hold the codes, which f16 holds exactly, and a position's K

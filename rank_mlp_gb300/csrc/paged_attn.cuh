@@ -6,11 +6,12 @@
 // takes, all of them unless they outnumber its rows), as many whole tokens as a tile's
 // rows hold.  An item is (sequence, slice, tile of tt tokens); it has one unit for every KT
 // positions that its rows see (one where they see none) and IT units before them, for what
-// an item costs beside its tiles (Q, merging, the output).  The lengths are known on the device only, so every
-// CTA counts all units itself and takes an equal, contiguous share of them: long and
-// short sequences, causal tiles and few-row batches fill the GPU alike.  An item that a
-// share boundary cuts leaves its parts' maxima, sums and unnormalised outputs in the
-// workspace, at most two of them per CTA, and a second launch joins them in a fixed order.
+// an item costs beside its tiles (Q, merging, the output).  The lengths are known on the
+// device only, so every CTA counts all units itself and takes an equal, contiguous share of
+// them: long and short sequences, causal tiles and few-row batches fill the GPU alike.  An
+// item that a share boundary cuts leaves its parts' maxima, sums and unnormalised outputs in
+// the workspace, at most two of them per CTA, and a second launch joins them in a fixed
+// order.
 #pragma once
 
 #include "serve.cuh"
