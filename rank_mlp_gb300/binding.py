@@ -636,7 +636,8 @@ def kv_cache(n_pages: int, page_size: int, heads: int, head_dim: int, format: st
     dev = torch.device(device)
     k, v = (torch.zeros(n_pages, heads, page_size, head_dim, dtype=torch.uint8 if format != "bf16" else torch.bfloat16,
                         device=dev).view(KV_DTYPE[format]) for _ in range(2))
-    scales = (None, None) if format == "bf16" else         tuple(torch.zeros(n_pages, heads, page_size, dtype=torch.float32, device=dev) for _ in range(2))
+    scales = [None if format == "bf16" else torch.zeros(n_pages, heads, page_size, dtype=torch.float32, device=dev)
+              for _ in range(2)]
     return KVCache(k, v, *scales)
 
 
