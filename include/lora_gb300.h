@@ -381,11 +381,13 @@ typedef struct {
  * out bf16 [M x heads_q x head_dim], dense (the O projection's input); lse f32 [M x
  * heads_q] or NULL receives ln sum_j e^(s_j).  A token that sees nothing (kv_len 0, or
  * p < 0) gets out 0 and lse -inf.  Rows of M that no sequence owns are not written.
- * q is a view (of strides above 0); heads_q is a multiple of the cache's heads, and M * heads_q at most 2^31 - 1.
+ * q is a view (of strides above 0); heads_q is a multiple of the cache's heads, and
+ * M * heads_q at most 2^31 - 1.
  * Scores, maxima, sums and the accumulated output are f32; the weights e^(...) are
  * rounded to the matrix units' 16 bits before they multiply V (bf16 with a bf16 cache, f16
  * with an 8-bit one, where the many-row kernel also rounds V, code times scale, to f16's 11
- * bits), and the result is rounded once.  What lies past kv_len in a page is not looked at,
+ * bits; f16 weights below 2^-14 of a row's largest are rounded to 2^-24 of it), and the result
+ * is rounded once.  What lies past kv_len in a page is not looked at,
  * whatever bits it holds; a page outside the cache is read as page 0, and a length past
  * the table or a query range outside M is cut to it, each reported by lora_poll_status
  * (LORA_ERR_DEVICE_INPUT).  An infinity or NaN in a position of a sequence's own V

@@ -3,8 +3,8 @@
 // bounds it; the products run on the warp-level matrix units (m16n8k16), whose 16 rows
 // these few rows fill, straight from the tiles in shared memory.
 //
-// A CTA: one producer warp fills a ring of K/V tiles of 64 or 128 positions by TMA (128- or
-// 64-byte swizzle, one box per page), four warps take a quarter of each tile's positions
+// A CTA: one producer warp fills a ring of K/V tiles of 64 positions by TMA (128- or 64-byte
+// swizzle, one box per page), four warps take a quarter of each tile's positions
 // and keep a running maximum, sum and output of their own in registers, merged when the
 // item's part ends.  Measured: one token of four sequences of 50,000 to 65,536 positions, 8
 // cache heads of 128 features: 948 MB in 148 us (6.4 TB/s, 94% of a copy's rate).
@@ -38,7 +38,9 @@ struct FewCfg {
   static constexpr int kGroups = kKT / 64;                    // of 16 positions, per warp and tile
   static constexpr int kTile = kKT * kRow;
   static constexpr int kStage = 2 * kTile;
-  // D = 256 needs the registers of a whole SM for 160 threads; otherwise two CTAs share one
+  // CTAs of an SM, 160 threads each: D = 256 needs the registers of one alone.  Two and three
+  // took 171 and 201 us (bf16; shorter rings), 141 and 132 us (int8), 150 and 149 us (fp8) for
+  // 64 sequences of 200 to 8192 positions with 128 features.
   static constexpr int kCtas = D == 256 ? 1 : D == 128 && FMT == LORA_KV_BF16 ? 2 : 3;
   static constexpr int kStagesFit = (kCtas == 1 ? 192 * 1024 : kCtas == 2 ? 96 * 1024 : 62 * 1024) / kStage;
   static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;

@@ -54,7 +54,7 @@ struct ManyCfg {
   static constexpr int kHalves = D / 64;                     // 128-byte columns of a bf16 row
   static constexpr int kTile = KT * D * 2;                   // one bf16 K or V tile
   static constexpr int kQBytes = 128 * D * 2;                // one row half of Q
-  static constexpr int kRawRow = D, kRawBox = D < 128 ? D : 128, kRawBoxes = D / kRawBox;
+  static constexpr int kRawBox = D < 128 ? D : 128, kRawBoxes = D / kRawBox;
   static constexpr int kRawTile = kRaw ? KT * D : 0;
   static constexpr int kRawStages = kRaw ? 3 : 0;
   static constexpr int kStages = kRaw ? (D == 64 ? 6 : NQ == 1 && D == 128 ? 4 : 3) : (D == 64 ? 8 : D == 128 && NQ == 1 ? 6 : 5);
