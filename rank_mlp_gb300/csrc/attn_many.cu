@@ -7,7 +7,7 @@
 //   S = Q K^T        operands in shared memory, S in tensor memory (two buffers)
 //   P = 2^(c S - m)  one thread per row: maximum, exponential and sum without a shuffle;
 //                    P replaces S in place, packed as bf16: each weight is rounded by at
-//                    most 2^-9 of itself, as an output is, and the sum that divides them is
+//                    most 2^-8 of itself, as an output is, and the sum that divides them is
 //                    the sum of the f32 weights
 //   O += P V         P from tensor memory, V from shared memory as it lies (MN-major)
 // Roles: warp 0 fills a ring of K and V tiles by TMA (one box per page); warp 1 (and, with
