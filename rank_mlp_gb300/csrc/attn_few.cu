@@ -387,12 +387,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
       if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
     }
     if (k8) {
-      // the outputs back to the scores' maximum
+      // the outputs back to the scores' maximum (in two factors: 2^(vtop - top) may leave f32's
+      // range where the product does not)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float f = vtop[h] == -INFINITY ? 0.0f : exp2_approx(vtop[h] - top[h]);
+        const float f = vtop[h] == -INFINITY ? 0.0f : exp2_approx(0.5f * (vtop[h] - top[h]));
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
+        for (int n = 0; n < D / 8; ++n) o[n][2 * h] = o[n][2 * h] * f * f, o[n][2 * h + 1] = o[n][2 * h + 1] * f * f;
       }
     }
 

@@ -28,13 +28,21 @@
 //
 // 8-bit caches run in f16: four more warps turn the ring's raw tiles into f16 tiles once for
 // all the tile's rows.  K tiles hold the codes, which f16 holds exactly, and a position's K
-// scale multiplies its score in f32.  V tiles hold a code times its row's scale over a power
-// of two 2^eV that brings the tile's largest scale to (1/2, 1], rounded to f16's 11 bits,
-// eight times finer than the bf16 rows that went into the cache; the weights carry 2^(eV -
-// E), E the largest eV so far, and so do the sums (a scale per position in the weights, too,
-// cost a sixth of the time).  The softmax warps turn their rows of Q, scaled by a power of
-// two to f16's upper range (exact for features down to 2^-29 of the row's largest).  What is
-// lost are products below 2^-24 of the largest V scale so far.
+// scale multiplies its score in f32.  V tiles come in two kinds, told apart by the tile's
+// largest and smallest V scale:
+//   alike (within 2^6, nearly every tile)  a code times its row's scale over a power of two
+//          2^eV that brings the largest scale to (1/2, 1], rounded to f16's 11 bits, eight
+//          times finer than the bf16 rows that went into the cache; the weights are
+//          2^(s + eV - r)
+//   apart  the codes alone, exactly; a position's scale joins its weight as an exponent,
+//          2^(s + log2 vs - r) (taken for every tile, this cost a sixth of the time)
+// r is a row's own reference: the running maximum of s + eV (s + log2 vs) over what the row
+// sees, so that neither a position of little weight nor a hidden one moves the other
+// positions' weights out of f16's range, whatever the scales are.  It stands kBoost powers
+// of two below the top of f16: a weight is rounded by 2^-11 of itself or, with the 2^6
+// above, 2^-25 of the row's largest weight times scale.  The sums are relative to the scores'
+// own maximum.  The softmax warps turn their rows of Q, scaled by a power of two to f16's
+// upper range (exact for features down to 2^-29 of the row's largest).
 #include <type_traits>
 
 #include "paged_attn.cuh"
@@ -75,7 +83,7 @@ struct ManyCfg {
   static constexpr int kOffRaw = kOffRing + kStages * kTile;
   static constexpr int kOffRawScales = kOffRaw + kRawStages * kRawTile;
   static constexpr int kOffScales = kOffRawScales + (kRaw ? kRawStages * 2 * KT * 4 : 0);
-  // (a slot: the tile's KT K scales, eV, the V scales)
+  // (a slot: the tile's KT K scales, eV, whether the V scales are apart, the V scales)
   static constexpr int kSlotBytes = 2 * KT * 4 + 16;
   static constexpr int kOffBars = (kOffScales + (kRaw ? kScaleSlots * kSlotBytes : 0) + 127) & ~127;
   static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 6 + 5 * NQ + (kRaw ? kScaleSlots + NQ : 0);
@@ -98,9 +106,15 @@ __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
 
 // 2^e of a normal exponent.
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<unsigned>(127 + e) << 23); }
-// The e with 2^(e - 1) <= x < 2^e of a scale's bits, kept where weights and sums over it stay
-// inside f32.
-__device__ __forceinline__ int scale_exponent(unsigned bits) { return max(-90, min(110, static_cast<int>(bits >> 23) - 126)); }
+// A tile's V scales, from the bits of the smallest and the largest: alike if the largest is at
+// most 2^6 times the smallest, finite and below 2^126 (a NaN's bits are above every number's;
+// no position at all: 0 and ~0).  eV of a largest scale: 2^(eV - 1) <= x < 2^eV (subnormal
+// ones less).
+__device__ __forceinline__ bool scales_alike(unsigned small, unsigned big) {
+  return big < 0x7E800000u && (big == 0 || small + (6u << 23) >= big);
+}
+__device__ __forceinline__ int scale_exponent(unsigned bits) { return max(-125, static_cast<int>(bits >> 23) - 126); }
+constexpr float kBoost = 7.0f;       // f16 weights are at most 2^(kBoost + kMaxSlack) = 2^15
 
 // Row halves of an item that hold rows of the sequence.
 template <class C>
@@ -521,18 +535,19 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         __syncwarp();
         if (lane == 0) mbar_arrive(qready_bar(q));
       }
-      // top: the row's running maximum (scaled, log2); ref = top + exponent: what weights and
-      // sums are relative to
-      float top = -INFINITY, ref = -INFINITY;
-      int exponent = C::kRaw ? -90 : 0;
+      // top: the row's running maximum (scaled, log2), which the sums are relative to; ref: what
+      // the weights are relative to (8-bit: the maximum with the V scales; bf16: top itself)
+      float top = -INFINITY, vtop = -INFINITY;
+      float& ref = C::kRaw ? vtop : top;
       float2 sum = make_float2(0.0f, 0.0f);          // two partial sums
       for (int i = 0; i < n; ++i) {
         const uint32_t buf = C::NQ == 2 ? q : (T + i) & 1u;
         const int k0 = (w.ja + i) * KT;
         const uint32_t s_tmem = tmem + lanes + C::kSCol0 + buf * C::kSCols;
         const uint32_t vidx = tile + 2u * i + 1u;
-        int ev = 0;                               // 8-bit: exponent of the tile's V scales
-        const float* ks = nullptr;                // and its K scales
+        int ev = 0;                               // 8-bit: exponent of the tile's V scales,
+        bool apart = false;                       // whether they differ too much for one,
+        const float* ks = nullptr;                // and the tile's K scales
         ok = attn_wait(sfull_bar(buf), (sphase >> buf) & 1u, abort_flag, p);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         sphase ^= 1u << buf;
@@ -542,13 +557,16 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           ks = reinterpret_cast<const float*>(smem + C::kOffScales + sc * C::kSlotBytes);
           ev = __float_as_int(ks[KT]);
+          apart = __float_as_int(ks[KT + 1]) != 0;
         }
         tc_fence_after_sync();
         const bool edge = k0 < lo_max || k0 + KT > hi_min;
-        // compiled twice: for tiles that all of the warp's rows see whole (nearly all), and for
-        // the others
-        auto softmax = [&](auto at_edge) {
-        constexpr bool kEdge = decltype(at_edge)::value;
+        // compiled for tiles that all of the warp's rows see whole (nearly all), for the others,
+        // and for an exponent per position
+        auto softmax = [&](auto at_edge, auto each_exponent) {
+        constexpr bool kEdge = decltype(at_edge)::value, kEach = decltype(each_exponent)::value;
+        // log2 of the scale that position e's weight carries
+        auto exponent_of = [&](int e) { return apart ? log2_approx(ks[KT + 4 + e]) : static_cast<float>(ev); };
         // the row's scores, read once and held in registers, 32 columns on their way while the
         // 32 before are worked on
         uint32_t v[KT / 32][32];
@@ -570,7 +588,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             for (int e = 0; e < 32; ++e) v[e] = key + e >= lo && key + e < hi ? v[e] : 0xFF800000u;   // -inf
           }
         };
-        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, vmost = -INFINITY;
         auto maxima = [&](const uint32_t (&v)[32]) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
@@ -586,18 +604,22 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           if (x + 1 < KT / 32) tmem_ld32(s_tmem + 32 * (x + 1), v[x + 1]);
           finish(v[x], 32 * x);
           maxima(v[x]);
+          if (kEach) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) vmost = fmaxf(vmost, fmaf(__uint_as_float(v[x][e]), c, exponent_of(32 * x + e)));
+          }
         }
         const float cand = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
-        const int larger = C::kRaw ? max(exponent, ev) : 0;
+        const float vcand = kEach ? vmost : C::kRaw ? cand + ev : cand;
         // (rows that are nobody's hold any numbers: they have no say)
-        if (__any_sync(0xffffffffu, own && (cand > top + kMaxSlack || larger > exponent))) {
-          top = fmaxf(top, cand);
-          exponent = larger;
-          const float next = top + exponent;
-          const float f = next == -INFINITY ? 1.0f : exp2_approx(ref - next);
-          ref = next;
-          sum.x *= f;
-          sum.y *= f;
+        if (__any_sync(0xffffffffu, own && (cand > top + kMaxSlack || (C::kRaw && vcand > ref + kMaxSlack)))) {
+          const float next = fmaxf(top, cand), vnext = C::kRaw ? fmaxf(ref, vcand) : next;
+          const float f = vnext == -INFINITY ? 1.0f : exp2_approx(ref - vnext);
+          const float fs = !C::kRaw ? f : next == -INFINITY ? 1.0f : exp2_approx(top - next);
+          ref = vnext;
+          top = next;
+          sum.x *= fs;
+          sum.y *= fs;
           if (i > 0) {
             ok = attn_wait(odone_bar(q), (done - 1u) & 1u, abort_flag, p);
             if (!__all_sync(0xffffffffu, ok)) return false;
@@ -614,7 +636,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             tmem_st_wait();
           }
         }
-        const float base = ref == -INFINITY ? 0.0f : static_cast<float>(ev) - ref;
+        const float base = ref == -INFINITY ? 0.0f : C::kRaw ? (kEach ? kBoost : kBoost + ev) - ref : -ref;
+        const float seen = top == -INFINITY ? 0.0f : -top;
         const float2 c2 = make_float2(c, c), ref2 = make_float2(base, base);
         float2 l[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         auto weights = [&](const uint32_t (&v)[32], int x) {
@@ -624,6 +647,18 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             float2 y[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+              if (kEach) {
+                float z[2];
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                  const float s = __uint_as_float(v[e + 2 * k + d]);
+                  z[d] = exp2_approx(fmaf(s, c, seen));
+                  // (a hidden position's scale, which may be a NaN, is not looked at)
+                  (d ? y[k].y : y[k].x) = s == -INFINITY ? 0.0f : exp2_approx(fmaf(s, c, exponent_of(x + e + 2 * k + d) + base));
+                }
+                l[k] = add_f32x2(l[k], make_float2(z[0], z[1]));
+                continue;
+              }
               y[k] = fma_f32x2(make_float2(__uint_as_float(v[e + 2 * k]), __uint_as_float(v[e + 2 * k + 1])), c2, ref2);
               y[k].x = exp2_approx(y[k].x);
               y[k].y = exp2_approx(y[k].y);
@@ -667,11 +702,23 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           if (x == KT / 32 - 1) hand_over(1);
         }
         l[0] = add_f32x2(l[0], l[1]);
-        if (C::kRaw) l[0] = mul_f32x2(l[0], make_float2(exp2_int(-ev), exp2_int(-ev)));
+        if (C::kRaw && !kEach && top != -INFINITY) {     // from the weights' reference to the sums'
+          const float f = exp2_approx(-base - top);
+          l[0] = mul_f32x2(l[0], make_float2(f, f));
+        }
         sum = add_f32x2(sum, l[0]);
         return true;
         };
-        ok = edge ? softmax(std::true_type{}) : softmax(std::false_type{});
+        if constexpr (C::kRaw) {
+          // An exponent per position also where a row's reference is so far above this tile's
+          // scale that its weights, of which the sum takes part, could leave f32's range.
+          if (__any_sync(0xffffffffu, apart || (own && top + ev < ref - 90.0f)))
+            ok = softmax(std::true_type{}, std::true_type{});
+          else
+            ok = edge ? softmax(std::true_type{}, std::false_type{}) : softmax(std::false_type{}, std::false_type{});
+        } else {
+          ok = edge ? softmax(std::true_type{}, std::false_type{}) : softmax(std::false_type{}, std::false_type{});
+        }
         if (!ok) break;
         ++done;
       }
@@ -686,6 +733,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
       const float all = sum.x + sum.y;
       const bool none = top == -INFINITY && all == 0.0f;
       const float inv = none ? 0.0f : 1.0f / all;
+      // 8-bit: the output from the weights' reference to the sums', 2^(ref - top - kBoost), in two
+      // factors, which stay in f32's range together with what they multiply
+      const float back = !C::kRaw ? 1.0f : ref == -INFINITY ? 0.0f : exp2_approx(0.5f * (ref - top - kBoost));
       const int orow = own ? (w.s.q0 + tok) * p.hq + head : -1;       // below 2^31
       const long long prow = slot * R + q * 128 + r;
       // A thread writes its row's whole sectors straight away.  (Rows through shared memory, so
@@ -698,11 +748,17 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         tmem_ld32(o_tmem + x, v);
         tmem_ld_wait();
         if (!own) continue;
+        if (C::kRaw) {
+          const float first = whole ? inv * back : back;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * first * back);
+        }
         if (whole) {
           uint32_t u[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            u[e] = none ? 0u : pack_bf16x2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
+            u[e] = none ? 0u : C::kRaw ? pack_bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]))
+                                       : pack_bf16x2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
           store_row32_bf16(p.out + static_cast<long long>(orow) * D + x, u, 0, 32, out_v8);
         } else {
 #pragma unroll
@@ -711,9 +767,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
       }
       if (own) {
         if (!whole)
-          p.part_ml[prow] = make_float2(ref, all);
+          p.part_ml[prow] = make_float2(top, all);
         else if (p.lse != nullptr)
-          p.lse[orow] = none ? -INFINITY : (ref + log2f(all)) * 0.6931471805599453f;
+          p.lse[orow] = none ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
       }
       tc_fence_before_sync();
       __syncwarp();
@@ -756,6 +812,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             auto convert = [&](auto v_tile) {
               constexpr bool kV = decltype(v_tile)::value;
               const float unit = kV ? exp2_int(-__float_as_int(slot[KT])) : 1.0f;
+              const bool apart = kV && __float_as_int(slot[KT + 1]) != 0;
 #pragma unroll 1
               for (int k0 = 0; k0 < kSteps; k0 += kBatch) {
                 uint4 v[kBatch];
@@ -770,7 +827,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
                     const int r = row + (k0 + k) * kStepRows;
                     if (r >= live) v[k] = make_uint4(0, 0, 0, 0);
                     // the row's factor as a sum of two f16 numbers, so that a product is rounded once
-                    const float f = r >= live ? 0.0f : slot[KT + 4 + r] * unit;
+                    const float f = r >= live ? 0.0f : apart ? 1.0f : slot[KT + 4 + r] * unit;
                     const __half hi = __float2half_rn(f);
                     f1 = __half2half2(hi), f0 = __half2half2(__float2half_rn(f - __half2float(hi)));
                   }
@@ -788,21 +845,29 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
               }
             };
             if (kv == 0) {
-              // The tile's scales and eV (broken rows' NaN aside) into its slot, which was last
-              // read for the tile kScaleSlots before, whose V tile has left the ring.
+              // The tile's scales, eV and their likeness into its slot, which was last read for the
+              // tile kScaleSlots before, whose V tile has left the ring.
               const float* scales = reinterpret_cast<const float*>(smem + C::kOffRawScales) + rs * 2 * KT;
-              unsigned big = 0;
+              unsigned big = 0, small = 0xffffffffu;
 #pragma unroll
               for (int x = 0; x < KT / 32; ++x) {
                 const unsigned bits = __float_as_uint(scales[KT + 32 * x + lane]);
-                if (32 * x + lane < live && bits < 0x7F800000u) big = max(big, bits);
+                if (32 * x + lane < live) {
+                  big = max(big, bits);
+                  small = min(small, bits);
+                }
               }
               if (tid < KT) {
                 slot[tid] = scales[tid];
                 slot[KT + 4 + tid] = scales[KT + tid];
               }
               big = __reduce_max_sync(0xffffffffu, big);
-              if (tid == 0) slot[KT] = __int_as_float(scale_exponent(big));
+              small = __reduce_min_sync(0xffffffffu, small);
+              if (tid == 0) {
+                const bool alike = scales_alike(small, big);
+                slot[KT] = __int_as_float(alike ? scale_exponent(big) : 0);
+                slot[KT + 1] = __int_as_float(!alike);
+              }
               __syncwarp();
               if (lane == 0) mbar_arrive(scale_bar(sc));
               convert(std::false_type{});
