@@ -387,12 +387,14 @@ typedef struct {
  * rounded to the matrix units' 16 bits before they multiply V (bf16 with a bf16 cache, f16
  * with an 8-bit one, where many query rows may also have V, code times scale, rounded to f16's
  * 11 bits; a weight whose product with its V's scale is below 2^-14 of the row's largest such
- * product is rounded to 2^-24 of that), and the result is rounded once.  What lies past kv_len in a page is not looked at,
- * whatever bits it holds; a page outside the cache is read as page 0, and a length past
- * the table or a query range outside M is cut to it, each reported by lora_poll_status
- * (LORA_ERR_DEVICE_INPUT).  An infinity or NaN in a position of a sequence's own V in a bf16
- * cache (kv_len's inside; in an e4m3 one a NaN code, which lora_kv_append never writes) may
- * also reach tokens of that sequence that do not see the position.
+ * product is rounded to 2^-24 of that), and the result is rounded once.
+ * What lies past kv_len in a page is not looked at, whatever bits it holds, and neither are
+ * the table entries and pages that lie wholly before the window of a sequence's first new
+ * token (they may have been released).  Any other page outside the cache is read as page 0,
+ * and a length past the table or a query range outside M is cut to it, each reported by
+ * lora_poll_status (LORA_ERR_DEVICE_INPUT).  An infinity or NaN in a position of a sequence's
+ * own V in a bf16 cache (kv_len's inside; in an e4m3 one a NaN code, which lora_kv_append
+ * never writes) may also reach tokens of that sequence that do not see the position.
  * ws: lora_paged_attention_workspace_bytes. */
 size_t lora_paged_attention_workspace_bytes(int64_t M, int64_t n_seqs, int heads_q, const lora_kv_cache_t* cache);
 lora_status_t lora_paged_attention(int64_t M, int heads_q, const lora_heads_t* q, const lora_kv_cache_t* cache,

@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
       const int kvh = w.slice / p.spg;
       const int* row = p.table + static_cast<long long>(w.b) * p.max_pages;
       const int pages = (w.s.kv + ps - 1) >> p.cache.page_shift;
+      const int low = lowest_seen(p, w);
       int held = -64, page = 0;           // lane l holds the table's entry held + l
       for (int j = w.ja; j < w.jb; ++j) {
         ok = attn_wait(empty_bar(stage), phase ^ 1u, abort_flag, p);
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
         if (at + boxes > held + 32) {
           held = at;
           page = 0;
-          if (at + lane < pages) {
+          if (at + lane < pages && at + lane >= low >> p.cache.page_shift) {
             page = __ldg(row + at + lane);
             if (page < 0 || page >= p.cache.n_pages) {
               atomicOr(p.status, kStatusInput);
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
         const int mine = __shfl_sync(0xffffffffu, page, at - held + (lane < boxes ? lane : 0));
         const int left = w.s.kv - j * KT;                      // positions from the tile's first on
         const int live = left <= 0 ? 0 : min(boxes, (left + box_rows - 1) / box_rows);
+        const int skip = max(0, low - j * KT) / box_rows;      // boxes that no row sees, below `live`
         const uint32_t fb = full_bar(stage);
         if (p.inject_stall && first) {                         // leave this stage empty
           first = false;
@@ -131,15 +133,16 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
           first = false;
           if (lane == 0) {
             if (live > 0)
-              mbar_arrive_expect_tx(fb, live * box_rows * (2u * C::kRow + (FMT == LORA_KV_BF16 ? 0u : 8u)));
+              mbar_arrive_expect_tx(fb, box_rows * (live * 2u * C::kRow + (FMT == LORA_KV_BF16 ? 0u : (live - skip) * 8u)));
             else
               mbar_arrive(fb);
           }
           __syncwarp();
           if (lane < live) {
             const int r0 = lane * box_rows;
-            const long long src = ((static_cast<long long>(mine) * p.cache.heads + kvh) << p.cache.page_shift) +
-                                  ((j * KT + r0) & (ps - 1));
+            const long long src = lane < skip ? -box_rows
+                                              : ((static_cast<long long>(mine) * p.cache.heads + kvh) << p.cache.page_shift) +
+                                                    ((j * KT + r0) & (ps - 1));
             const uint32_t kt = sbase + stage * C::kStage, vt = kt + C::kTile;
 #pragma unroll
             for (int x = 0; x < C::kBoxes; ++x) {
@@ -148,7 +151,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
               tma_load_2d(vt + x * (KT * C::kBox) + r0 * C::kBox, &p.vmap, fb, x * (C::kBox / C::kEl),
                           static_cast<int>(src));
             }
-            if (FMT != LORA_KV_BF16) {
+            if (FMT != LORA_KV_BF16 && lane >= skip) {
               const uint32_t sc = sbase + C::kOffScales + stage * C::kScales + r0 * 4;
               bulk_load(sc, p.cache.ks + src, box_rows * 4, fb);
               bulk_load(sc + KT * 4, p.cache.vs + src, box_rows * 4, fb);

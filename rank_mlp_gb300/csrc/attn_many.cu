@@ -217,13 +217,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
       const int kvh = w.slice / p.spg;
       const int* row = p.table + static_cast<long long>(w.b) * p.max_pages;
       const int pages = (w.s.kv + ps - 1) >> p.cache.page_shift;
+      const int low = lowest_seen(p, w);
       int held = -64, page = 0;           // lane l holds the table's entry held + l
       for (int j = w.ja; ok && j < w.jb; ++j) {
         const int at = (j * KT) >> p.cache.page_shift;
         if (at + boxes > held + 32) {
           held = at;
           page = 0;
-          if (at + lane < pages) {
+          if (at + lane < pages && at + lane >= low >> p.cache.page_shift) {
             page = __ldg(row + at + lane);
             if (page < 0 || page >= p.cache.n_pages) {
               atomicOr(p.status, kStatusInput);
@@ -234,9 +235,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         const int mine = __shfl_sync(0xffffffffu, page, at - held + (lane < boxes ? lane : 0));
         const int left = w.s.kv - j * KT;
         const int live = left <= 0 ? 0 : min(boxes, (left + box_rows - 1) / box_rows);
+        const int skip = max(0, low - j * KT) / box_rows;      // boxes that no row sees, below `live`
         const int r0 = lane * box_rows;
-        const long long src = ((static_cast<long long>(mine) * p.cache.heads + kvh) << p.cache.page_shift) +
-                              ((j * KT + r0) & (ps - 1));
+        const long long src = lane < skip ? -box_rows
+                                          : ((static_cast<long long>(mine) * p.cache.heads + kvh) << p.cache.page_shift) +
+                                                ((j * KT + r0) & (ps - 1));
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {  // the K tile, then the V tile
           ok = attn_wait(ebar(stage), phase ^ 1u, abort_flag, p);
@@ -249,7 +252,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             first = false;
             if (lane == 0) {
               if (live > 0)
-                mbar_arrive_expect_tx(fb, live * box_rows * (static_cast<uint32_t>(D * kEl) + (C::kRaw && kv == 0 ? 8u : 0u)));
+                mbar_arrive_expect_tx(fb, box_rows * (live * static_cast<uint32_t>(D * kEl) + (C::kRaw && kv == 0 ? (live - skip) * 8u : 0u)));
               else
                 mbar_arrive(fb);
             }
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
 #pragma unroll
               for (int x = 0; x < kBoxes; ++x)
                 tma_load_2d(dst + x * (KT * kBox), kv ? &p.vmap : &p.kmap, fb, x * (kBox / kEl), static_cast<int>(src));
-              if (C::kRaw && kv == 0) {   // the K tile brings both tiles' scales
+              if (C::kRaw && kv == 0 && lane >= skip) {   // the K tile brings both tiles' scales
                 const uint32_t sc = sbase + C::kOffRawScales + stage * (2 * KT * 4) + r0 * 4;
                 bulk_load(sc, p.cache.ks + src, box_rows * 4, fb);
                 bulk_load(sc + KT * 4, p.cache.vs + src, box_rows * 4, fb);
@@ -848,18 +851,20 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
               // The tile's scales, eV and their likeness into its slot, which was last read for the
               // tile kScaleSlots before, whose V tile has left the ring.
               const float* scales = reinterpret_cast<const float*>(smem + C::kOffRawScales) + rs * 2 * KT;
+              // (positions that no row sees, whose scales may be anything, count as 0)
+              const int from = max(0, lowest_seen(p, w) - j * KT);
               unsigned big = 0, small = 0xffffffffu;
 #pragma unroll
               for (int x = 0; x < KT / 32; ++x) {
                 const unsigned bits = __float_as_uint(scales[KT + 32 * x + lane]);
-                if (32 * x + lane < live) {
+                if (32 * x + lane >= from && 32 * x + lane < live) {
                   big = max(big, bits);
                   small = min(small, bits);
                 }
               }
               if (tid < KT) {
                 slot[tid] = scales[tid];
-                slot[KT + 4 + tid] = scales[KT + tid];
+                slot[KT + 4 + tid] = tid >= from ? scales[KT + tid] : 0.0f;
               }
               big = __reduce_max_sync(0xffffffffu, big);
               small = __reduce_min_sync(0xffffffffu, small);

@@ -69,14 +69,18 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b, bool report)
 
 __device__ __forceinline__ int row_tiles(const AttnParams& p, const Seq& s) { return (s.n + p.tt - 1) / p.tt; }
 
+// The lowest position that token t's window leaves it (0 without a window).
+__device__ __forceinline__ int first_seen(const AttnParams& p, const Seq& s, int t) {
+  return p.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(s.kv) - s.n + t - p.window + 1)) : 0;
+}
+
 // Tiles [j0, j1) of KT positions that row tile rt sees any of; one empty tile if none.
 template <int KT>
 __device__ __forceinline__ void item_tiles(const AttnParams& p, const Seq& s, int rt, int& j0, int& j1) {
   const int t0 = rt * p.tt, t1 = min(s.n, t0 + p.tt) - 1;
   const int off = s.kv - s.n;
   const int hi = p.causal ? max(0, min(s.kv, off + t1 + 1)) : s.kv;
-  const int lo = p.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(off) + t0 - p.window + 1)) : 0;
-  j0 = lo / KT;
+  j0 = first_seen(p, s, t0) / KT;
   j1 = max(j0 + 1, (hi + KT - 1) / KT);
 }
 
@@ -84,7 +88,7 @@ __device__ __forceinline__ void item_tiles(const AttnParams& p, const Seq& s, in
 __device__ __forceinline__ void row_range(const AttnParams& p, const Seq& s, int t, int& lo, int& hi) {
   const int pos = s.kv - s.n + t;
   hi = p.causal ? min(s.kv, pos + 1) : s.kv;
-  lo = p.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(pos) - p.window + 1)) : 0;
+  lo = first_seen(p, s, t);
 }
 
 // Token and query head of row r of tile rt's half q; false past the half's tokens, the
@@ -251,6 +255,11 @@ struct Span {
   bool starts, ends;         // holds the item's first / last tile
   int after;                 // units of the item after this part
 };
+
+// No row of the item sees a position before this one.  Pages that lie wholly before it may have
+// been released: their table entries are not looked at, and their boxes are loaded from
+// before the first row of the cache, which TMA fills with zeros (their scales are not loaded).
+__device__ __forceinline__ int lowest_seen(const AttnParams& p, const Span& w) { return first_seen(p, w.s, w.rt * p.tt); }
 
 // Walks a CTA's share; every role walks it by itself.
 template <int KT, int IT>
