@@ -383,11 +383,12 @@ typedef struct {
  * p < 0) gets out 0 and lse -inf.  Rows of M that no sequence owns are not written.
  * q is a view (of strides above 0); heads_q is a multiple of the cache's heads, and
  * M * heads_q at most 2^31 - 1.
- * Scores, maxima, sums and the accumulated output are f32; the weights e^(...) are
- * rounded to the matrix units' 16 bits before they multiply V (bf16 with a bf16 cache, f16
- * with an 8-bit one, where many query rows may also have V, code times scale, rounded to f16's
- * 11 bits; a weight whose product with its V's scale is below 2^-14 of the row's largest such
- * product is rounded to 2^-24 of that), and the result is rounded once.
+ * Scores, maxima, sums and the accumulated output are f32; the weights e^(...) are rounded
+ * to the matrix units' 16 bits before they multiply V, and the result is rounded once.  With a
+ * bf16 cache the weights are bf16; few query rows carry them in two parts, 16 bits of
+ * significand.  With an 8-bit cache they are f16, and many query rows may also have V, code
+ * times scale, rounded to f16's 11 bits; a weight whose product with its V's scale is below
+ * 2^-14 of the row's largest such product is rounded to 2^-24 of that.
  * What lies past kv_len in a page is not looked at, whatever bits it holds, and neither are
  * the table entries and pages that lie wholly before the window of a sequence's first new
  * token (they may have been released).  Any other page outside the cache is read as page 0,

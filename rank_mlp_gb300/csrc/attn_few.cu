@@ -6,7 +6,8 @@
 // A CTA: one producer warp fills a ring of K/V tiles of 64 positions by TMA (128- or 64-byte
 // swizzle, one box per page), four warps take a quarter of each tile's positions
 // and keep a running maximum, sum and output of their own in registers, merged when the
-// item's part ends.  Measured: one token of four sequences of 50,000 to 65,536 positions, 8
+// item's part ends.  bf16 weights go to the matrix units in two parts, P V is issued twice
+// (beside the waits for memory this costs 1%).  Measured: one token of four sequences of 50,000 to 65,536 positions, 8
 // cache heads of 128 features: 948 MB in 148 us (6.4 TB/s, 94% of a copy's rate).
 //
 // 8-bit caches run in f16, which holds both formats' codes exactly and to which they turn
@@ -330,7 +331,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
         }
         const float m[2] = {top[0] == -INFINITY ? 0.0f : top[0], top[1] == -INFINITY ? 0.0f : top[1]};
         const float vm[2] = {vtop[0] == -INFINITY ? 0.0f : vtop[0], vtop[1] == -INFINITY ? 0.0f : vtop[1]};
-        uint32_t a[NG][4];
+        // A weight's 16 bits; bf16 ones carry 16 bits of significand in two parts, the second
+        // rounded by 2^-16 of the weight.  (Parts of the same sign, and neither 0 unless both
+        // are: they take an infinity of V to the same infinity.)
+        uint32_t a[NG][4], rest[NG][4];
 #pragma unroll
         for (int g = 0; g < 2 * NG; ++g) {
           float x[4];
@@ -344,8 +348,20 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
               if (kEdge && s[g][e] == -INFINITY) x[e] = 0.0f;        // a hidden position's scale is not looked at
             }
           }
-          a[g >> 1][2 * (g & 1)] = k8 ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
-          a[g >> 1][2 * (g & 1) + 1] = k8 ? pack_f16x2(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t& w = a[g >> 1][2 * (g & 1) + h];
+            if (k8) {
+              w = pack_f16x2(x[2 * h], x[2 * h + 1]);
+            } else {
+              w = __byte_perm(__float_as_uint(x[2 * h]), __float_as_uint(x[2 * h + 1]), 0x7632);
+              float r[2];
+#pragma unroll
+              for (int d = 0; d < 2; ++d)
+                r[d] = fmaxf(x[2 * h + d] - __uint_as_float(__float_as_uint(x[2 * h + d]) & 0xFFFF0000u), x[2 * h + d] * 0x1p-24f);
+              rest[g >> 1][2 * (g & 1) + h] = pack_bf16x2(r[0], r[1]);
+            }
+          }
         }
         // rows of V past the sequence hold anything: zero weights do not silence a NaN
 #pragma unroll
@@ -367,6 +383,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
             if (!k8) {
               mma_m16n8k16_bf16(o[x], a[kg], b[0], b[1]);
               mma_m16n8k16_bf16(o[x + 1], a[kg], b[2], b[3]);
+              mma_m16n8k16_bf16(o[x], rest[kg], b[0], b[1]);
+              mma_m16n8k16_bf16(o[x + 1], rest[kg], b[2], b[3]);
             } else {
               // o[2 x] holds features 16 x + 2 n, o[2 x + 1] features 16 x + 2 n + 1
 #pragma unroll
