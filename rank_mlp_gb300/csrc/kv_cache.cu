@@ -200,9 +200,10 @@ __global__ void __launch_bounds__(kAppendThreads, FMT == LORA_KV_BF16 ? 6 : 7) a
       turn_piece<VEC>(p, w[i], row ? row_of(h) : p.k.x, f0, from, t, row && p.rotate && !is_v, y);
       // the row's largest magnitude (a NaN if it holds one)
       float top = 0.0f;
-      if (FMT == LORA_KV_BF16) {
-        __syncwarp();          // every lane of the row has read it (yq may be q)
-      } else if (__any_sync(0xffffffffu, row && !is_q)) {
+      // every lane of the row has read its partners' features before any writes (yq may be q;
+      // the vote below orders no memory)
+      if (FMT == LORA_KV_BF16 || !VEC) __syncwarp();
+      if (FMT != LORA_KV_BF16 && __any_sync(0xffffffffu, row && !is_q)) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = max_abs_nan(top, y[e]);
 #pragma unroll
