@@ -396,7 +396,8 @@ typedef struct {
  * lora_poll_status (LORA_ERR_DEVICE_INPUT).  An infinity or NaN in a position of a sequence's
  * own V in a bf16 cache (kv_len's inside; in an e4m3 one a NaN code, which lora_kv_append
  * never writes) may also reach tokens of that sequence that do not see the position.
- * ws: lora_paged_attention_workspace_bytes. */
+ * ws: lora_paged_attention_workspace_bytes, the same for every M, n_seqs and heads_q over a
+ * cache (0 for arguments that the call refuses): steps of any size can share one. */
 size_t lora_paged_attention_workspace_bytes(int64_t M, int64_t n_seqs, int heads_q, const lora_kv_cache_t* cache);
 lora_status_t lora_paged_attention(int64_t M, int heads_q, const lora_heads_t* q, const lora_kv_cache_t* cache,
                                    const lora_paged_batch_t* batch, float scale, int causal, int64_t window,

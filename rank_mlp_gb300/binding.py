@@ -175,14 +175,17 @@ def _lin(lin, name) -> LoraLinear:
 
 # ------------------------------------------------------------------ workspaces
 
-_WS = {}
+_WS = {}           # (device, stream): its workspace
+_RECORDED = {}     # (device, stream): its workspaces that calls under capture were given
+_capturing = torch.cuda.is_current_stream_capturing
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:
     """A workspace of at least nbytes for the current stream of `device` (cached per
     device and stream, grown on demand, first 256 bytes zeroed: they hold the
     asynchronous status word).  Calls that share a workspace must not overlap on the
-    GPU, so each stream gets its own; calls on one stream are ordered anyway."""
+    GPU, so each stream gets its own; calls on one stream are ordered anyway.  One that a
+    graph has recorded is never freed: the graph's replays go on writing to it."""
     device = torch.device(device)
     idx = device.index if device.index is not None else torch.cuda.current_device()
     key = (idx, torch.cuda.current_stream(idx).cuda_stream)
@@ -193,14 +196,24 @@ def workspace(nbytes: int, device) -> torch.Tensor:
         if old is not None:
             ws[:4].copy_(old[:4])     # keep a status bit that has not been polled yet (same stream)
         _WS[key] = ws
+    if _capturing():
+        kept = _RECORDED.setdefault(key, [])
+        if not any(w is ws for w in kept):
+            kept.append(ws)
     return ws
 
 
 def poll_status(ws: torch.Tensor | None = None) -> int:
+    """Reads and clears the status word of ws, or of the current stream's workspaces: the
+    cached one and those that graphs captured on the stream have recorded."""
     lib = load()
-    if ws is None:
-        ws = workspace(256, torch.cuda.current_device())
-    return lib.lora_poll_status(ctypes.c_void_p(ws.data_ptr()), _stream(ws.device))
+    if ws is not None:
+        return lib.lora_poll_status(ctypes.c_void_p(ws.data_ptr()), _stream(ws.device))
+    ws = workspace(256, torch.cuda.current_device())
+    key = (ws.get_device(), torch.cuda.current_stream(ws.device).cuda_stream)
+    every = [ws] + [w for w in _RECORDED.get(key, ()) if w is not ws]
+    codes = [lib.lora_poll_status(ctypes.c_void_p(w.data_ptr()), _stream(w.device)) for w in every]
+    return min((c for c in codes if c), default=0)       # an expired wait before a bad input
 
 
 def poll_noalloc_status() -> int:
@@ -550,7 +563,7 @@ def _call(t, nbytes, ws):
     stream = _RAW_STREAM(idx)
     if ws is None:
         ws = _WS.get((idx, stream))
-        if ws is None or ws.numel() < nbytes:
+        if ws is None or ws.numel() < nbytes or _capturing():
             ws = workspace(nbytes, t.device)
     return stream, ws.data_ptr(), ws.numel()
 

@@ -21,7 +21,10 @@ static int row_halves(int64_t M, int64_t n_seqs, int group, int head_dim) {
   return head_dim == 256 || M * group <= 128 * n_seqs ? 1 : 2;
 }
 
-// Workspace: header, the parts' descriptors, maxima and sums, outputs.
+// Workspace: header, the parts' descriptors, maxima and sums, outputs.  It is the same for
+// every call over a cache, that of the kernel with the larger tiles: a decode step that a
+// graph has recorded and the prefills between its replays share one workspace.
+static int largest_halves(int head_dim) { return head_dim == 256 ? 1 : 2; }
 static void carve_parts(Carve& c, int halves, int head_dim, AttnParams& p) {
   const int64_t ctas = halves ? kMaxManyCtas : kMaxFewCtas, rows = 2 * ctas * (halves ? 128 * halves : kFewRows);
   c.take(kWsHeader);
@@ -41,7 +44,7 @@ extern "C" size_t lora_paged_attention_workspace_bytes(int64_t M, int64_t n_seqs
     return 0;
   AttnParams p;
   Carve c(nullptr);
-  carve_parts(c, row_halves(M, n_seqs, heads_q / cache->heads, cache->head_dim), cache->head_dim, p);
+  carve_parts(c, largest_halves(cache->head_dim), cache->head_dim, p);
   return c.off;
 }
 
@@ -87,7 +90,7 @@ extern "C" lora_status_t lora_paged_attention(int64_t M, int heads_q, const lora
   p.inject_stall = take_expiry();
   Carve c(ws);
   const int halves = row_halves(M, batch->n_seqs, p.group, cache->head_dim);
-  carve_parts(c, halves, cache->head_dim, p);
+  carve_parts(c, halves, cache->head_dim, p);        // (never more than the largest)
   return halves ? launch_attn_many(p, halves, cache->head_dim, cache->format, stream)
                 : launch_attn_few(p, cache->head_dim, cache->format, stream);
 }
