@@ -543,6 +543,20 @@ def _ints(t, dtype, shape, name) -> int:
     return t.data_ptr()
 
 
+_current_device = torch.cuda.current_device
+
+
+def _together(first, *others):
+    """Checks that a call's tensors (None: not passed) lie on the current device, whose context
+    its kernels run in: a kernel that reads another device's memory faults."""
+    idx = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != idx:
+            raise ValueError(f"tensors of one call must be on one device (got {idx} and {t.get_device()})")
+    if idx != _current_device():
+        raise ValueError(f"the tensors are on device {idx}, the current device is {_current_device()}")
+
+
 def _rotary(rope, tokens) -> bytes:
     """A lora_rotary_t of dict(cos, sin, pos[, layout]): f32 tables [n_pos, rot_dim/2] and int32 positions
     [tokens] on the device; layout "half" (default) or "interleaved"."""
@@ -605,6 +619,7 @@ def rotary(q, k=None, *, rope, inverse=False, q_out=None, k_out=None, ws=None):
     elif q_out.shape != shape:
         raise ValueError("q_out must have q's shape")
     rot = _rotary(rope, tokens)
+    _together(q, q_out, k, k_out, rope["cos"], rope["sin"], rope["pos"], ws)
     stream, wp, wn = _call(q, 256, ws)
     if k is None:
         _check(lib.lora_rotary(tokens, dim, view, _heads(q_out, "q_out"), None, None, rot, int(inverse), wp, wn, stream),
@@ -641,6 +656,8 @@ class KVCache:
         self.n_pages, self.heads, self.page_size, self.head_dim = shape
         self._struct = LoraKvCache(_ints(k, k.dtype, shape, "k"), _ints(v, k.dtype, shape, "v"), sc[0], sc[1],
                                    shape[0], shape[2], shape[1], shape[3], KV_FORMAT[k.dtype])
+        if any(t is not None and t.get_device() != k.get_device() for t in (v, k_scale, v_scale)):
+            raise ValueError("a cache's tensors must be on one device")
         self._at = _at(self._struct)
 
 
@@ -666,6 +683,9 @@ def kv_append(cache: KVCache, k, v, slots, *, q=None, rope=None, q_out=None, ws=
         raise ValueError(f"k and v must be [tokens, {cache.heads}, {dim}]")
     slot_at = _ints(slots, torch.int64, (tokens,), "slots")
     rot = None if rope is None else _rotary(rope, tokens)
+    _together(k, v, cache.k, slots, q, q_out, ws)
+    if rope is not None:
+        _together(k, rope["cos"], rope["sin"], rope["pos"])
     stream, wp, wn = _call(k, 256, ws)
     if q is None:
         _check(lib.lora_kv_append(tokens, cache._at, view, _heads(v, "v"), slot_at, None, None, rot, wp, wn, stream),
@@ -693,6 +713,7 @@ def kv_read(cache: KVCache, page_table, cu_kv, total: int, *, ws=None):
     if page_table.dim() != 2:
         raise ValueError("page_table must be [n_seqs, max_pages]")
     n, width = page_table.shape
+    _together(cache.k, page_table, cu_kv, ws)
     shape, dev = (total, cache.heads, cache.head_dim), cache.k.device
     k, v = torch.empty(shape, dtype=_BF16, device=dev), torch.empty(shape, dtype=_BF16, device=dev)
     stream, wp, wn = _call(cache.k, 256, ws)
@@ -716,6 +737,8 @@ class PagedBatch:
         self._struct = LoraPagedBatch(n, _ints(page_table, torch.int32, (n, width), "page_table"), width,
                                       _ints(kv_len, torch.int32, (n,), "kv_len"),
                                       _ints(cu_q, torch.int32, (n + 1,), "cu_q"))
+        if not page_table.get_device() == kv_len.get_device() == cu_q.get_device():
+            raise ValueError("a batch's tensors must be on one device")
         self._at, self.n_seqs = _at(self._struct), n
 
 
@@ -743,6 +766,7 @@ def paged_attention(q, cache: KVCache, batch: PagedBatch, *, scale=None, causal=
     else:
         out_at = _dev(out, "out")
     lse_at = None if lse is None else _ints(lse, torch.float32, (tokens, hq), "lse")
+    _together(q, cache.k, batch.cu_q, out, lse, ws)
     need = lib.lora_paged_attention_workspace_bytes(tokens, batch.n_seqs, hq, cache._at)
     stream, wp, wn = _call(q, need, ws)
     _check(lib.lora_paged_attention(tokens, hq, view, cache._at, batch._at, dim ** -0.5 if scale is None else scale,
