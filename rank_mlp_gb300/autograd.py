@@ -89,22 +89,39 @@ class LoraLinearFunction(torch.autograd.Function):
 
 
 class RotaryFunction(torch.autograd.Function):
-    """Rotary positions of q and k, views [tokens, heads, head_dim] (rope as in
-    ``binding.rotary``); the gradient is the rotation back."""
+    """Rotary positions of q and k (or None), views [tokens, heads, head_dim] (rope as in
+    ``binding.rotary``); the gradient is the rotation back, and its gradient the rotation.
+    The tables and positions are saved: a change in place before the backward is an error."""
 
     @staticmethod
-    def forward(ctx, q, k, rope):
-        ctx.rope = rope
-        return binding.rotary(q, k, rope=rope)
+    def forward(ctx, q, k, rope, inverse=False):
+        ctx.save_for_backward(rope["cos"], rope["sin"], rope["pos"])
+        ctx.layout, ctx.inverse = rope.get("layout", "half"), inverse
+        ctx.set_materialize_grads(False)
+        return binding.rotary(q, k, rope=rope, inverse=inverse)
 
     @staticmethod
-    def backward(ctx, dq, dk):
-        rows = lambda d: d if d.stride(-1) == 1 and all(s % 8 == 0 for s in d.stride()[:2]) \
-            and d.data_ptr() % 16 == 0 else d.contiguous()  # noqa: E731
-        return *binding.rotary(rows(_bf16(dq)), rows(_bf16(dk)), rope=ctx.rope, inverse=True), None
+    def backward(ctx, dq, dk=None):
+        cos, sin, pos = ctx.saved_tensors
+        rope = {"cos": cos, "sin": sin, "pos": pos, "layout": ctx.layout}
+        wanted = [d for d, need in zip((dq, dk), ctx.needs_input_grad) if need and d is not None]
+        back = []
+        if wanted:
+            back = RotaryFunction.apply(*(_rows(_bf16(d)) for d in wanted), *(None,) * (2 - len(wanted)), rope,
+                                        not ctx.inverse)
+            back = list(back) if len(wanted) == 2 else [back]
+        grads = [back.pop(0) if need and d is not None else None for d, need in zip((dq, dk), ctx.needs_input_grad)]
+        return *grads, None, None
+
+
+def _rows(d):
+    """d as a view of heads that the library takes."""
+    fits = d.stride(-1) == 1 and all(s % 8 == 0 for s in d.stride()[:2]) and d.data_ptr() % 16 == 0
+    return d if fits else d.contiguous()
 
 
 def lora_rotary(q, k, rope):
+    """(rotated q, rotated k), or the rotated q alone where k is None."""
     return RotaryFunction.apply(q, k, rope)
 
 
