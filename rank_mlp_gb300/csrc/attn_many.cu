@@ -35,7 +35,8 @@
 //          times finer than the bf16 rows that went into the cache; the weights are
 //          2^(s + eV - r)
 //   apart  the codes alone, exactly; a position's scale joins its weight as an exponent,
-//          2^(s + log2 vs - r) (taken for every tile, this cost a sixth of the time)
+//          2^(s + log2 vs - r) (512 new tokens of two sequences over 16,000 fp8 positions:
+//          307 us with every tile alike, 703 us with every tile apart)
 // r is a row's own reference: the running maximum of s + eV (s + log2 vs) over what the row
 // sees, so that neither a position of little weight nor a hidden one moves the other
 // positions' weights out of f16's range, whatever the scales are.  It stands kBoost powers
@@ -83,7 +84,8 @@ struct ManyCfg {
   static constexpr int kOffRaw = kOffRing + kStages * kTile;
   static constexpr int kOffRawScales = kOffRaw + kRawStages * kRawTile;
   static constexpr int kOffScales = kOffRawScales + (kRaw ? kRawStages * 2 * KT * 4 : 0);
-  // (a slot: the tile's KT K scales, eV, whether the V scales are apart, the V scales)
+  // (a slot: the tile's KT K scales, eV, whether the V scales are apart, the V scales
+  // or, apart, their log2)
   static constexpr int kSlotBytes = 2 * KT * 4 + 16;
   static constexpr int kOffBars = (kOffScales + (kRaw ? kScaleSlots * kSlotBytes : 0) + 127) & ~127;
   static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 6 + 5 * NQ + (kRaw ? kScaleSlots + NQ : 0);
@@ -564,12 +566,51 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         }
         tc_fence_after_sync();
         const bool edge = k0 < lo_max || k0 + KT > hi_min;
-        // compiled for tiles that all of the warp's rows see whole (nearly all), for the others,
-        // and for an exponent per position
-        auto softmax = [&](auto at_edge, auto each_exponent) {
-        constexpr bool kEdge = decltype(at_edge)::value, kEach = decltype(each_exponent)::value;
-        // log2 of the scale that position e's weight carries
-        auto exponent_of = [&](int e) { return apart ? log2_approx(ks[KT + 4 + e]) : static_cast<float>(ev); };
+        // Raises the row's maxima to a tile's where one exceeds them by more than the slack.
+        auto raise = [&](float cand, float vcand) {
+          // (rows that are nobody's hold any numbers: they have no say)
+          if (!__any_sync(0xffffffffu, own && (cand > top + kMaxSlack || (C::kRaw && vcand > ref + kMaxSlack)))) return true;
+          const float next = fmaxf(top, cand), vnext = C::kRaw ? fmaxf(ref, vcand) : next;
+          const float f = vnext == -INFINITY ? 1.0f : exp2_approx(ref - vnext);
+          const float fs = !C::kRaw ? f : next == -INFINITY ? 1.0f : exp2_approx(top - next);
+          ref = vnext;
+          top = next;
+          sum.x *= fs;
+          sum.y *= fs;
+          if (i == 0) return true;
+          ok = attn_wait(odone_bar(q), (done - 1u) & 1u, abort_flag, p);
+          if (!__all_sync(0xffffffffu, ok)) return false;
+          tc_fence_after_sync();
+#pragma unroll 1
+          for (int x = 0; x < D; x += 16) {
+            uint32_t v[16];
+            tmem_ld16(o_tmem + x, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+            tmem_st16(o_tmem + x, v);
+          }
+          tmem_st_wait();
+          return true;
+        };
+        // Half of a tile's weights are handed over while the other half is made.
+        auto hand_over = [&](int half) {
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pready_bar(buf, half));
+        };
+        // With one half the last scores do not wait for the O += P V before theirs; it has to be
+        // seen done before these weights go out, or the wait for the last one below could take
+        // its phase for the one before.
+        auto last_but_one_done = [&]() {
+          if (C::NQ != 1 || i == 0 || i + 1 != n) return true;
+          ok = attn_wait(odone_bar(q), (done - 1u) & 1u, abort_flag, p);
+          return __all_sync(0xffffffffu, ok) != 0;
+        };
+        // compiled for tiles that all of the warp's rows see whole (nearly all), and for the others
+        auto softmax = [&](auto at_edge) {
+        constexpr bool kEdge = decltype(at_edge)::value;
         // the row's scores, read once and held in registers, 32 columns on their way while the
         // 32 before are worked on
         uint32_t v[KT / 32][32];
@@ -591,7 +632,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             for (int e = 0; e < 32; ++e) v[e] = key + e >= lo && key + e < hi ? v[e] : 0xFF800000u;   // -inf
           }
         };
-        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, vmost = -INFINITY;
+        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         auto maxima = [&](const uint32_t (&v)[32]) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
@@ -607,40 +648,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           if (x + 1 < KT / 32) tmem_ld32(s_tmem + 32 * (x + 1), v[x + 1]);
           finish(v[x], 32 * x);
           maxima(v[x]);
-          if (kEach) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) vmost = fmaxf(vmost, fmaf(__uint_as_float(v[x][e]), c, exponent_of(32 * x + e)));
-          }
         }
         const float cand = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
-        const float vcand = kEach ? vmost : C::kRaw ? cand + ev : cand;
-        // (rows that are nobody's hold any numbers: they have no say)
-        if (__any_sync(0xffffffffu, own && (cand > top + kMaxSlack || (C::kRaw && vcand > ref + kMaxSlack)))) {
-          const float next = fmaxf(top, cand), vnext = C::kRaw ? fmaxf(ref, vcand) : next;
-          const float f = vnext == -INFINITY ? 1.0f : exp2_approx(ref - vnext);
-          const float fs = !C::kRaw ? f : next == -INFINITY ? 1.0f : exp2_approx(top - next);
-          ref = vnext;
-          top = next;
-          sum.x *= fs;
-          sum.y *= fs;
-          if (i > 0) {
-            ok = attn_wait(odone_bar(q), (done - 1u) & 1u, abort_flag, p);
-            if (!__all_sync(0xffffffffu, ok)) return false;
-            tc_fence_after_sync();
-#pragma unroll 1
-            for (int x = 0; x < D; x += 16) {
-              uint32_t v[16];
-              tmem_ld16(o_tmem + x, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-              tmem_st16(o_tmem + x, v);
-            }
-            tmem_st_wait();
-          }
-        }
-        const float base = ref == -INFINITY ? 0.0f : C::kRaw ? (kEach ? kBoost : kBoost + ev) - ref : -ref;
-        const float seen = top == -INFINITY ? 0.0f : -top;
+        if (!raise(cand, cand + ev)) return false;
+        const float base = ref == -INFINITY ? 0.0f : C::kRaw ? kBoost + ev - ref : -ref;
         const float2 c2 = make_float2(c, c), ref2 = make_float2(base, base);
         float2 l[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         auto weights = [&](const uint32_t (&v)[32], int x) {
@@ -650,18 +661,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             float2 y[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              if (kEach) {
-                float z[2];
-#pragma unroll
-                for (int d = 0; d < 2; ++d) {
-                  const float s = __uint_as_float(v[e + 2 * k + d]);
-                  z[d] = exp2_approx(fmaf(s, c, seen));
-                  // (a hidden position's scale, which may be a NaN, is not looked at)
-                  (d ? y[k].y : y[k].x) = s == -INFINITY ? 0.0f : exp2_approx(fmaf(s, c, exponent_of(x + e + 2 * k + d) + base));
-                }
-                l[k] = add_f32x2(l[k], make_float2(z[0], z[1]));
-                continue;
-              }
               y[k] = fma_f32x2(make_float2(__uint_as_float(v[e + 2 * k]), __uint_as_float(v[e + 2 * k + 1])), c2, ref2);
               y[k].x = exp2_approx(y[k].x);
               y[k].y = exp2_approx(y[k].y);
@@ -684,44 +683,87 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
               st_shared_v4(vt + (e >> 3) * (KT * 128) + row * 128 + ((e & 7) << 4), make_uint4(0, 0, 0, 0));
           fence_proxy_async_smem();
         }
-        // half of a tile's weights are handed over while the other half is made
-        auto hand_over = [&](int half) {
-          tmem_st_wait();
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pready_bar(buf, half));
-        };
 #pragma unroll
         for (int x = 0; x < KT / 32; ++x) {
           weights(v[x], 32 * x);
-          if (C::NQ == 1 && x == KT / 32 - 1 && i > 0 && i + 1 == n) {
-            // With one half the last scores do not wait for the O += P V before theirs; it has to
-            // be seen done before these weights go out, or the wait for the last one below
-            // could take its phase for the one before.
-            ok = attn_wait(odone_bar(q), (done - 1u) & 1u, abort_flag, p);
-            if (!__all_sync(0xffffffffu, ok)) return false;
-          }
+          if (x == KT / 32 - 1 && !last_but_one_done()) return false;
           if (x == KT / 64 - 1) hand_over(0);
           if (x == KT / 32 - 1) hand_over(1);
         }
         l[0] = add_f32x2(l[0], l[1]);
-        if (C::kRaw && !kEach && top != -INFINITY) {     // from the weights' reference to the sums'
+        if (C::kRaw && top != -INFINITY) {     // from the weights' reference to the sums'
           const float f = exp2_approx(-base - top);
           l[0] = mul_f32x2(l[0], make_float2(f, f));
         }
         sum = add_f32x2(sum, l[0]);
         return true;
         };
-        if constexpr (C::kRaw) {
-          // An exponent per position also where a row's reference is so far above this tile's
-          // scale that its weights, of which the sum takes part, could leave f32's range.
-          if (__any_sync(0xffffffffu, apart || (own && top + ev < ref - 90.0f)))
-            ok = softmax(std::true_type{}, std::true_type{});
-          else
-            ok = edge ? softmax(std::true_type{}, std::false_type{}) : softmax(std::false_type{}, std::false_type{});
-        } else {
-          ok = edge ? softmax(std::true_type{}, std::false_type{}) : softmax(std::false_type{}, std::false_type{});
-        }
+        // The same with an exponent per position (8-bit), in two passes over the scores: such
+        // tiles are few, and the code stays small and out of the others' registers.
+        auto softmax_apart = [&]() {
+          // the scores of columns [x, x + 32), and the exponents of columns e to e + 3
+          auto scores_at = [&](int x, uint32_t (&v)[32]) {
+            __syncwarp();
+            tmem_ld32(s_tmem + x, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              v[e] = k0 + x + e >= lo && k0 + x + e < hi ? __float_as_uint(__uint_as_float(v[e]) * ks[x + e]) : 0xFF800000u;
+          };
+          auto exponents_at = [&](int e, float (&g)[4]) {
+            const float4 f = *reinterpret_cast<const float4*>(ks + KT + 4 + e);
+            g[0] = apart ? f.x : ev, g[1] = apart ? f.y : ev, g[2] = apart ? f.z : ev, g[3] = apart ? f.w : ev;
+          };
+          float most = -INFINITY, vmost = -INFINITY;
+#pragma unroll 1
+          for (int x = 0; x < KT; x += 32) {
+            uint32_t v[32];
+            scores_at(x, v);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float g[4];
+              exponents_at(x + e, g);
+#pragma unroll
+              for (int d = 0; d < 4; ++d) {
+                most = fmaxf(most, __uint_as_float(v[e + d]));
+                vmost = fmaxf(vmost, fmaf(__uint_as_float(v[e + d]), c, g[d]));
+              }
+            }
+          }
+          if (!raise(most * c, vmost)) return false;
+          const float base = ref == -INFINITY ? 0.0f : kBoost - ref, seen = top == -INFINITY ? 0.0f : -top;
+          // (a pass's weights stand where scores of the passes before stood)
+#pragma unroll 1
+          for (int x = 0; x < KT; x += 32) {
+            uint32_t v[32], u[16];
+            scores_at(x, v);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float g[4], y[4];
+              exponents_at(x + e, g);
+#pragma unroll
+              for (int d = 0; d < 4; ++d) {
+                const float s = __uint_as_float(v[e + d]);
+                // (a hidden position's scale, which may be a NaN, is not looked at)
+                y[d] = s == -INFINITY ? 0.0f : exp2_approx(fmaf(s, c, g[d] + base));
+                (d % 2 ? sum.y : sum.x) += exp2_approx(fmaf(s, c, seen));
+              }
+              u[e / 2] = pack_f16x2(y[0], y[1]);
+              u[e / 2 + 1] = pack_f16x2(y[2], y[3]);
+            }
+            tmem_st16(s_tmem + x / 2, u);
+            if (x == KT - 32 && !last_but_one_done()) return false;
+            if (x == KT / 2 - 32) hand_over(0);
+            if (x == KT - 32) hand_over(1);
+          }
+          return true;
+        };
+        // (also where a row's reference is so far above this tile's scale that its weights, of
+        // which the sum takes part, could leave f32's range)
+        if (C::kRaw && __any_sync(0xffffffffu, apart || (own && top + ev < ref - 90.0f)))
+          ok = softmax_apart();
+        else
+          ok = edge ? softmax(std::true_type{}) : softmax(std::false_type{});
         if (!ok) break;
         ++done;
       }
@@ -868,11 +910,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
               }
               big = __reduce_max_sync(0xffffffffu, big);
               small = __reduce_min_sync(0xffffffffu, small);
+              const bool alike = scales_alike(small, big);
               if (tid == 0) {
-                const bool alike = scales_alike(small, big);
                 slot[KT] = __int_as_float(alike ? scale_exponent(big) : 0);
                 slot[KT + 1] = __int_as_float(!alike);
               }
+              if (!alike && tid < KT) slot[KT + 4 + tid] = log2_approx(slot[KT + 4 + tid]);
               __syncwarp();
               if (lane == 0) mbar_arrive(scale_bar(sc));
               convert(std::false_type{});
