@@ -32,11 +32,10 @@ struct FewCfg {
   static constexpr int kRow = D * kEl;                        // bytes of a cached row
   static constexpr int kBox = kRow < 128 ? kRow : 128;        // bytes of a row that one box holds
   static constexpr int kBoxes = kRow / kBox;
-  static constexpr int kKT = 64;
+  static constexpr int kKT = 64;                              // 16 positions for each of four warps
   // An item's own cost, in tiles: measured 1, 2, 3, 4, 6 at 152, 141, 136, 131, 136 us for 64
   // sequences of 200 to 8192 int8 positions.
   static constexpr int kItem = 4;
-  static constexpr int kGroups = kKT / 64;                    // of 16 positions, per warp and tile
   static constexpr int kTile = kKT * kRow;
   static constexpr int kStage = 2 * kTile;
   // CTAs of an SM, 160 threads each: D = 256 needs the registers of one alone.  Two and three
@@ -173,7 +172,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
 
   // -------------------------------------------------------------- the four product warps
   constexpr bool k8 = FMT != LORA_KV_BF16;
-  constexpr int NG = C::kGroups;
   const int t = lane & 3, r0 = lane >> 2;         // fragment column pair and row (rows r0, r0 + 8)
   float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
@@ -181,7 +179,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
   // 16-byte piece is permuted within its row by the row's low bits (TMA's swizzle), so that
   // piece x + 4 lies at an offset that differs in one bit, and other rows of the same lane
   // at a constant distance.
-  const int first = warp * 16 * NG;
+  const int first = warp * 16;
   const uint32_t k_at = C::kBox == 128 ? (first + (lane & 7)) * 128 + (((lane >> 3) ^ (lane & 7)) << 4)
                                        : (first + (lane & 7)) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
   const uint32_t v_at = C::kBox == 128 ? (first + (lane & 15)) * 128 + (((lane >> 4) ^ (lane & 7)) << 4)
@@ -263,15 +261,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
         const uint32_t ka = sbase + stage * C::kStage + k_at, va = sbase + stage * C::kStage + C::kTile + v_at;
         const float* ks = reinterpret_cast<const float*>(smem + C::kOffScales + stage * C::kScales) + first;
         const float* vs = ks + KT;
-        float s[2 * NG][4];                       // positions k0 + 8 g + 2 t + {0, 1}, rows r0 and r0 + 8
+        float s[2][4];                            // positions k0 + 8 g + 2 t + {0, 1}, rows r0 and r0 + 8
 #pragma unroll
-        for (int g = 0; g < 2 * NG; ++g)
+        for (int g = 0; g < 2; ++g)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[g][e] = 0.0f;
 #pragma unroll
         for (int x = 0; x < C::kRow / 16; x += 4) {          // four 16-byte pieces of a row
 #pragma unroll
-          for (int g = 0; g < 2 * NG; ++g) {
+          for (int g = 0; g < 2; ++g) {
             uint32_t b[4];
             ldmatrix_x4((ka ^ ((x & 7) << 4)) + (x >> 3) * (KT * 128) + 8 * g * C::kBox, b);
             if (!k8) {
@@ -285,9 +283,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
           }
         }
         float most[2] = {-INFINITY, -INFINITY}, vmost[2] = {-INFINITY, -INFINITY};
-        float2 lv[2 * NG];
+        float2 lv[2];
 #pragma unroll
-        for (int g = 0; g < 2 * NG; ++g) {
+        for (int g = 0; g < 2; ++g) {
           if (k8) {
             const float2 sc = *reinterpret_cast<const float2*>(ks + 8 * g + 2 * t);
             s[g][0] *= sc.x, s[g][1] *= sc.y, s[g][2] *= sc.x, s[g][3] *= sc.y;
@@ -334,9 +332,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
         // A weight's 16 bits; bf16 ones carry 16 bits of significand in two parts, the second
         // rounded by 2^-16 of the weight.  (Parts of the same sign, and neither 0 unless both
         // are: they take an infinity of V to the same infinity.)
-        uint32_t a[NG][4], rest[NG][4];
+        uint32_t a[4], rest[4];
 #pragma unroll
-        for (int g = 0; g < 2 * NG; ++g) {
+        for (int g = 0; g < 2; ++g) {
           float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -350,7 +348,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t& w = a[g >> 1][2 * (g & 1) + h];
+            uint32_t& w = a[2 * g + h];
             if (k8) {
               w = pack_f16x2(x[2 * h], x[2 * h + 1]);
             } else {
@@ -359,46 +357,43 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attn_few_kernel(const _
 #pragma unroll
               for (int d = 0; d < 2; ++d)
                 r[d] = fmaxf(x[2 * h + d] - __uint_as_float(__float_as_uint(x[2 * h + d]) & 0xFFFF0000u), x[2 * h + d] * 0x1p-24f);
-              rest[g >> 1][2 * (g & 1) + h] = pack_bf16x2(r[0], r[1]);
+              rest[2 * g + h] = pack_bf16x2(r[0], r[1]);
             }
           }
         }
         // rows of V past the sequence hold anything: zero weights do not silence a NaN
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (kEdge) {
+          const int a0 = w.s.kv - k0 - 2 * t, a1 = a0 - 8;      // positions left from this lane's first
+          keep0 = a0 >= 2 ? 0xffffffffu : a0 == 1 ? 0x0000ffffu : 0u;
+          keep1 = a1 >= 2 ? 0xffffffffu : a1 == 1 ? 0x0000ffffu : 0u;
+        }
 #pragma unroll
-        for (int kg = 0; kg < NG; ++kg) {
-          uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        for (int x = 0; x < C::kRow / 16; x += 2) {        // two 16-byte pieces of 16 rows
+          uint32_t b[4];
+          ldmatrix_x4_trans((va ^ ((x & 7) << 4)) + (x >> 3) * (KT * 128), b);
           if (kEdge) {
-            const int a0 = w.s.kv - k0 - 16 * kg - 2 * t, a1 = a0 - 8;      // positions left from this lane's first
-            keep0 = a0 >= 2 ? 0xffffffffu : a0 == 1 ? 0x0000ffffu : 0u;
-            keep1 = a1 >= 2 ? 0xffffffffu : a1 == 1 ? 0x0000ffffu : 0u;
+            // (8-bit: a 16-bit element of the transposed tile is two features' codes)
+            b[0] &= keep0, b[1] &= keep1, b[2] &= keep0, b[3] &= keep1;
           }
+          if (!k8) {
+            mma_m16n8k16_bf16(o[x], a, b[0], b[1]);
+            mma_m16n8k16_bf16(o[x + 1], a, b[2], b[3]);
+            mma_m16n8k16_bf16(o[x], rest, b[0], b[1]);
+            mma_m16n8k16_bf16(o[x + 1], rest, b[2], b[3]);
+          } else {
+            // o[2 x] holds features 16 x + 2 n, o[2 x + 1] features 16 x + 2 n + 1
 #pragma unroll
-          for (int x = 0; x < C::kRow / 16; x += 2) {        // two 16-byte pieces of 16 rows
-            uint32_t b[4];
-            ldmatrix_x4_trans((va ^ ((x & 7) << 4)) + (x >> 3) * (KT * 128) + 16 * kg * C::kBox, b);
-            if (kEdge) {
-              // (8-bit: a 16-bit element of the transposed tile is two features' codes)
-              b[0] &= keep0, b[1] &= keep1, b[2] &= keep0, b[3] &= keep1;
-            }
-            if (!k8) {
-              mma_m16n8k16_bf16(o[x], a[kg], b[0], b[1]);
-              mma_m16n8k16_bf16(o[x + 1], a[kg], b[2], b[3]);
-              mma_m16n8k16_bf16(o[x], rest[kg], b[0], b[1]);
-              mma_m16n8k16_bf16(o[x + 1], rest[kg], b[2], b[3]);
-            } else {
-              // o[2 x] holds features 16 x + 2 n, o[2 x + 1] features 16 x + 2 n + 1
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                mma_m16n8k16_f16(o[k8 ? 2 * (x + e) : 0], a[kg], codes02_to_f16x2<FMT>(b[2 * e]),
-                                 codes02_to_f16x2<FMT>(b[2 * e + 1]));
-                mma_m16n8k16_f16(o[k8 ? 2 * (x + e) + 1 : 0], a[kg], codes13_to_f16x2<FMT>(b[2 * e]),
-                                 codes13_to_f16x2<FMT>(b[2 * e + 1]));
-              }
+            for (int e = 0; e < 2; ++e) {
+              mma_m16n8k16_f16(o[k8 ? 2 * (x + e) : 0], a, codes02_to_f16x2<FMT>(b[2 * e]),
+                               codes02_to_f16x2<FMT>(b[2 * e + 1]));
+              mma_m16n8k16_f16(o[k8 ? 2 * (x + e) + 1 : 0], a, codes13_to_f16x2<FMT>(b[2 * e]),
+                               codes13_to_f16x2<FMT>(b[2 * e + 1]));
             }
           }
         }
         };
-        if (k0 >= lo_max && k0 + 16 * NG <= hi_min)
+        if (k0 >= lo_max && k0 + 16 <= hi_min)
           tile(std::false_type{});
         else
           tile(std::true_type{});
