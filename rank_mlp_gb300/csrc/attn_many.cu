@@ -36,7 +36,7 @@
 //          2^(s + eV - r)
 //   apart  the codes alone, exactly; a position's scale joins its weight as an exponent,
 //          2^(s + log2 vs - r) (512 new tokens of two sequences over 16,000 fp8 positions:
-//          307 us with every tile alike, 703 us with every tile apart)
+//          305 us with every tile alike, 651 us with every tile apart)
 // r is a row's own reference: the running maximum of s + eV (s + log2 vs) over what the row
 // sees, so that neither a position of little weight nor a hidden one moves the other
 // positions' weights out of f16's range, whatever the scales are.  It stands kBoost powers
@@ -84,8 +84,7 @@ struct ManyCfg {
   static constexpr int kOffRaw = kOffRing + kStages * kTile;
   static constexpr int kOffRawScales = kOffRaw + kRawStages * kRawTile;
   static constexpr int kOffScales = kOffRawScales + (kRaw ? kRawStages * 2 * KT * 4 : 0);
-  // (a slot: the tile's KT K scales, eV, whether the V scales are apart, the V scales
-  // or, apart, their log2)
+  // (a slot: the tile's KT K scales, eV or kApart, the V scales or, apart, their log2)
   static constexpr int kSlotBytes = 2 * KT * 4 + 16;
   static constexpr int kOffBars = (kOffScales + (kRaw ? kScaleSlots * kSlotBytes : 0) + 127) & ~127;
   static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 6 + 5 * NQ + (kRaw ? kScaleSlots + NQ : 0);
@@ -110,12 +109,14 @@ __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<unsigned>(127 + e) << 23); }
 // A tile's V scales, from the bits of the smallest and the largest: alike if the largest is at
 // most 2^6 times the smallest, finite and below 2^126 (a NaN's bits are above every number's;
-// no position at all: 0 and ~0).  eV of a largest scale: 2^(eV - 1) <= x < 2^eV (subnormal
-// ones less).
-__device__ __forceinline__ bool scales_alike(unsigned small, unsigned big) {
-  return big < 0x7E800000u && (big == 0 || small + (6u << 23) >= big);
-}
+// no position at all: 0 and ~0), and at most 2^80 times below `most`, the largest eV of the
+// part's tiles before: a row's weights, of which its sum takes part, then stay inside f32.
+// eV of a largest scale: 2^(eV - 1) <= x < 2^eV (subnormal ones less).
 __device__ __forceinline__ int scale_exponent(unsigned bits) { return max(-125, static_cast<int>(bits >> 23) - 126); }
+__device__ __forceinline__ bool scales_alike(unsigned small, unsigned big, int most) {
+  return big < 0x7E800000u && (big == 0 || small + (6u << 23) >= big) && scale_exponent(big) >= most - 80;
+}
+constexpr int kApart = 1000;         // stands for eV where the scales are apart
 constexpr float kBoost = 7.0f;       // f16 weights are at most 2^(kBoost + kMaxSlack) = 2^15
 
 // Row halves of an item that hold rows of the sequence.
@@ -550,9 +551,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
         const int k0 = (w.ja + i) * KT;
         const uint32_t s_tmem = tmem + lanes + C::kSCol0 + buf * C::kSCols;
         const uint32_t vidx = tile + 2u * i + 1u;
-        int ev = 0;                               // 8-bit: exponent of the tile's V scales,
-        bool apart = false;                       // whether they differ too much for one,
-        const float* ks = nullptr;                // and the tile's K scales
+        int ev = 0;                               // 8-bit: exponent of the tile's V scales, or kApart
+        const float* ks = nullptr;                // and its K scales
         ok = attn_wait(sfull_bar(buf), (sphase >> buf) & 1u, abort_flag, p);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         sphase ^= 1u << buf;
@@ -562,7 +562,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           ks = reinterpret_cast<const float*>(smem + C::kOffScales + sc * C::kSlotBytes);
           ev = __float_as_int(ks[KT]);
-          apart = __float_as_int(ks[KT + 1]) != 0;
         }
         tc_fence_after_sync();
         const bool edge = k0 < lo_max || k0 + KT > hi_min;
@@ -712,7 +711,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           };
           auto exponents_at = [&](int e, float (&g)[4]) {
             const float4 f = *reinterpret_cast<const float4*>(ks + KT + 4 + e);
-            g[0] = apart ? f.x : ev, g[1] = apart ? f.y : ev, g[2] = apart ? f.z : ev, g[3] = apart ? f.w : ev;
+            g[0] = f.x, g[1] = f.y, g[2] = f.z, g[3] = f.w;
           };
           float most = -INFINITY, vmost = -INFINITY;
 #pragma unroll 1
@@ -758,9 +757,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
           }
           return true;
         };
-        // (also where a row's reference is so far above this tile's scale that its weights, of
-        // which the sum takes part, could leave f32's range)
-        if (C::kRaw && __any_sync(0xffffffffu, apart || (own && top + ev < ref - 90.0f)))
+        if (C::kRaw && ev == kApart)
           ok = softmax_apart();
         else
           ok = edge ? softmax(std::true_type{}) : softmax(std::false_type{});
@@ -836,6 +833,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
       uint32_t idx = 0;
       bool ok = true;
       while (ok && walk.next(p, w)) {
+        const int low = lowest_seen(p, w);
+        int most = -1000;                            // the largest eV so far
         for (int j = w.ja; ok && j < w.jb; ++j) {
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++idx) {
@@ -856,8 +855,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
             // us; one unrolled piece of code for both 341 us, unrolled and apart 316 us).
             auto convert = [&](auto v_tile) {
               constexpr bool kV = decltype(v_tile)::value;
-              const float unit = kV ? exp2_int(-__float_as_int(slot[KT])) : 1.0f;
-              const bool apart = kV && __float_as_int(slot[KT + 1]) != 0;
+              const int ev = kV ? __float_as_int(slot[KT]) : 0;
+              const bool apart = ev == kApart;
+              const float unit = apart ? 1.0f : exp2_int(-ev);
 #pragma unroll 1
               for (int k0 = 0; k0 < kSteps; k0 += kBatch) {
                 uint4 v[kBatch];
@@ -890,11 +890,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
               }
             };
             if (kv == 0) {
-              // The tile's scales, eV and their likeness into its slot, which was last read for the
-              // tile kScaleSlots before, whose V tile has left the ring.
+              // The tile's scales and eV into its slot, which was last read for the tile kScaleSlots
+              // before, whose V tile has left the ring.  (The softmax needs them after the K tile:
+              // the search for eV runs beside its conversion.)
               const float* scales = reinterpret_cast<const float*>(smem + C::kOffRawScales) + rs * 2 * KT;
               // (positions that no row sees, whose scales may be anything, count as 0)
-              const int from = max(0, lowest_seen(p, w) - j * KT);
+              const int from = max(0, low - j * KT);
               unsigned big = 0, small = 0xffffffffu;
 #pragma unroll
               for (int x = 0; x < KT / 32; ++x) {
@@ -910,15 +911,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) attn_many_kernel(const __grid_
               }
               big = __reduce_max_sync(0xffffffffu, big);
               small = __reduce_min_sync(0xffffffffu, small);
-              const bool alike = scales_alike(small, big);
-              if (tid == 0) {
-                slot[KT] = __int_as_float(alike ? scale_exponent(big) : 0);
-                slot[KT + 1] = __int_as_float(!alike);
-              }
+              convert(std::false_type{});
+              const bool alike = scales_alike(small, big, most);
+              most = max(most, scale_exponent(big));
+              if (tid == 0) slot[KT] = __int_as_float(alike ? scale_exponent(big) : kApart);
               if (!alike && tid < KT) slot[KT + 4 + tid] = log2_approx(slot[KT + 4 + tid]);
               __syncwarp();
               if (lane == 0) mbar_arrive(scale_bar(sc));
-              convert(std::false_type{});
             } else {
               // (the slot is whole: other warps wrote parts of it)
               ok = attn_wait(scale_bar(sc), ((idx >> 1) / C::kScaleSlots) & 1u, abort_flag, p);

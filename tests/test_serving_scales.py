@@ -156,6 +156,22 @@ def test_large_v_without_weight_in_whole_items(lib, fmt, dim, n, more, where):
 
 @FMT
 @DIM
+@pytest.mark.parametrize("n", [1, 30, 80])
+@pytest.mark.parametrize("step", [-13, -6, 6, 13])
+def test_tiles_of_different_size_in_whole_items(lib, fmt, dim, n, step):
+    """Sizes up to 2^104 apart among tiles that one block walks."""
+    p = Paged(lib, [(n, 600)] * 160, 8, 2, dim, 32, fmt, seed=dim + n)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    for b in (3, 158):
+        e = ((torch.arange(600, device=DEV) // 64 - 4) * step).double()[:, None, None]
+        fill(p, lib, b, v=_rows(p, g) * 2.0 ** e)
+    out, lse = run(p, lib)
+    for b in (3, 158):
+        check8(p, out, lse, b)
+
+
+@FMT
+@DIM
 @NEW
 @pytest.mark.parametrize("what", ["2^26", "nan"])
 def test_large_and_broken_hidden_v(lib, fmt, dim, n, what):
