@@ -452,7 +452,7 @@ lora_status_t lora_set_split_tail(int mode);
 int lora_split_tail(void);
 
 /* Test hook for the failure path (no counterpart in the pages): the next `launches`
- * GEMM launches (0 .. 64; 0 cancels) each leave the first pipeline stage of every
+ * GEMM or paged-attention launches (0 .. 64; 0 cancels) each leave the first pipeline stage of every
  * CTA's first tile unfilled, so the waits on it expire after the wait limit and the
  * call reports LORA_ERR_TIMEOUT through the status word.  Nothing faults, traps or
  * hangs: the waits are the bounded ones above.  Returns LORA_ERR_INVALID_ARG out of

@@ -246,7 +246,7 @@ def split_tail() -> int:
 
 
 def test_expire_waits(launches: int):
-    """Failure-path tests: the next `launches` GEMM launches let a bounded wait expire."""
+    """Failure-path tests: the next `launches` GEMM or attention launches let a bounded wait expire."""
     _check(load().lora_test_expire_waits(launches), "lora_test_expire_waits")
 
 

@@ -7,14 +7,17 @@ namespace lgb {
 // Which kernel: the one whose tiles the rows fill.  A call's lengths are on the device, so
 // the rule takes the mean number of query rows that share a cache head.  Returns the row
 // halves of the tcgen05 kernel, or 0 for the few-row kernel.  Measured with 64 sequences of
-// 4096 positions, eight cache heads of 128 features (us):
+// 4096 positions, eight cache heads of 128 features (us, single calls on cold caches):
 //   rows of a cache head        4    16    20   128   132   256
-//   bf16  few-row kernel      168   171   323  1245  1391  2456
-//         one row half        165   168   169   185   331   340
-//         two row halves      176   180   182   197   220   232
-//   fp8   few-row kernel      146   151   274  1055  1184  2088
-//         one row half        251   266   268   280   510   532
-//         two row halves      258   268   269   278   336   345
+//   bf16  few-row kernel      186   188   341  1265  1405  2490
+//         one row half        186   188   190   199   353   359
+//         two row halves      191   195   197   209   227   238
+//   fp8   few-row kernel      151   156   281  1067  1195  2103
+//         one row half        261   281   282   291   525   550
+//         two row halves      264   275   275   285   338   353
+// (bf16 with few rows: either; the few-row kernel keeps more bits of the weights.)  The mean
+// counts idle sequences too, so a chunk among many of them, or among many single tokens, can
+// go to the few-row kernel: right, but slower by the columns to the right.
 // head_dim 256 has one half: two outputs would fill the tensor memory.
 static int row_halves(int64_t M, int64_t n_seqs, int group, int head_dim) {
   if (M * group <= kFewRows * n_seqs) return 0;
