@@ -403,6 +403,121 @@ lora_status_t lora_paged_attention(int64_t M, int heads_q, const lora_heads_t* q
                                    const lora_paged_batch_t* batch, float scale, int causal, int64_t window,
                                    void* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------- the rest of a training step
+ * What a step runs around the block's projections: the norms before them, the loss behind
+ * the last block, and the clipping of the adapters' gradients.
+ *
+ * RMS norm, with the residual's addition before it.  A row is one token's head of the views
+ * (heads == 1: one token), `dim` features:
+ *   s = x + residual, rounded to bf16 (residual NULL or data NULL: s = x)
+ *   rstd = (mean s^2 + eps)^(-1/2),   y = s * rstd * (weight + offset)
+ * The norm is of s as it is rounded.  f32 arithmetic; y is rounded once.
+ * - sum receives s (required with a residual; NULL or data NULL without one).  It may be x or
+ *   the residual itself; any other overlap of an output with an input is undefined, but that
+ *   without a residual a dense x may be y.
+ * - weight bf16 [dim]; offset is added to it in f32 (1 for weights stored around zero).
+ * - y dense [M x heads x dim]: bf16 (LORA_NORM_BF16), or e4m3 codes with a scale for each row
+ *   (LORA_NORM_FP8): scale = max(amax|y| * (1/448), the smallest normal f32), codes =
+ *   rn(y * (1 / scale)) of the y that was not rounded; a row whose y holds an infinity or a
+ *   NaN gets the scale NaN and codes 0.  Codes are 8-byte aligned.  y_scale f32 [M x heads], NULL
+ *   with LORA_NORM_BF16.
+ * - rstd f32 [M x heads], or NULL (inference).
+ * dim a multiple of 8, at most 32768.  M * heads at most 2^31 - 1.  ws: at least 256 bytes. */
+typedef enum { LORA_NORM_BF16 = 0, LORA_NORM_FP8 = 1 } lora_norm_format_t;
+lora_status_t lora_rms_norm(int64_t M, int dim, const lora_heads_t* x, const lora_heads_t* residual,
+                            const void* weight, float offset, float eps, int format, const lora_heads_t* sum,
+                            void* y, float* y_scale, float* rstd, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Gradients of <dy, y> + <ds, s>, s and rstd the forward's (s its sum, or x without a residual):
+ *   dx = ds + rstd * (g - s * rstd^2 * mean(g * s)),  g = dy * (weight + offset)
+ *   dweight = sum over the rows of dy * s * rstd
+ * dx, dense bf16 [M x heads x dim], is the gradient of x and of the residual.  ds NULL or
+ * data NULL: none.  dweight bf16 [dim], or NULL (a frozen weight's gradient is skipped); its
+ * f32 sums run in an order that depends on the sizes and the device alone.  dx may be dy or ds where
+ * they are dense.  M == 0 sets dweight to zero.  ws: lora_rms_norm_workspace_bytes (0 for
+ * sizes that the calls refuse). */
+size_t lora_rms_norm_workspace_bytes(int64_t M, int64_t heads, int dim);
+lora_status_t lora_rms_norm_backward(int64_t M, int dim, const lora_heads_t* dy, const lora_heads_t* s,
+                                     const void* weight, float offset, const float* rstd, const lora_heads_t* ds,
+                                     void* dx, void* dweight, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Cross entropy of a frozen head, from the hidden rows to the loss and their gradient without
+ * keeping the logits ("Model Patches and Kernels", section "Fused linear cross-entropy":
+ * logit scaling, softcap; "Cross-entropy": label smoothing; a frozen weight's gradient is
+ * skipped).  x bf16 [M x h], W bf16 [vocab x h], labels int64 [M]:
+ *   z = logit_scale * x W^T,   z' = softcap * tanh(z / softcap)  (softcap 0: z' = z)
+ *   lse_m = ln sum_v e^(z'_v),   loss_m = lse_m - (1 - smoothing) z'_y - smoothing * mean_v z'_v
+ *   total = sum_m loss_m, divided for LORA_LOSS_MEAN by the number of labelled tokens (by 1 if
+ *   there is none)
+ *   dx = the gradient of total with respect to x
+ * A token whose label is ignore_index has no part in it: its loss, lse and dx row are 0 and its
+ * x is not used.  So has one whose label is outside [0, vocab), which is reported
+ * (LORA_ERR_DEVICE_INPUT).  loss, lse f32 [M], or NULL; total f32 [1]; dx bf16 [M x h], or
+ * NULL (the loss alone).  dx may not be x.
+ * Logits, their exponentials and all sums are f32.  For dx the exponentials of all but the
+ * label's are rounded to bf16 on their way to the product with W, the label's stays f32.
+ * Tokens are taken in pieces of up to 1 GiB of such exponentials, which live in the
+ * workspace.  h a multiple of 8; x, W, dx 16-byte aligned.  logit_scale finite, not 0;
+ * softcap finite, >= 0; 0 <= smoothing < 1.
+ * ws: lora_linear_ce_workspace_bytes (0 for sizes or options that the call refuses), which
+ * grows with M by x's own size and the pieces. */
+typedef enum { LORA_LOSS_SUM = 0, LORA_LOSS_MEAN = 1 } lora_loss_reduction_t;
+typedef struct {
+  float logit_scale;
+  float softcap;
+  float smoothing;
+  int reduction;            /* lora_loss_reduction_t */
+  int64_t ignore_index;
+} lora_ce_t;
+size_t lora_linear_ce_workspace_bytes(int64_t M, int64_t h, int64_t vocab, const lora_ce_t* opts, int want_dx);
+lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, const void* x, const void* W,
+                             const int64_t* labels, const lora_ce_t* opts, float* loss, float* lse, float* total,
+                             void* dx, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* A tensor of a list: count elements, one after the other, aligned to their own size.  The
+ * list itself is host memory and is copied by the call (into the launch, so that a captured
+ * call keeps it). */
+typedef enum { LORA_BF16 = 0, LORA_F32 = 1 } lora_dtype_t;
+typedef struct {
+  void* data;               /* may be NULL where count is 0 */
+  int64_t count;
+  int dtype;                /* lora_dtype_t */
+} lora_tensor_t;
+
+/* The norm of all tensors of a list together: (sum g^2)^(1/2) (LORA_GRAD_NORM_2) or max |g|
+ * (LORA_GRAD_NORM_INF; a NaN if there is one), f32 [1], 0 for a list of nothing.  Squares are f32,
+ * so an element beyond 1.8e19 makes the first kind infinite; sums over more than a
+ * block are f64, in a fixed order.
+ * lora_clip_grads: out_i = g_i * min(1, max_norm / (norm + 1e-6)), rounded once to its type;
+ * norm receives the norm before it.  A norm that is not finite goes into the factor as it is:
+ * infinite gives 0 (and NaN for an infinite element), NaN gives NaN.  out: NULL (in place, and
+ * nothing is written where the factor is 1) or a list like grads (counts and types), whose
+ * tensors overlap no other tensor of grads or out but may be the same one of grads.
+ * max_norm > 0 (infinity: out is a copy).  Neither synchronises.  n at most 2^20 tensors.
+ * ws: lora_grad_norm_workspace_bytes(n) (0 for n that the calls refuse). */
+typedef enum { LORA_GRAD_NORM_2 = 0, LORA_GRAD_NORM_INF = 1 } lora_grad_norm_t;
+size_t lora_grad_norm_workspace_bytes(int64_t n);
+lora_status_t lora_grad_norm(int64_t n, const lora_tensor_t* grads, int norm_type, float* norm, void* ws,
+                             size_t ws_bytes, cudaStream_t stream);
+lora_status_t lora_clip_grads(int64_t n, const lora_tensor_t* grads, const lora_tensor_t* out, int norm_type,
+                              float max_norm, float* norm, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* DP-SGD's clipped sum of per-example gradients (those of lora_mlp_backward_per_example and
+ * whatever else belongs to the same examples): each tensor of grads holds n_examples gradients
+ * of count / n_examples elements, example-major, and
+ *   out_i = scale * sum_e c_e g_i[e],   c_e = min(1, max_norm / (sum_i |g_i[e]|^2)^(1/2))
+ * out: n tensors of f32, of count / n_examples elements each, that overlap nothing else.
+ * sq_norms f32 [n_examples] holds the examples' squared norms: norms_given != 0 reads them (as
+ * lora_mlp_backward_per_example gives them, added over its calls), else the call writes them.
+ * Sums are f32 over a fixed order of the examples (the norms' over blocks in f64).  An example
+ * whose norm is not finite makes the sums NaN where its factor or its elements do.
+ * max_norm > 0, scale finite; n_examples at most 65535.
+ * ws: lora_clip_examples_workspace_bytes(n, n_examples) (0 for what the call refuses). */
+size_t lora_clip_examples_workspace_bytes(int64_t n, int64_t n_examples);
+lora_status_t lora_clip_examples(int64_t n, const lora_tensor_t* grads, int64_t n_examples, const lora_tensor_t* out,
+                                 float max_norm, float scale, float* sq_norms, int norms_given, void* ws,
+                                 size_t ws_bytes, cudaStream_t stream);
+
 /* ---------------------------------------------------------------- status, counters
  * lora_poll_status: synchronises `stream`, reads the asynchronous status word in
  * ws, clears it, and returns LORA_OK, LORA_ERR_TIMEOUT or LORA_ERR_DEVICE_INPUT
@@ -476,7 +591,10 @@ enum {
   LORA_KIND_DGRAD = 7,       /* input-gradient GEMM (dx, d o_in) */
   LORA_KIND_ROPE = 8,        /* RoPE transpose rotation of dy_q, dy_k; RoPE tables; lora_rotary */
   LORA_KIND_CACHE = 9,       /* cache writes and reads */
-  LORA_KIND_ATTN = 10        /* attention over the cache, and the joining of its split sums */
+  LORA_KIND_ATTN = 10,       /* attention over the cache, and the joining of its split sums */
+  LORA_KIND_NORM = 11,       /* RMS norm and its gradient */
+  LORA_KIND_LOSS = 12,       /* the linear cross entropy: its GEMMs and what stands between them */
+  LORA_KIND_CLIP = 13        /* gradient norms and clipping */
 };
 lora_status_t lora_trace_enable(int capacity);
 int lora_trace_read(int* kind, float* ms, int max);

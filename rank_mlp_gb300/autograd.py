@@ -3,7 +3,8 @@ call ``loss.backward()``.
 
 They only route tensors: the forward and backward of each function are one call each
 of ``lora_mlp_forward/backward``, ``lora_qkvo_forward/backward`` (the Q/K/V half),
-``lora_linear_forward/backward`` and ``lora_rotary`` (both ways).  The base weights W are frozen ("Model Patches and
+``lora_linear_forward/backward``, ``lora_rotary`` (both ways), ``lora_rms_norm`` and its
+backward, and ``lora_linear_ce``, whose one call gives the loss and the gradient.  The base weights W are frozen ("Model Patches and
 Kernels": a frozen weight gets no gradient), so they never receive a gradient; the
 adapters A, B and the input x do.  Inputs may carry leading batch dimensions
 ([..., features]); every tensor is bf16 on the GPU.
@@ -12,6 +13,7 @@ adapters A, B and the input x do.  Inputs may carry leading batch dimensions
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding
 
@@ -114,6 +116,69 @@ class RotaryFunction(torch.autograd.Function):
         return *grads, None, None
 
 
+class RmsNormFunction(torch.autograd.Function):
+    """(y, s) of ``binding.rms_norm`` in bf16 with a residual, or y without one, over rows [..., dim] (or
+    views of heads [tokens, heads, dim]).  The gradient that reaches s is added in the same call; a
+    weight that needs no gradient gets none."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps: float, offset: float):
+        x2, r2 = _tokens(x), None if residual is None else _tokens(residual)
+        y, s, rstd = binding.rms_norm(x2, weight, residual=r2, eps=eps, offset=offset, training=True)
+        ctx.save_for_backward(s, weight, rstd)
+        ctx.offset, ctx.xshape = offset, x.shape
+        ctx.set_materialize_grads(False)
+        return y.reshape(x.shape) if residual is None else (y.reshape(x.shape), s.reshape(x.shape))
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, ds=None):
+        s, weight, rstd = ctx.saved_tensors
+        need_x, need_w, need_r = ctx.needs_input_grad[:3]
+        if dy is None:
+            return ds if need_x else None, None, ds if need_r else None, None, None
+        dx, dw = binding.rms_norm_backward(_strided(_bf16(dy).reshape(s.shape)), s, weight, rstd, offset=ctx.offset,
+                                           ds=None if ds is None else _strided(_bf16(ds).reshape(s.shape)), dweight=need_w)
+        dx = dx.reshape(ctx.xshape)
+        return dx if need_x else None, dw, dx if need_r else None, None, None
+
+
+class LinearCrossEntropyFunction(torch.autograd.Function):
+    """``binding.linear_cross_entropy`` over rows [..., h] and labels [...]: the total, or with reduction
+    "none" each token's loss.  The forward's call computes the gradient too, where x needs one;
+    the backward scales it.  W is frozen."""
+
+    @staticmethod
+    def forward(ctx, x, W, labels, scale, softcap, smoothing, ignore_index, reduction):
+        ctx.xshape, ctx.none = x.shape, reduction == "none"
+        total, loss, _, dx = binding.linear_cross_entropy(
+            _flat(x), W, labels.reshape(-1).contiguous(), scale=scale, softcap=softcap, smoothing=smoothing,
+            ignore_index=ignore_index, reduction="sum" if ctx.none else reduction, grad=ctx.needs_input_grad[0])
+        ctx.save_for_backward(dx)
+        return loss.reshape(labels.shape) if ctx.none else total
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        dx, = ctx.saved_tensors
+        # one rounding more where g is no power of two
+        dx = (dx * g.reshape(-1, 1)).to(torch.bfloat16) if ctx.none else dx * g
+        return dx.reshape(ctx.xshape), None, None, None, None, None, None, None
+
+
+def _tokens(t):
+    """t as rows [tokens, dim] or a view of heads [tokens, heads, dim] that the library takes."""
+    if t.dim() == 2 or (t.dim() == 3 and not t.is_contiguous()):
+        return _strided(t)
+    return _flat(t)
+
+
+def _strided(t):
+    """t, or a copy where its strides do not suit the library."""
+    fits = t.stride(-1) == 1 and all(s % 8 == 0 for s in t.stride()[:-1]) and t.data_ptr() % 16 == 0
+    return t if fits else t.contiguous()
+
+
 def _rows(d):
     """d as a view of heads that the library takes."""
     fits = d.stride(-1) == 1 and all(s % 8 == 0 for s in d.stride()[:2]) and d.data_ptr() % 16 == 0
@@ -123,6 +188,17 @@ def _rows(d):
 def lora_rotary(q, k, rope):
     """(rotated q, rotated k), or the rotated q alone where k is None."""
     return RotaryFunction.apply(q, k, rope)
+
+
+def lora_rms_norm(x, weight, residual=None, eps=1e-6, offset=0.0):
+    """y, or with a residual (y, x + residual)."""
+    return RmsNormFunction.apply(x, weight, residual, eps, offset)
+
+
+def lora_linear_cross_entropy(x, W, labels, *, scale=1.0, softcap=0.0, smoothing=0.0, ignore_index=-100,
+                              reduction="mean"):
+    """The loss of a frozen head W over x: reduction "mean" over the labelled tokens, "sum" or "none"."""
+    return LinearCrossEntropyFunction.apply(x, W, labels, scale, softcap, smoothing, ignore_index, reduction)
 
 
 def lora_mlp(x, gate, up, down, s, act="swiglu"):

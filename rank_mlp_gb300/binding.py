@@ -22,10 +22,14 @@ from . import build as _build
 
 ACT = {"swiglu": 0, "geglu_tanh": 1, "geglu_erf": 2}
 KIND_NAMES = {0: "pack", 1: "reduce", 2: "rank_proj", 3: "rank_grad", 4: "gate_up",
-              5: "proj", 6: "act_bwd", 7: "dgrad", 8: "rope", 9: "cache", 10: "attn"}
+              5: "proj", 6: "act_bwd", 7: "dgrad", 8: "rope", 9: "cache", 10: "attn", 11: "norm", 12: "loss",
+              13: "clip"}
 LAYOUT = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
 KV_FORMAT = {torch.bfloat16: 0, torch.float8_e4m3fn: 1, torch.int8: 2}
+NORM_FORMAT = {"bf16": 0, "fp8": 1}
+LIST_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+GRAD_NORM = {2.0: 0, float("inf"): 1}
 KV_DTYPE = {"bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn, "int8": torch.int8}
 STATUS = {0: "ok", 1: "invalid argument", 2: "alignment", 3: "unsupported",
           4: "workspace too small", 5: "CUDA error", 6: "timeout", 7: "device input out of range"}
@@ -77,6 +81,15 @@ class LoraPagedBatch(ctypes.Structure):
                 ("kv_len", ctypes.c_void_p), ("cu_q", ctypes.c_void_p)]
 
 
+class LoraCe(ctypes.Structure):
+    _fields_ = [("logit_scale", ctypes.c_float), ("softcap", ctypes.c_float), ("smoothing", ctypes.c_float),
+                ("reduction", ctypes.c_int), ("ignore_index", ctypes.c_int64)]
+
+
+class LoraTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("count", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
 _LIB = None
 _LOCK = threading.Lock()
 _I64, _INT, _F32, _VP, _SZ = ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
@@ -113,6 +126,16 @@ _SIGS = {
     "lora_kv_read": (_INT, [_I64, _I64, _VP, _VP, _I64, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "lora_paged_attention_workspace_bytes": (_SZ, [_I64, _I64, _INT, _VP]),
     "lora_paged_attention": (_INT, [_I64, _INT, _VP, _VP, _VP, _F32, _INT, _I64, _VP, _VP, _VP, _SZ, _VP]),
+    "lora_rms_norm": (_INT, [_I64, _INT, _VP, _VP, _VP, _F32, _F32, _INT, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "lora_rms_norm_workspace_bytes": (_SZ, [_I64, _I64, _INT]),
+    "lora_rms_norm_backward": (_INT, [_I64, _INT, _VP, _VP, _VP, _F32, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "lora_linear_ce_workspace_bytes": (_SZ, [_I64, _I64, _I64, _VP, _INT]),
+    "lora_linear_ce": (_INT, [_I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "lora_grad_norm_workspace_bytes": (_SZ, [_I64]),
+    "lora_grad_norm": (_INT, [_I64, _VP, _INT, _VP, _VP, _SZ, _VP]),
+    "lora_clip_grads": (_INT, [_I64, _VP, _VP, _INT, _F32, _VP, _VP, _SZ, _VP]),
+    "lora_clip_examples_workspace_bytes": (_SZ, [_I64, _I64]),
+    "lora_clip_examples": (_INT, [_I64, _VP, _I64, _VP, _F32, _F32, _VP, _INT, _VP, _SZ, _VP]),
     "lora_poll_status": (_INT, [_VP, _VP]),
     "lora_status_string": (ctypes.c_char_p, [_INT]),
     "lora_launch_count": (ctypes.c_uint64, []),
@@ -772,3 +795,209 @@ def paged_attention(q, cache: KVCache, batch: PagedBatch, *, scale=None, causal=
     _check(lib.lora_paged_attention(tokens, hq, view, cache._at, batch._at, dim ** -0.5 if scale is None else scale,
                                     int(causal), window, out_at, lse_at, wp, wn, stream), "lora_paged_attention")
     return out
+
+
+# ------------------------------------------------------------------ norm, loss, clipping
+
+def _rows(t, name):
+    """Rows [tokens, dim], or a view of heads [tokens, heads, dim], as (lora_heads_t, heads)."""
+    if isinstance(t, torch.Tensor) and t.dim() == 2:
+        t = t.unsqueeze(1)
+    return _heads(t, name), t.shape[1]
+
+
+def _weight(w, dim, name="weight"):
+    if isinstance(w, torch.Tensor) and w.shape != (dim,):
+        raise ValueError(f"{name} must be [{dim}] (got {tuple(w.shape)})")
+    return _dev(w, name)
+
+
+def rms_norm(x, weight, *, residual=None, eps=1e-6, offset=0.0, format="bf16", training=False, sum_out=None, out=None,
+             ws=None):
+    """RMS norm of the rows of x [tokens, dim] (or of the heads of a view [tokens, heads, dim]), after adding
+    the residual if there is one.  Returns (y, s, rstd): s = x + residual in bf16 (x itself without one; sum_out,
+    which may be x or residual, receives it), y = s * rstd * (weight + offset) in bf16, or with format "fp8" the
+    pair (e4m3 codes, f32 scale of each row); rstd, f32, is what the gradient needs (None unless training)."""
+    lib = _LIB or load()
+    view, heads = _rows(x, "x")
+    shape = x.shape
+    tokens, dim = shape[0], shape[-1]
+    w_at = _weight(weight, dim)
+    dev = x.device
+    res = total = None
+    if residual is not None:
+        if residual.shape != shape:
+            raise ValueError("residual must have x's shape")
+        res = _rows(residual, "residual")[0]
+        if sum_out is None:
+            sum_out = torch.empty(shape, dtype=_BF16, device=dev)
+        elif sum_out.shape != shape:
+            raise ValueError("sum_out must have x's shape")
+        total = _rows(sum_out, "sum_out")[0]
+    elif sum_out is not None:
+        raise ValueError("sum_out receives x + residual: there is no residual")
+    code = NORM_FORMAT[format]
+    scale = None if code == 0 else torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    dtype = _BF16 if code == 0 else torch.float8_e4m3fn
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    elif out.shape != shape or out.dtype != dtype or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {dtype} tensor of x's shape")
+    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if training else None
+    _together(x, weight, residual, sum_out, out, ws)
+    stream, wp, wn = _call(x, 256, ws)
+    _check(lib.lora_rms_norm(tokens, dim, view, res, w_at, offset, eps, code, total, out.data_ptr(),
+                             None if scale is None else scale.data_ptr(), None if rstd is None else rstd.data_ptr(),
+                             wp, wn, stream), "lora_rms_norm")
+    return (out if scale is None else (out, scale)), (x if residual is None else sum_out), rstd
+
+
+def rms_norm_backward(dy, s, weight, rstd, *, offset=0.0, ds=None, dweight=True, dx=None, ws=None):
+    """(dx, dweight) of rms_norm from dy, the gradient of y, and ds, the gradient that reaches s from elsewhere
+    (or None).  s and rstd are the forward's.  dx (bf16, dense; may be passed in, dy or ds among others) is the
+    gradient of x and of the residual; dweight is bf16 [dim], or None where it is not asked for."""
+    lib = _LIB or load()
+    view, heads = _rows(s, "s")
+    shape = s.shape
+    tokens, dim = shape[0], shape[-1]
+    w_at = _weight(weight, dim)
+    if dy.shape != shape or (ds is not None and ds.shape != shape):
+        raise ValueError("dy and ds must have s's shape")
+    if dx is None:
+        dx = torch.empty(shape, dtype=_BF16, device=s.device)
+    elif dx.shape != shape:
+        raise ValueError("dx must have s's shape")
+    dw = torch.empty(dim, dtype=_BF16, device=s.device) if dweight else None
+    _together(s, dy, weight, rstd, ds, dx, ws)
+    stream, wp, wn = _call(s, lib.lora_rms_norm_workspace_bytes(tokens, heads, dim), ws)
+    _check(lib.lora_rms_norm_backward(tokens, dim, _rows(dy, "dy")[0], view, w_at, offset,
+                                      _ints(rstd, torch.float32, shape[:-1], "rstd"),
+                                      None if ds is None else _rows(ds, "ds")[0], _dev(dx, "dx"),
+                                      None if dw is None else dw.data_ptr(), wp, wn, stream), "lora_rms_norm_backward")
+    return dx, dw
+
+
+def linear_cross_entropy(x, W, labels, *, scale=1.0, softcap=0.0, smoothing=0.0, ignore_index=-100, reduction="mean",
+                         grad=True, dx=None, ws=None):
+    """Cross entropy of the logits scale * x W^T (softcap > 0: capped by a tanh) of a frozen head W [vocab, h] over
+    x [tokens, h], with int64 labels [tokens], and its gradient, without keeping the logits.  Returns (total, loss,
+    lse, dx): total f32 (0-dim), the mean over the labelled tokens or the "sum"; loss and lse f32 [tokens] (0 where
+    the label is ignore_index); dx the gradient of total with respect to x, or None without grad."""
+    lib = _LIB or load()
+    if x.dim() != 2 or W.dim() != 2 or W.shape[1] != x.shape[1]:
+        raise ValueError("x must be [tokens, h] and W [vocab, h]")
+    tokens, h = x.shape
+    vocab, dev = W.shape[0], x.device
+    if reduction not in ("mean", "sum"):
+        raise ValueError('reduction must be "mean" or "sum"')
+    opts = LoraCe(scale, softcap, smoothing, 1 if reduction == "mean" else 0, ignore_index)
+    e = lambda *sh: torch.empty(sh, dtype=torch.float32, device=dev)  # noqa: E731
+    total, loss, lse = e(), e(tokens), e(tokens)
+    if not grad:
+        dx = None
+    elif dx is None:
+        dx = torch.empty(tokens, h, dtype=_BF16, device=dev)
+    elif dx.shape != x.shape:
+        raise ValueError("dx must have x's shape")
+    args = (_dev(x, "x"), _dev(W, "W"), _ints(labels, torch.int64, (tokens,), "labels"))
+    _together(x, W, labels, dx, ws)
+    need = lib.lora_linear_ce_workspace_bytes(tokens, h, vocab, _at(opts), int(grad))
+    stream, wp, wn = _call(x, need, ws)
+    _check(lib.lora_linear_ce(tokens, h, vocab, *args, _at(opts), loss.data_ptr(), lse.data_ptr(), total.data_ptr(),
+                              _opt(dx, "dx"), wp, wn, stream), "lora_linear_ce")
+    return total, loss, lse, dx
+
+
+class TensorList:
+    """The tensors of a call that takes many: contiguous bf16 or f32 tensors on one device, in an order
+    that stays.  A program whose gradients stay where they are builds it once."""
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        self._structs = (LoraTensor * max(1, len(self.tensors)))()
+        for i, t in enumerate(self.tensors):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("a list's entries must be torch.Tensors")
+            if t.dtype not in LIST_DTYPE or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"a list's tensors must be contiguous bf16 or f32 CUDA tensors (entry {i}: {t.dtype}, "
+                                 f"{t.device}, strides {t.stride()})")
+            if t.get_device() != self.tensors[0].get_device():
+                raise ValueError("a list's tensors must be on one device")
+            self._structs[i] = LoraTensor(t.data_ptr(), t.numel(), LIST_DTYPE[t.dtype])
+        self._at = _at(self._structs)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def tensor_list(tensors) -> TensorList:
+    return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+
+
+def _list_device(grads):
+    """A tensor of the list's device, or of the current one for an empty list."""
+    return grads.tensors[0] if grads.tensors else torch.empty(0, device=torch.device("cuda", _current_device()))
+
+
+def grad_norm(grads, *, norm_type=2.0, ws=None):
+    """The norm of all gradients together (a TensorList, or any iterable of tensors), f32, 0-dim: norm_type 2
+    or infinity."""
+    lib = _LIB or load()
+    grads = tensor_list(grads)
+    t = _list_device(grads)
+    _together(t, ws)
+    norm = torch.empty((), dtype=torch.float32, device=t.device)
+    stream, wp, wn = _call(t, lib.lora_grad_norm_workspace_bytes(len(grads)), ws)
+    _check(lib.lora_grad_norm(len(grads), grads._at, GRAD_NORM[float(norm_type)], norm.data_ptr(), wp, wn, stream),
+           "lora_grad_norm")
+    return norm
+
+
+def clip_grad_norm(grads, max_norm, *, norm_type=2.0, out=None, ws=None):
+    """Scales all gradients by min(1, max_norm / (norm + 1e-6)), in place or into out (a list of the same shapes and
+    types).  Returns their norm before that, f32, 0-dim."""
+    lib = _LIB or load()
+    grads = tensor_list(grads)
+    t = _list_device(grads)
+    if out is not None:
+        out = tensor_list(out)
+        if len(out) != len(grads):                   # (sizes and types are compared in the library)
+            raise ValueError("out must match the gradients, tensor by tensor")
+        if out.tensors:
+            _together(t, out.tensors[0])
+    _together(t, ws)
+    norm = torch.empty((), dtype=torch.float32, device=t.device)
+    stream, wp, wn = _call(t, lib.lora_grad_norm_workspace_bytes(len(grads)), ws)
+    _check(lib.lora_clip_grads(len(grads), grads._at, None if out is None else out._at, GRAD_NORM[float(norm_type)],
+                               max_norm, norm.data_ptr(), wp, wn, stream), "lora_clip_grads")
+    return norm
+
+
+def clip_examples(grads, max_norm, *, sq_norms=None, scale=1.0, out=None, ws=None):
+    """DP-SGD's clipped sum: grads are tensors [examples, ...] of per-example gradients (mlp_backward_per_example's, of
+    any number of calls); returns (sums, sq_norms) with sums[i] = scale * sum_e min(1, max_norm / |example e|)
+    grads[i][e], f32.  sq_norms, f32 [examples]: the squared norms if they are known (mlp_backward_per_example's, added
+    up), else computed.  out: the f32 tensors for sums."""
+    lib = _LIB or load()
+    grads = tensor_list(grads)
+    if not grads.tensors:
+        raise ValueError("clip_examples needs a gradient")
+    first = grads.tensors[0]
+    if any(g.dim() < 1 or g.shape[0] != first.shape[0] for g in grads.tensors):
+        raise ValueError("all gradients must be of the same examples (their first extent)")
+    n, dev = first.shape[0], first.device
+    if out is None:
+        out = [torch.empty(g.shape[1:], dtype=torch.float32, device=dev) for g in grads.tensors]
+    sums = tensor_list(out)
+    if len(sums) != len(grads) or any(o.shape != g.shape[1:] or o.dtype != torch.float32
+                                      for o, g in zip(sums.tensors, grads.tensors)):
+        raise ValueError("out must be f32 tensors of one example's shapes")
+    given = sq_norms is not None
+    if not given:
+        sq_norms = torch.empty(n, dtype=torch.float32, device=dev)
+    sq_at = _ints(sq_norms, torch.float32, (n,), "sq_norms")
+    _together(first, sums.tensors[0], sq_norms, ws)
+    stream, wp, wn = _call(first, lib.lora_clip_examples_workspace_bytes(len(grads), n), ws)
+    _check(lib.lora_clip_examples(len(grads), grads._at, n, sums._at, max_norm, scale, sq_at, int(given), wp, wn, stream),
+           "lora_clip_examples")
+    return list(sums.tensors), sq_norms

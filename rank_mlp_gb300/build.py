@@ -20,7 +20,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB_NAME = "liblora_gb300.so"
 SOURCES = ("lora_api.cu", "lora_linear.cu", "lora_mlp.cu", "lora_qkvo.cu", "gemm_big.cu", "gemm_skinny.cu",
-           "noalloc.cu", "rotary.cu", "kv_cache.cu", "paged_attn.cu",
+           "noalloc.cu", "rms_norm.cu", "linear_ce.cu", "gemm_ce.cu", "grad_clip.cu", "rotary.cu", "kv_cache.cu", "paged_attn.cu",
            "attn_few.cu", "attn_many.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

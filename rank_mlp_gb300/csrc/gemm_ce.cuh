@@ -1,0 +1,489 @@
+// The linear cross entropy's GEMMs on CTA pairs (256 x 256 tiles, tcgen05 cta_group::2), and
+// what they share with the kernels between them (linear_ce.cu).
+//
+// Logits never leave the chip as such.  One GEMM multiplies the hidden rows by the head's
+// K-major rows and its epilogue, a row a thread, turns a tile's 256 logits into
+//   CE_STATS   the row's maximum and sum of exponentials relative to it
+//   CE_GRAD    the row's exponentials relative to a reference known beforehand, stored in bf16
+//              (and their sum and maximum)
+// the other, CE_PART, multiplies those exponentials by the head read MN-major.
+//
+// With e_v = 2^(z_v - ref) the gradient of a row is, up to the row's factor, sum_v e_v W_v / S
+// minus W_y: bf16's range lets e_v keep its relative precision whatever the reference, so the
+// product needs no second pass over the logits once S is known.  The label's own term is left
+// out of e and S: it joins in f32 from the label's logit, where 1 - p_y keeps its precision
+// however near p_y is to 1.
+//
+// Rows are the labelled tokens, packed; their number is on the device, so a launch covers the
+// most rows there can be and its units follow from the number it finds.
+#pragma once
+
+#include "gemm_pair.cuh"
+
+namespace lgb {
+
+enum CeKind : int { CE_STATS = 0, CE_GRAD = 1, CE_PART = 2 };
+
+constexpr int kCeStages = 6;
+constexpr int kCeWarps = 8;              // epilogue warps: two for each TMEM lane quarter
+constexpr int kCeSlots = kCeWarps / 4;   // partial results of a row in one tile
+constexpr int kCeMaxSplits = 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// What a launch finds on the device about its piece of the rows.
+struct CePiece {
+  int live;                // labelled rows of the piece
+  int splits;              // k-ranges of CE_PART
+  unsigned redo;           // CE_GRAD's sums left their range: the launches of the second try run
+  int pad;
+};
+
+// Logits in units of ln 2 from accumulator values: z2 = v * k2, or cap2 * tanh with
+// v * kc = 2 log2(e) x, x the tanh's argument.
+struct CeLogit {
+  float k2, cap2, kc;
+};
+
+struct CeGemmParams {
+  CUtensorMap a, b;
+  const CePiece* piece;
+  int when_redo;           // 1: only if the piece's `redo` is set
+  int kb_total, kvalid;    // 64-wide k-blocks, valid K
+  int tiles_n, band;
+  unsigned* status;
+  unsigned long long timeout_ns;
+  int inject_stall;
+  // CE_STATS, CE_GRAD (arrays start at the piece's first row)
+  int vocab;
+  CeLogit lg;
+  const int* label;
+  const float* ref2;
+  float2* part;            // [tiles_n * kCeSlots][ldp] (maximum, sum), both without the label
+  float* zsum;             // [tiles_n * kCeSlots][ldp] sums of z2, label included, or NULL
+  float* zlab;             // the label's z2
+  long long ldp;
+  __nv_bfloat16* e;        // [rows][lde]
+  long long lde;
+  float minus;             // CE_GRAD: taken off each exponential before the tanh's slope
+  // CE_PART
+  float* slab;             // [splits][tiles][256][256]
+};
+
+// k-ranges a piece's product with the head is cut into: `tiles` tiles of kb k-blocks on `pairs`
+// CTA pairs.  The busiest pair works through ceil(tiles s / pairs) units of kb / s k-blocks; a unit
+// also writes its 256 KB of partial sums and has them read back, at a pair's share of the
+// memory rate about the time of kCeSlabKb k-blocks.
+constexpr int kCeSlabKb = 21;
+constexpr int kCeSlabTiles = 608;        // units of a launch at most, but for the tiles themselves
+__host__ __device__ inline int ce_splits(int tiles, int kb, int pairs) {
+  int best = 1;
+  float least = 3.0e38f;
+  for (int s = 1; s <= kCeMaxSplits; ++s) {
+    if (s > 1 && (tiles * s > kCeSlabTiles || kb < 4 * s)) break;
+    const float cost = static_cast<float>((tiles * s + pairs - 1) / pairs) * (static_cast<float>(kb) / s + kCeSlabKb);
+    if (cost < least * 0.999f) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// z2 of an accumulator value, and with a cap the tanh's slope 1 - tanh^2:
+// q = 2 / (1 + e^(2x)): tanh x = 1 - q, 1 - tanh^2 x = q (2 - q).
+template <bool CAP>
+__device__ __forceinline__ float ce_logit(float v, const CeLogit& lg, float& slope) {
+  if constexpr (!CAP) {
+    slope = 1.0f;
+    return v * lg.k2;
+  } else {
+    const float q = __fdividef(2.0f, 1.0f + exp2_approx(v * lg.kc));
+    slope = q * (2.0f - q);
+    return fmaf(-lg.cap2, q, lg.cap2);
+  }
+}
+
+__device__ __forceinline__ bool ce_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, const CeGemmParams& p) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > p.timeout_ns) {
+      *abort_flag = 1;
+      atomicOr(p.status, kStatusTimeout);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void ce_wait_drain(uint32_t bar, uint32_t parity, const CeGemmParams& p) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > 20000000ull) {
+      atomicOr(p.status, kStatusTimeout);
+      return;
+    }
+  }
+}
+
+// The units of a CTA pair: tiles in bands of n-tiles (the n-tile fastest inside a band), k-range
+// by k-range, so that pairs working at the same time read the same slices.
+struct CeUnit {
+  int tm, tn, split, kb0, kb1;
+};
+struct CeIter {
+  int u, step, end, tiles, tiles_m, splits;
+  __device__ __forceinline__ CeIter(const CeGemmParams& p, int live, int splits_, int pair, int npairs) {
+    tiles_m = (live + 2 * kBM - 1) / (2 * kBM);
+    tiles = tiles_m * p.tiles_n;
+    splits = splits_;
+    u = pair;
+    step = npairs;
+    end = tiles * splits;
+  }
+  __device__ __forceinline__ bool next(const CeGemmParams& p, CeUnit& U) {
+    if (u >= end) return false;
+    U.split = u / tiles;
+    const int t = u - U.split * tiles;
+    const int b = t / (tiles_m * p.band);
+    const int rem = t - b * tiles_m * p.band;
+    const int nb = min(p.band, p.tiles_n - b * p.band);
+    U.tm = rem / nb;
+    U.tn = b * p.band + rem % nb;
+    U.kb0 = static_cast<int>(static_cast<long long>(p.kb_total) * U.split / splits);
+    U.kb1 = static_cast<int>(static_cast<long long>(p.kb_total) * (U.split + 1) / splits);
+    u += step;
+    return true;
+  }
+};
+
+// The epilogue of one tile row: columns [part * 128, part * 128 + 128) of the tile.
+// Warp-collective (tcgen05.ld); `ok`: the row is one of the piece's.
+template <int KIND, bool CAP>
+__device__ __forceinline__ void ce_rows(const CeGemmParams& p, const CeUnit& U, uint32_t tacc, int row, bool ok, int part) {
+  constexpr int BN = 256, kSpan = BN / kCeSlots;
+  const int first = U.tn * BN + part * kSpan;
+  const int label = ok ? __ldg(p.label + row) : -1;
+  const float ref2 = KIND == CE_GRAD && ok ? __ldcg(p.ref2 + row) : 0.0f;
+  float top = -INFINITY, sum = 0.0f, zs = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < kSpan; c += 32) {
+    uint32_t v[32];
+    __syncwarp();
+    tmem_ld32(tacc + part * kSpan + c, v);
+    tmem_ld_wait();
+    const int col0 = first + c;
+    if (col0 >= p.vocab) continue;               // wholly past the vocabulary
+    const int at = label - col0;                 // the label's place in the chunk
+    const int width = p.vocab - col0;            // columns below the vocabulary's size
+    const bool plain = !__any_sync(0xffffffffu, static_cast<unsigned>(at) < 32u) && width >= 32;
+    // z2 of all columns; the label's and those past the vocabulary leave the sums
+    auto chunk = [&](auto tag) {
+      constexpr bool PLAIN = decltype(tag)::value != 0;
+      if constexpr (KIND == CE_STATS) {
+        float z[32], most = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          float slope;
+          z[j] = ce_logit<CAP>(__uint_as_float(v[j]), p.lg, slope);
+          if (!PLAIN) {
+            if (p.zsum != nullptr && j < width) zs += z[j];
+            if (j == at) p.zlab[row] = z[j];
+            if (j == at || j >= width) z[j] = -INFINITY;
+          }
+          most = fmaxf(most, z[j]);
+        }
+        if (PLAIN && p.zsum != nullptr) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) zs += z[j];
+        }
+        if (most > top) {
+          sum *= exp2_approx(top - most);
+          top = most;
+        }
+        const float base = top == -INFINITY ? 0.0f : top;
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          s0 += exp2_approx(z[j] - base);
+          s1 += exp2_approx(z[j + 1] - base);
+        }
+        sum += s0 + s1;
+      } else {
+        uint32_t w[16];
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          float e[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float slope;
+            const float z = ce_logit<CAP>(__uint_as_float(v[j + h]), p.lg, slope);
+            float x = exp2_approx(CAP ? z - ref2 : fmaf(__uint_as_float(v[j + h]), p.lg.k2, -ref2));
+            if (!PLAIN) {
+              if (p.zsum != nullptr && j + h < width) zs += z;
+              if (j + h == at) p.zlab[row] = z;
+              if (j + h == at || j + h >= width) x = 0.0f;
+              else top = fmaxf(top, z);
+            } else {
+              top = fmaxf(top, z);
+            }
+            (h ? s1 : s0) += x;
+            e[h] = CAP ? (x - p.minus) * slope : x;
+            if (!PLAIN && (j + h == at || j + h >= width)) e[h] = 0.0f;
+            if (PLAIN && p.zsum != nullptr) zs += z;
+          }
+          w[j / 2] = pack_bf16x2(e[0], e[1]);
+        }
+        sum += s0 + s1;
+        if (ok) {
+          __nv_bfloat16* dst = p.e + static_cast<long long>(row) * p.lde + col0;
+          if (col0 + 32 <= p.lde) {
+            st_global_v8(dst, w);
+            st_global_v8(dst + 16, w + 8);
+          } else {
+            st_global_v8(dst, w);                // lde is a multiple of 16
+          }
+        }
+      }
+    };
+    if (plain) chunk(ActTag<1>{}); else chunk(ActTag<0>{});
+  }
+  if (ok) {
+    const long long at = (static_cast<long long>(U.tn) * kCeSlots + part) * p.ldp + row;
+    p.part[at] = make_float2(top, sum);
+    if (p.zsum != nullptr) p.zsum[at] = zs;
+  }
+}
+
+template <int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarps), 1)
+    ce_gemm_kernel(const __grid_constant__ CeGemmParams p) {
+  constexpr int STAGES = kCeStages;
+  constexpr bool B_MN = KIND == CE_PART;
+  using C = PairCfg<STAGES, kCeWarps>;
+  constexpr int BN = C::BN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * C::kStageBytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+  const int npairs = static_cast<int>(gridDim.x >> 1);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * kCeWarps);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&p.a);
+    tma_prefetch_map(&p.b);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  cluster_sync_all();                     // both CTAs' barriers exist before any remote arrive
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();                             // the previous kernels' writes are visible from here
+  pdl_launch_dependents();
+  // every thread of the launch reads the same three words: all roles walk the same units
+  const int live = p.when_redo && __ldcg(&p.piece->redo) == 0 ? 0 : __ldcg(&p.piece->live);
+  const int splits = KIND == CE_PART ? __ldcg(&p.piece->splits) : 1;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int armed[STAGES];
+      for (int s = 0; s < STAGES; ++s) armed[s] = -1;
+      bool ok = true, first_stage = true;
+      CeIter it(p, live, splits, pair, npairs);
+      CeUnit U;
+      while (ok && it.next(p, U)) {
+        const int a_row = U.tm * (2 * kBM) + static_cast<int>(rank) * kBM;
+        const int b_row = U.tn * BN + static_cast<int>(rank) * C::kBLocal;
+        for (int j = U.kb0; j < U.kb1; ++j) {
+          const int kc = j * kBK;
+          if (!ce_wait(empty_bar(stage), phase ^ 1u, abort_flag, p)) { ok = false; break; }
+          const uint32_t fb = full_bar(stage);
+          if (p.inject_stall && first_stage && leader) {   // failure-path tests: never arm it
+            first_stage = false;
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            continue;
+          }
+          first_stage = false;
+          if (leader) {
+            mbar_arrive_expect_tx(fb, C::kTxBytes);
+            armed[stage] = static_cast<int>(phase);
+          }
+          const uint32_t fb_even = mapa_shared(fb, 0);
+          const uint32_t sa = sbase + stage * C::kStageBytes;
+          const uint32_t sb = sa + C::kABytes;
+          tma_load_2d_pair(sa, &p.a, fb_even, kc, a_row);
+          if (!B_MN) {
+            tma_load_2d_pair(sb, &p.b, fb_even, kc, b_row);
+          } else {
+#pragma unroll
+            for (int c = 0; c < C::kBLocal / 64; ++c) tma_load_2d_pair(sb + c * 8192u, &p.b, fb_even, b_row + c * 64, kc);
+          }
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok && leader) {
+        for (int s = 0; s < STAGES; ++s)
+          if (armed[s] >= 0) ce_wait_drain(full_bar(s), static_cast<uint32_t>(armed[s]), p);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (leader && lane == 0) {
+      // kept lean as in the projections' kernel: descriptors are stage 0's plus constants, the
+      // next stage is tested before this stage's last MMA
+      constexpr uint32_t idesc = idesc_bf16_f32(2 * kBM, BN, 0, B_MN ? 1 : 0);
+      const uint64_t adesc0 = smem_desc_sw128(sbase, 16u, 1024u);
+      const uint64_t bdesc0 = B_MN ? smem_desc_sw128(sbase + C::kABytes, 8192u, 1024u)
+                                   : smem_desc_sw128(sbase + C::kABytes, 16u, 1024u);
+      constexpr uint64_t kStageStep = C::kStageBytes >> 4;
+      constexpr uint64_t kAStep = 32 >> 4;
+      constexpr uint64_t kBStep = B_MN ? (2048 >> 4) : (32 >> 4);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool landed = false;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      CeIter it(p, live, splits, pair, npairs);
+      CeUnit U;
+      while (ok && it.next(p, U)) {
+        if (!ce_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p)) { ok = false; break; }
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+        uint32_t accumulate = 0;
+        for (int j = U.kb0; j < U.kb1; ++j) {
+          const int kc = j * kBK;
+          if (!landed && !ce_wait(full_bar(stage), phase, abort_flag, p)) { ok = false; break; }
+          tc_fence_after_sync();
+          const int nstage = stage + 1 == STAGES ? 0 : stage + 1;
+          const uint32_t nphase = stage + 1 == STAGES ? phase ^ 1u : phase;
+          const uint64_t ad = adesc0 + static_cast<uint64_t>(stage) * kStageStep;
+          const uint64_t bd = bdesc0 + static_cast<uint64_t>(stage) * kStageStep;
+          if (kc + kBK <= p.kvalid && accumulate) {
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k) {
+              if (k == kBK / 16 - 1) landed = mbar_test_wait(full_bar(nstage), nphase);
+              tc_mma_bf16_pair(d_tmem, ad + k * kAStep, bd + k * kBStep, idesc, 1u);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k) {
+              if (k == kBK / 16 - 1) landed = mbar_test_wait(full_bar(nstage), nphase);
+              if (kc + 16 * k < p.kvalid) {
+                tc_mma_bf16_pair(d_tmem, ad + k * kAStep, bd + k * kBStep, idesc, accumulate);
+                accumulate = 1;
+              }
+            }
+          }
+          tc_commit_pair_multicast(empty_bar(stage), 0x3);   // frees this stage in both CTAs
+          stage = nstage;
+          phase = nphase;
+        }
+        if (!ok) break;
+        tc_commit_pair_multicast(tfull_bar(acc), 0x3);       // both halves of the tile ready
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      }
+      if (!ok) {
+        tc_commit_pair_multicast(drain_bar, 0x1);
+        ce_wait_drain(drain_bar, 0, p);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3;
+    const int part = (warp - 2) >> 2;
+    const int row_in_tile = static_cast<int>(rank) * kBM + q * 32 + lane;
+    const uint32_t tempty_even[2] = {mapa_shared(tempty_bar(0), 0), mapa_shared(tempty_bar(1), 0)};
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    CeIter it(p, live, splits, pair, npairs);
+    CeUnit U;
+    while (it.next(p, U)) {
+      const bool ready = ce_wait(tfull_bar(acc), acc_phase, abort_flag, p);
+      if (!__all_sync(0xffffffffu, ready)) break;
+      tc_fence_after_sync();
+      const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
+      const int row = U.tm * (2 * kBM) + row_in_tile;
+      if constexpr (KIND == CE_PART) {
+        constexpr int kSpan = BN / kCeSlots;
+        float* dst = p.slab + ((static_cast<long long>(U.split) * it.tiles + U.tm * p.tiles_n + U.tn) * (2 * kBM) + row_in_tile) * BN;
+#pragma unroll 1
+        for (int c = part * kSpan; c < (part + 1) * kSpan; c += 32) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld32(tacc + c, v);
+          tmem_ld_wait();
+          if (row < live) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) st_global_v8(dst + c + j, v + j);
+          }
+        }
+      } else {
+        if (p.lg.cap2 > 0.0f) {
+          ce_rows<KIND, true>(p, U, tacc, row, row < live, part);
+        } else {
+          ce_rows<KIND, false>(p, U, tacc, row, row < live, part);
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty_even[acc]);
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    }
+  }
+
+  if (*abort_flag) settle_after_abort();
+  __syncwarp();
+  tc_fence_before_sync();
+  cluster_sync_all();                     // no remote arrive or MMA read of either CTA is pending
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, C::kTmemCols);
+  }
+}
+
+// Defined in gemm_ce.cu.
+cudaError_t launch_ce_gemm(int kind, const CeGemmParams& p, int grid, cudaStream_t st);
+
+}  // namespace lgb

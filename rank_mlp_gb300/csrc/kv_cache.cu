@@ -99,40 +99,6 @@ __device__ __forceinline__ void turn_piece(const AppendParams& p, uint4 own, con
     if (VEC || ((t.turned >> e) & 1u)) y[e] = __fadd_rn(__fmul_rn(y[e], t.c[e]), __fmul_rn(o[e], t.s[e]));
 }
 
-template <int FMT>
-struct Quant;
-template <>
-struct Quant<LORA_KV_FP8> {
-  static constexpr float kTop = 448.0f;
-  static __device__ __forceinline__ uint2 codes(const float (&y)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * e], y[2 * e + 1]), __NV_SATFINITE, __NV_E4M3);
-    return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
-  }
-};
-template <>
-struct Quant<LORA_KV_INT8> {
-  static constexpr float kTop = 127.0f;
-  // |y| is at most 127 (1 + 2^-22): adding 1.5 * 2^23 rounds it to a whole number, ties to
-  // even, whose two's complement is the sum's low byte
-  static __device__ __forceinline__ uint2 codes(const float (&y)[8]) {
-    uint32_t w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__fadd_rn(y[e], 12582912.0f));
-    return make_uint2(__byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410),
-                      __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410));
-  }
-};
-
-// The larger of |a| and |b|; a NaN if either is one.
-__device__ __forceinline__ float max_abs_nan(float a, float b) {
-  float y;
-  asm("{\n\t.reg .f32 a, b;\n\tabs.f32 a, %1;\n\tabs.f32 b, %2;\n\tmax.NaN.f32 %0, a, b;\n\t}" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-
 // Four heads' pieces in flight a lane, and blocks an SM: 8192 tokens took 44.4, 40.5 and 55.9
 // us with 5, 6 and 7 blocks (bf16; at 7 the pieces spill), 49.4, 44.9, 42.6 and 57.7 us with 5
 // to 8 (fp8).

@@ -1,6 +1,6 @@
-// Declarations shared by the serving operators (rotary.cu, kv_cache.cu, paged_attn*.cu):
-// views of heads, the cache as the kernels see it, the argument rules, and the device
-// arithmetic they have in common.
+// Declarations shared by the operators on views of heads (rotary.cu, kv_cache.cu,
+// paged_attn*.cu, rms_norm.cu): the views, the cache as the kernels see it, the argument
+// rules, and the device arithmetic they have in common.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -123,6 +123,41 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 __device__ __forceinline__ void load8f(const float* p, float (&x)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+// Eight values as codes of an 8-bit format (the values already divided by their row's scale).
+template <int FMT>
+struct Quant;
+template <>
+struct Quant<LORA_KV_FP8> {
+  static constexpr float kTop = 448.0f;
+  static __device__ __forceinline__ uint2 codes(const float (&y)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * e], y[2 * e + 1]), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
+  }
+};
+template <>
+struct Quant<LORA_KV_INT8> {
+  static constexpr float kTop = 127.0f;
+  // |y| is at most 127 (1 + 2^-22): adding 1.5 * 2^23 rounds it to a whole number, ties to
+  // even, whose two's complement is the sum's low byte
+  static __device__ __forceinline__ uint2 codes(const float (&y)[8]) {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__fadd_rn(y[e], 12582912.0f));
+    return make_uint2(__byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410));
+  }
+};
+
+// The larger of |a| and |b|; a NaN if either is one.
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+  float y;
+  asm("{\n\t.reg .f32 a, b;\n\tabs.f32 a, %1;\n\tabs.f32 b, %2;\n\tmax.NaN.f32 %0, a, b;\n\t}" : "=f"(y) : "f"(a), "f"(b));
+  return y;
 }
 
 // The sequence that owns row r: the last b with cu[b] <= r, or -1 where none does.
