@@ -485,9 +485,9 @@ typedef struct {
 } lora_tensor_t;
 
 /* The norm of all tensors of a list together: (sum g^2)^(1/2) (LORA_GRAD_NORM_2) or max |g|
- * (LORA_GRAD_NORM_INF; a NaN if there is one), f32 [1], 0 for a list of nothing.  Squares are f32,
- * so an element beyond 1.8e19 makes the first kind infinite; sums over more than a
- * block are f64, in a fixed order.
+ * (LORA_GRAD_NORM_INF; a NaN if there is one), f32 [1], 0 for a list of nothing.  Squares and their
+ * sums are f32, in short chains whose order depends on the counts and the tensors' alignment
+ * alone: the first kind is infinite beyond 1.8e19.
  * lora_clip_grads: out_i = g_i * min(1, max_norm / (norm + 1e-6)), rounded once to its type;
  * norm receives the norm before it.  A norm that is not finite goes into the factor as it is:
  * infinite gives 0 (and NaN for an infinite element), NaN gives NaN.  out: NULL (in place, and
@@ -509,7 +509,7 @@ lora_status_t lora_clip_grads(int64_t n, const lora_tensor_t* grads, const lora_
  * out: n tensors of f32, of count / n_examples elements each, that overlap nothing else.
  * sq_norms f32 [n_examples] holds the examples' squared norms: norms_given != 0 reads them (as
  * lora_mlp_backward_per_example gives them, added over its calls), else the call writes them.
- * Sums are f32 over a fixed order of the examples (the norms' over blocks in f64).  An example
+ * Sums are f32, in a fixed order of the examples.  An example
  * whose norm is not finite makes the sums NaN where its factor or its elements do.
  * max_norm > 0, scale finite; n_examples at most 65535.
  * ws: lora_clip_examples_workspace_bytes(n, n_examples) (0 for what the call refuses). */

@@ -800,10 +800,16 @@ def paged_attention(q, cache: KVCache, batch: PagedBatch, *, scale=None, causal=
 # ------------------------------------------------------------------ norm, loss, clipping
 
 def _rows(t, name):
-    """Rows [tokens, dim], or a view of heads [tokens, heads, dim], as (lora_heads_t, heads)."""
-    if isinstance(t, torch.Tensor) and t.dim() == 2:
-        t = t.unsqueeze(1)
-    return _heads(t, name), t.shape[1]
+    """Rows [tokens, dim], or a view of heads [tokens, heads, dim], as a lora_heads_t (bytes)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        return _heads(t, name)
+    if t.dtype is not _BF16 or not t.is_cuda:
+        _bad_heads(t, name)
+    n, dim = t.shape
+    ts, one = t.stride()
+    if one != 1 and dim > 1:
+        _bad_heads(t, name)
+    return _PACK_HEADS(t.data_ptr(), 1, ts if n > 1 else dim, dim)
 
 
 def _weight(w, dim, name="weight"):
@@ -819,7 +825,7 @@ def rms_norm(x, weight, *, residual=None, eps=1e-6, offset=0.0, format="bf16", t
     which may be x or residual, receives it), y = s * rstd * (weight + offset) in bf16, or with format "fp8" the
     pair (e4m3 codes, f32 scale of each row); rstd, f32, is what the gradient needs (None unless training)."""
     lib = _LIB or load()
-    view, heads = _rows(x, "x")
+    view = _rows(x, "x")
     shape = x.shape
     tokens, dim = shape[0], shape[-1]
     w_at = _weight(weight, dim)
@@ -828,12 +834,12 @@ def rms_norm(x, weight, *, residual=None, eps=1e-6, offset=0.0, format="bf16", t
     if residual is not None:
         if residual.shape != shape:
             raise ValueError("residual must have x's shape")
-        res = _rows(residual, "residual")[0]
+        res = _rows(residual, "residual")
         if sum_out is None:
             sum_out = torch.empty(shape, dtype=_BF16, device=dev)
         elif sum_out.shape != shape:
             raise ValueError("sum_out must have x's shape")
-        total = _rows(sum_out, "sum_out")[0]
+        total = _rows(sum_out, "sum_out")
     elif sum_out is not None:
         raise ValueError("sum_out receives x + residual: there is no residual")
     code = NORM_FORMAT[format]
@@ -857,9 +863,9 @@ def rms_norm_backward(dy, s, weight, rstd, *, offset=0.0, ds=None, dweight=True,
     (or None).  s and rstd are the forward's.  dx (bf16, dense; may be passed in, dy or ds among others) is the
     gradient of x and of the residual; dweight is bf16 [dim], or None where it is not asked for."""
     lib = _LIB or load()
-    view, heads = _rows(s, "s")
+    view = _rows(s, "s")
     shape = s.shape
-    tokens, dim = shape[0], shape[-1]
+    tokens, dim, heads = shape[0], shape[-1], shape[1] if len(shape) == 3 else 1
     w_at = _weight(weight, dim)
     if dy.shape != shape or (ds is not None and ds.shape != shape):
         raise ValueError("dy and ds must have s's shape")
@@ -870,9 +876,9 @@ def rms_norm_backward(dy, s, weight, rstd, *, offset=0.0, ds=None, dweight=True,
     dw = torch.empty(dim, dtype=_BF16, device=s.device) if dweight else None
     _together(s, dy, weight, rstd, ds, dx, ws)
     stream, wp, wn = _call(s, lib.lora_rms_norm_workspace_bytes(tokens, heads, dim), ws)
-    _check(lib.lora_rms_norm_backward(tokens, dim, _rows(dy, "dy")[0], view, w_at, offset,
+    _check(lib.lora_rms_norm_backward(tokens, dim, _rows(dy, "dy"), view, w_at, offset,
                                       _ints(rstd, torch.float32, shape[:-1], "rstd"),
-                                      None if ds is None else _rows(ds, "ds")[0], _dev(dx, "dx"),
+                                      None if ds is None else _rows(ds, "ds"), _dev(dx, "dx"),
                                       None if dw is None else dw.data_ptr(), wp, wn, stream), "lora_rms_norm_backward")
     return dx, dw
 
@@ -914,20 +920,44 @@ class TensorList:
 
     def __init__(self, tensors):
         self.tensors = tuple(tensors)
-        self._structs = (LoraTensor * max(1, len(self.tensors)))()
+        flat = []
         for i, t in enumerate(self.tensors):
             if not isinstance(t, torch.Tensor):
                 raise TypeError("a list's entries must be torch.Tensors")
-            if t.dtype not in LIST_DTYPE or not t.is_cuda or not t.is_contiguous():
+            dtype = LIST_DTYPE.get(t.dtype)
+            if dtype is None or not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"a list's tensors must be contiguous bf16 or f32 CUDA tensors (entry {i}: {t.dtype}, "
                                  f"{t.device}, strides {t.stride()})")
             if t.get_device() != self.tensors[0].get_device():
                 raise ValueError("a list's tensors must be on one device")
-            self._structs[i] = LoraTensor(t.data_ptr(), t.numel(), LIST_DTYPE[t.dtype])
-        self._at = _at(self._structs)
+            flat += (t.data_ptr(), t.numel(), dtype)
+        self._bytes = _pack_tensors(flat)
+        self._examples = None
 
     def __len__(self):
         return len(self.tensors)
+
+    def _example_layout(self):
+        """(examples, shapes, sizes, starts, pieces, total): one example's parts as one f32 buffer, each 16-byte
+        aligned; pieces: the buffer cut at the parts' starts and ends."""
+        if self._examples is None:
+            n = self.tensors[0].shape[0] if self.tensors and self.tensors[0].dim() else 0
+            if not n or any(g.dim() < 1 or g.shape[0] != n for g in self.tensors):
+                raise ValueError("gradients of examples: each tensor [examples, ...], of the same examples and one at least")
+            shapes = [g.shape[1:] for g in self.tensors]
+            sizes = [g.numel() // n for g in self.tensors]
+            starts, pieces, total = [], [], 0
+            for k in sizes:
+                starts.append(total)
+                pieces += (k, -k % 4)
+                total += k + -k % 4
+            self._examples = n, shapes, sizes, starts, pieces, total
+        return self._examples
+
+
+def _pack_tensors(flat):
+    """lora_tensor_t array (bytes) of (address, count, type) after (address, count, type) ..."""
+    return struct.pack("=" + "QqQ" * (len(flat) // 3), *flat)      # (the type's int and its padding: little-endian)
 
 
 def tensor_list(tensors) -> TensorList:
@@ -948,7 +978,7 @@ def grad_norm(grads, *, norm_type=2.0, ws=None):
     _together(t, ws)
     norm = torch.empty((), dtype=torch.float32, device=t.device)
     stream, wp, wn = _call(t, lib.lora_grad_norm_workspace_bytes(len(grads)), ws)
-    _check(lib.lora_grad_norm(len(grads), grads._at, GRAD_NORM[float(norm_type)], norm.data_ptr(), wp, wn, stream),
+    _check(lib.lora_grad_norm(len(grads), grads._bytes, GRAD_NORM[float(norm_type)], norm.data_ptr(), wp, wn, stream),
            "lora_grad_norm")
     return norm
 
@@ -968,7 +998,7 @@ def clip_grad_norm(grads, max_norm, *, norm_type=2.0, out=None, ws=None):
     _together(t, ws)
     norm = torch.empty((), dtype=torch.float32, device=t.device)
     stream, wp, wn = _call(t, lib.lora_grad_norm_workspace_bytes(len(grads)), ws)
-    _check(lib.lora_clip_grads(len(grads), grads._at, None if out is None else out._at, GRAD_NORM[float(norm_type)],
+    _check(lib.lora_clip_grads(len(grads), grads._bytes, None if out is None else out._bytes, GRAD_NORM[float(norm_type)],
                                max_norm, norm.data_ptr(), wp, wn, stream), "lora_clip_grads")
     return norm
 
@@ -980,24 +1010,25 @@ def clip_examples(grads, max_norm, *, sq_norms=None, scale=1.0, out=None, ws=Non
     up), else computed.  out: the f32 tensors for sums."""
     lib = _LIB or load()
     grads = tensor_list(grads)
-    if not grads.tensors:
-        raise ValueError("clip_examples needs a gradient")
+    n, shapes, sizes, starts, pieces, total = grads._example_layout()
     first = grads.tensors[0]
-    if any(g.dim() < 1 or g.shape[0] != first.shape[0] for g in grads.tensors):
-        raise ValueError("all gradients must be of the same examples (their first extent)")
-    n, dev = first.shape[0], first.device
+    dev = first.device
     if out is None:
-        out = [torch.empty(g.shape[1:], dtype=torch.float32, device=dev) for g in grads.tensors]
-    sums = tensor_list(out)
-    if len(sums) != len(grads) or any(o.shape != g.shape[1:] or o.dtype != torch.float32
-                                      for o, g in zip(sums.tensors, grads.tensors)):
-        raise ValueError("out must be f32 tensors of one example's shapes")
+        flat = torch.empty(total, dtype=torch.float32, device=dev)
+        base = flat.data_ptr()
+        sums = [t if len(sh) == 1 else t.view(sh) for t, sh in zip(flat.split_with_sizes(pieces)[::2], shapes)]
+        packed = _pack_tensors([v for a, k in zip(starts, sizes) for v in (base + 4 * a, k, 1)])
+    else:
+        out = tensor_list(out)
+        if len(out) != len(grads) or any(o.shape != sh or o.dtype != torch.float32 for o, sh in zip(out.tensors, shapes)):
+            raise ValueError("out must be f32 tensors of one example's shapes")
+        sums, packed = list(out.tensors), out._bytes
     given = sq_norms is not None
     if not given:
         sq_norms = torch.empty(n, dtype=torch.float32, device=dev)
     sq_at = _ints(sq_norms, torch.float32, (n,), "sq_norms")
-    _together(first, sums.tensors[0], sq_norms, ws)
+    _together(first, sums[0], sq_norms, ws)
     stream, wp, wn = _call(first, lib.lora_clip_examples_workspace_bytes(len(grads), n), ws)
-    _check(lib.lora_clip_examples(len(grads), grads._at, n, sums._at, max_norm, scale, sq_at, int(given), wp, wn, stream),
+    _check(lib.lora_clip_examples(len(grads), grads._bytes, n, packed, max_norm, scale, sq_at, int(given), wp, wn, stream),
            "lora_clip_examples")
-    return list(sums.tensors), sq_norms
+    return sums, sq_norms

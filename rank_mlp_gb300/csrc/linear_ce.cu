@@ -363,18 +363,24 @@ struct CeTotalArgs {
 __global__ void __launch_bounds__(1024) ce_total_kernel(const __grid_constant__ CeTotalArgs p) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ double slots[32];
-  double v = 0.0;
-  for (long long m = threadIdx.x; m < p.M; m += 1024) v += __ldcg(p.loss + m);
+  __shared__ float slots[32];
+  float v = 0.0f;
+  for (long long m = threadIdx.x; m < p.M;) {        // 32 losses at a time: short chains
+    float part = 0.0f;
+#pragma unroll 8
+    for (int k = 0; k < 32 && m < p.M; ++k, m += 1024) part += __ldcg(p.loss + m);
+    v += part;
+  }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
   __syncthreads();
-  if (threadIdx.x != 0) return;
-  v = 0.0;
-  for (int k = 0; k < 32; ++k) v += slots[k];
+  if (threadIdx.x >= 32) return;
+  v = slots[threadIdx.x];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   const int n = p.count != nullptr ? __ldcg(p.count) : 0;
-  *p.total = static_cast<float>(v / (p.mean && n > 0 ? n : 1));
+  if (threadIdx.x == 0) *p.total = v / static_cast<float>(p.mean && n > 0 ? n : 1);
 }
 
 // ---------------------------------------------------------------- host

@@ -56,9 +56,13 @@ def test_norm_and_clip(lib, name, dtype, kind):
             within(o, ref, (HALF[dtype] + 300 * F32) * ref.abs() + 1e-44)
             if k == 1.0:
                 assert torch.equal(o, t)
+        # in place, on copies (aligned otherwise, so their squares join in another order): the bits of out
         inplace = [t.clone() for t in ts]
+        copies = [torch.empty_like(t) for t in ts]
+        got = lib.clip_grad_norm(inplace, limit, norm_type=kind, out=copies)
+        assert abs(float(got) - want) <= tol
         assert torch.equal(lib.clip_grad_norm(inplace, limit, norm_type=kind), got)
-        assert all(torch.equal(a, b) for a, b in zip(inplace, outs))
+        assert all(torch.equal(a, b) for a, b in zip(inplace, copies))
     assert lib.poll_status() == 0
 
 
