@@ -938,20 +938,22 @@ class TensorList:
         return len(self.tensors)
 
     def _example_layout(self):
-        """(examples, shapes, sizes, starts, pieces, total): one example's parts as one f32 buffer, each 16-byte
-        aligned; pieces: the buffer cut at the parts' starts and ends."""
+        """(examples, shapes, sizes, starts, cut, total): one example's parts as one f32 buffer, each 16-byte
+        aligned; cut: the lengths that cut the buffer at the parts' starts and ends, and which of them are parts."""
         if self._examples is None:
             n = self.tensors[0].shape[0] if self.tensors and self.tensors[0].dim() else 0
             if not n or any(g.dim() < 1 or g.shape[0] != n for g in self.tensors):
                 raise ValueError("gradients of examples: each tensor [examples, ...], of the same examples and one at least")
             shapes = [g.shape[1:] for g in self.tensors]
             sizes = [g.numel() // n for g in self.tensors]
-            starts, pieces, total = [], [], 0
+            starts, pieces, parts, total = [], [], [], 0
             for k in sizes:
                 starts.append(total)
-                pieces += (k, -k % 4)
+                parts.append(len(pieces))
+                pieces += (k, -k % 4) if k % 4 else (k,)
                 total += k + -k % 4
-            self._examples = n, shapes, sizes, starts, pieces, total
+            pieces.append(n)
+            self._examples = n, shapes, sizes, starts, (pieces, parts), total
         return self._examples
 
 
@@ -1010,13 +1012,14 @@ def clip_examples(grads, max_norm, *, sq_norms=None, scale=1.0, out=None, ws=Non
     up), else computed.  out: the f32 tensors for sums."""
     lib = _LIB or load()
     grads = tensor_list(grads)
-    n, shapes, sizes, starts, pieces, total = grads._example_layout()
+    n, shapes, sizes, starts, (pieces, parts), total = grads._example_layout()
     first = grads.tensors[0]
     dev = first.device
     if out is None:
-        flat = torch.empty(total, dtype=torch.float32, device=dev)
+        flat = torch.empty(total + n, dtype=torch.float32, device=dev)     # (the norms behind them)
         base = flat.data_ptr()
-        sums = [t if len(sh) == 1 else t.view(sh) for t, sh in zip(flat.split_with_sizes(pieces)[::2], shapes)]
+        cut = flat.split_with_sizes(pieces)
+        sums = [cut[i] if len(sh) == 1 else cut[i].view(sh) for i, sh in zip(parts, shapes)]
         packed = _pack_tensors([v for a, k in zip(starts, sizes) for v in (base + 4 * a, k, 1)])
     else:
         out = tensor_list(out)
@@ -1025,7 +1028,7 @@ def clip_examples(grads, max_norm, *, sq_norms=None, scale=1.0, out=None, ws=Non
         sums, packed = list(out.tensors), out._bytes
     given = sq_norms is not None
     if not given:
-        sq_norms = torch.empty(n, dtype=torch.float32, device=dev)
+        sq_norms = cut[-1] if out is None else torch.empty(n, dtype=torch.float32, device=dev)
     sq_at = _ints(sq_norms, torch.float32, (n,), "sq_norms")
     _together(first, sums[0], sq_norms, ws)
     stream, wp, wn = _call(first, lib.lora_clip_examples_workspace_bytes(len(grads), n), ws)

@@ -5,7 +5,7 @@
 // K-major rows and its epilogue, a row a thread, turns a tile's 256 logits into
 //   CE_STATS   the row's maximum and sum of exponentials relative to it
 //   CE_GRAD    the row's exponentials relative to a reference known beforehand, stored in bf16
-//              (and their sum and maximum)
+//              (and their sum)
 // the other, CE_PART, multiplies those exponentials by the head read MN-major.
 //
 // With e_v = 2^(z_v - ref) the gradient of a row is, up to the row's factor, sum_v e_v W_v / S
@@ -25,18 +25,21 @@ namespace lgb {
 enum CeKind : int { CE_STATS = 0, CE_GRAD = 1, CE_PART = 2 };
 
 constexpr int kCeStages = 6;
-constexpr int kCeWarps = 8;              // epilogue warps: two for each TMEM lane quarter
-constexpr int kCeSlots = kCeWarps / 4;   // partial results of a row in one tile
+// Epilogue warps: one or two for each TMEM lane quarter, and so partial results of a row in one tile.
+constexpr int kCeShortKb = 32;           // logits of at most this many k-blocks take eight
+constexpr int ce_warps(int kb) { return kb <= kCeShortKb ? 8 : 4; }
+constexpr int ce_slots(int warps) { return warps / 4; }
 constexpr int kCeMaxSplits = 32;
+constexpr int kCeTailUnits = 304;        // units of a launch at most that are parts of tiles
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // What a launch finds on the device about its piece of the rows.
 struct CePiece {
   int live;                // labelled rows of the piece
-  int splits;              // k-ranges of CE_PART
+  int whole;               // CE_PART: tiles done in one unit, a multiple of the CTA pairs,
+  int splits;              // and the k-ranges that each tile after them is cut into
   unsigned redo;           // CE_GRAD's sums left their range: the launches of the second try run
-  int pad;
 };
 
 // Logits in units of ln 2 from accumulator values: z2 = v * k2, or cap2 * tanh with
@@ -59,35 +62,45 @@ struct CeGemmParams {
   CeLogit lg;
   const int* label;
   const float* ref2;
-  float2* part;            // [tiles_n * kCeSlots][ldp] (maximum, sum), both without the label
-  float* zsum;             // [tiles_n * kCeSlots][ldp] sums of z2, label included, or NULL
+  float2* part;            // CE_STATS: [tiles_n * slots][ldp] (maximum, sum), both without the label
+  float* psum;             // CE_GRAD: the sums alone
+  float* zsum;             // [tiles_n * slots][ldp] sums of z2, label included, or NULL
   float* zlab;             // the label's z2
   long long ldp;
-  __nv_bfloat16* e;        // [rows][lde]
-  long long lde;
+  __nv_bfloat16* e;        // [rows / 128][blocks][128][64]: what one CTA takes of a k-block together
+  int blocks;              // 64-wide blocks of the vocabulary
   float minus;             // CE_GRAD: taken off each exponential before the tanh's slope
   // CE_PART
-  float* slab;             // [splits][tiles][256][256]
+  float* slab;             // [units][256][256]
 };
 
-// k-ranges a piece's product with the head is cut into: `tiles` tiles of kb k-blocks on `pairs`
-// CTA pairs.  The busiest pair works through ceil(tiles s / pairs) units of kb / s k-blocks; a unit
-// also writes its 256 KB of partial sums and has them read back, at a pair's share of the
-// memory rate about the time of kCeSlabKb k-blocks.
+// The product with the head has few tiles and a long K.  Whole waves of tiles on the CTA pairs are
+// done a tile a unit; the `tail` tiles that are left, fewer than pairs, are cut into k-ranges: the
+// busiest pair then works through ceil(tail s / pairs) units of kb / s k-blocks, each of which also
+// has its 256 KB of partial sums written and read back, at a pair's share of the memory rate
+// about the time of kCeSlabKb k-blocks.
 constexpr int kCeSlabKb = 21;
-constexpr int kCeSlabTiles = 608;        // units of a launch at most, but for the tiles themselves
-__host__ __device__ inline int ce_splits(int tiles, int kb, int pairs) {
+__host__ __device__ inline int ce_splits(int tail, int kb, int pairs) {
   int best = 1;
   float least = 3.0e38f;
   for (int s = 1; s <= kCeMaxSplits; ++s) {
-    if (s > 1 && (tiles * s > kCeSlabTiles || kb < 4 * s)) break;
-    const float cost = static_cast<float>((tiles * s + pairs - 1) / pairs) * (static_cast<float>(kb) / s + kCeSlabKb);
+    if (s > 1 && (tail * s > kCeTailUnits || kb < 4 * s)) break;
+    const float cost = static_cast<float>((tail * s + pairs - 1) / pairs) * (static_cast<float>(kb) / s + kCeSlabKb);
     if (cost < least * 0.999f) {
       least = cost;
       best = s;
     }
   }
   return best;
+}
+__host__ __device__ inline CePiece ce_piece(int live, int tiles_n, int kb, int pairs) {
+  const int tiles = (live + 255) / 256 * tiles_n;
+  CePiece q;
+  q.live = live;
+  q.whole = tiles / pairs * pairs;
+  q.splits = tiles > q.whole ? ce_splits(tiles - q.whole, kb, pairs) : 1;
+  q.redo = 0;
+  return q;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -108,6 +121,13 @@ __device__ __forceinline__ float ce_logit(float v, const CeLogit& lg, float& slo
     slope = q * (2.0f - q);
     return fmaf(-lg.cap2, q, lg.cap2);
   }
+}
+
+// mbar_arrive_cluster that orders no memory: what it announces is that tensor memory has been read
+// (tcgen05.wait::ld, then the fence before it).  A releasing arrive would first wait for the
+// thread's stores of exponentials.
+__device__ __forceinline__ void arrive_read(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 __device__ __forceinline__ bool ce_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, const CeGemmParams& p) {
@@ -133,143 +153,175 @@ __device__ __forceinline__ void ce_wait_drain(uint32_t bar, uint32_t parity, con
   }
 }
 
-// The units of a CTA pair: tiles in bands of n-tiles (the n-tile fastest inside a band), k-range
-// by k-range, so that pairs working at the same time read the same slices.
+// The units of a CTA pair: tiles in bands of n-tiles (the n-tile fastest inside a band); of the
+// tiles cut into k-ranges all first ranges, then all second ones, so that pairs working at the same
+// time read the same slices.
 struct CeUnit {
-  int tm, tn, split, kb0, kb1;
+  int u, tm, tn, kb0, kb1;
 };
 struct CeIter {
-  int u, step, end, tiles, tiles_m, splits;
-  __device__ __forceinline__ CeIter(const CeGemmParams& p, int live, int splits_, int pair, int npairs) {
+  int u, step, end, whole, tail, tiles_m, splits;
+  __device__ __forceinline__ CeIter(const CeGemmParams& p, int live, int whole_, int splits_, int pair, int npairs) {
     tiles_m = (live + 2 * kBM - 1) / (2 * kBM);
-    tiles = tiles_m * p.tiles_n;
+    const int tiles = tiles_m * p.tiles_n;
+    whole = whole_ < 0 ? tiles : min(whole_, tiles);
+    tail = tiles - whole;
     splits = splits_;
     u = pair;
     step = npairs;
-    end = tiles * splits;
+    end = whole + tail * splits;
   }
   __device__ __forceinline__ bool next(const CeGemmParams& p, CeUnit& U) {
     if (u >= end) return false;
-    U.split = u / tiles;
-    const int t = u - U.split * tiles;
+    int t = u;
+    U.u = u;
+    U.kb0 = 0;
+    U.kb1 = p.kb_total;
+    if (u >= whole) {
+      const int v = u - whole, s = v / tail;
+      t = whole + v - s * tail;
+      U.kb0 = static_cast<int>(static_cast<long long>(p.kb_total) * s / splits);
+      U.kb1 = static_cast<int>(static_cast<long long>(p.kb_total) * (s + 1) / splits);
+    }
     const int b = t / (tiles_m * p.band);
     const int rem = t - b * tiles_m * p.band;
     const int nb = min(p.band, p.tiles_n - b * p.band);
     U.tm = rem / nb;
     U.tn = b * p.band + rem % nb;
-    U.kb0 = static_cast<int>(static_cast<long long>(p.kb_total) * U.split / splits);
-    U.kb1 = static_cast<int>(static_cast<long long>(p.kb_total) * (U.split + 1) / splits);
     u += step;
     return true;
   }
 };
+// The place of tile (tm, tn) in that order.
+__device__ __forceinline__ int ce_tile_place(int tm, int tn, int tiles_m, int tiles_n, int band) {
+  const int b = tn / band, nb = min(band, tiles_n - b * band);
+  return b * tiles_m * band + tm * nb + tn - b * band;
+}
 
-// The epilogue of one tile row: columns [part * 128, part * 128 + 128) of the tile.
-// Warp-collective (tcgen05.ld); `ok`: the row is one of the piece's.
+// 32 logits of a row, columns [col0, col0 + 32): into the row's running (top, sum, zs), the label's
+// own into zlab, and for CE_GRAD their exponentials into e.  Whole warps call it.
 template <int KIND, bool CAP>
-__device__ __forceinline__ void ce_rows(const CeGemmParams& p, const CeUnit& U, uint32_t tacc, int row, bool ok, int part) {
-  constexpr int BN = 256, kSpan = BN / kCeSlots;
+__device__ __forceinline__ void ce_chunk(const CeGemmParams& p, const uint32_t (&v)[32], int col0, int row, bool ok, int label,
+                                         float ref2, float& top, float& sum, float& zs) {
+  if (col0 >= p.vocab) return;                   // wholly past the vocabulary
+  const int at = label - col0;                   // the label's place in the chunk
+  const int width = p.vocab - col0;              // columns below the vocabulary's size
+  const bool plain = !__any_sync(0xffffffffu, static_cast<unsigned>(at) < 32u) && width >= 32;
+  // the label's column and those past the vocabulary leave the sums
+  auto chunk = [&](auto tag) {
+    constexpr bool PLAIN = decltype(tag)::value != 0;
+    if constexpr (KIND == CE_STATS) {
+      float z[32], most = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        float slope;
+        z[j] = ce_logit<CAP>(__uint_as_float(v[j]), p.lg, slope);
+        if (!PLAIN) {
+          if (p.zsum != nullptr && j < width) zs += z[j];
+          if (j == at) p.zlab[row] = z[j];
+          if (j == at || j >= width) z[j] = -INFINITY;
+        }
+        most = fmaxf(most, z[j]);
+      }
+      if (PLAIN && p.zsum != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) zs += z[j];
+      }
+      if (most > top) {
+        sum *= exp2_approx(top - most);
+        top = most;
+      }
+      const float base = top == -INFINITY ? 0.0f : top;
+      float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        s0 += exp2_approx(z[j] - base);
+        s1 += exp2_approx(z[j + 1] - base);
+      }
+      sum += s0 + s1;
+    } else {
+      uint32_t w[16];
+      float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        float e[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float slope = 1.0f, z = 0.0f;
+          if (CAP || !PLAIN || p.zsum != nullptr) z = ce_logit<CAP>(__uint_as_float(v[j + h]), p.lg, slope);
+          float x = exp2_approx(CAP ? z - ref2 : fmaf(__uint_as_float(v[j + h]), p.lg.k2, -ref2));
+          if (p.zsum != nullptr && (PLAIN || j + h < width)) zs += z;
+          if (!PLAIN) {
+            if (j + h == at) p.zlab[row] = z;
+            if (j + h == at || j + h >= width) x = 0.0f;
+          }
+          (h ? s1 : s0) += x;
+          e[h] = CAP ? (x - p.minus) * slope : x;
+          if (CAP && !PLAIN && (j + h == at || j + h >= width)) e[h] = 0.0f;
+        }
+        w[j / 2] = pack_bf16x2(e[0], e[1]);
+      }
+      sum += s0 + s1;
+      if (ok) {
+        // (row by row the same stores, 64 bytes each a whole row of the vocabulary apart, took a sixth
+        // of the launch)
+        __nv_bfloat16* dst = p.e + (static_cast<long long>(row >> 7) * p.blocks + (col0 >> 6)) * 8192 + (row & 127) * 64 + (col0 & 63);
+        st_global_v8(dst, w);
+        st_global_v8(dst + 16, w + 8);
+      }
+    }
+  };
+  if (plain) chunk(ActTag<1>{}); else chunk(ActTag<0>{});
+}
+
+// The epilogue of one tile row: the warp's share `part` of the tile's columns, 32 at a time, each read
+// from tensor memory while those before are worked on; release() once all have been read.
+// Warp-collective; `ok`: the row is one of the piece's.
+template <int KIND, int WARPS, bool CAP, typename F>
+__device__ __forceinline__ void ce_rows(const CeGemmParams& p, const CeUnit& U, uint32_t tacc, int row, bool ok, int part,
+                                        F&& release) {
+  constexpr int BN = 256, kSlots = ce_slots(WARPS), kSpan = BN / kSlots;
+  const uint32_t from = tacc + part * kSpan;
   const int first = U.tn * BN + part * kSpan;
+  uint32_t va[32], vb[32];
+  __syncwarp();
+  tmem_ld32(from, va);
   const int label = ok ? __ldg(p.label + row) : -1;
   const float ref2 = KIND == CE_GRAD && ok ? __ldcg(p.ref2 + row) : 0.0f;
   float top = -INFINITY, sum = 0.0f, zs = 0.0f;
 #pragma unroll 1
-  for (int c = 0; c < kSpan; c += 32) {
-    uint32_t v[32];
+  for (int c = 0; c < kSpan; c += 64) {
+    tmem_ld_wait_for(va);
     __syncwarp();
-    tmem_ld32(tacc + part * kSpan + c, v);
-    tmem_ld_wait();
-    const int col0 = first + c;
-    if (col0 >= p.vocab) continue;               // wholly past the vocabulary
-    const int at = label - col0;                 // the label's place in the chunk
-    const int width = p.vocab - col0;            // columns below the vocabulary's size
-    const bool plain = !__any_sync(0xffffffffu, static_cast<unsigned>(at) < 32u) && width >= 32;
-    // z2 of all columns; the label's and those past the vocabulary leave the sums
-    auto chunk = [&](auto tag) {
-      constexpr bool PLAIN = decltype(tag)::value != 0;
-      if constexpr (KIND == CE_STATS) {
-        float z[32], most = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          float slope;
-          z[j] = ce_logit<CAP>(__uint_as_float(v[j]), p.lg, slope);
-          if (!PLAIN) {
-            if (p.zsum != nullptr && j < width) zs += z[j];
-            if (j == at) p.zlab[row] = z[j];
-            if (j == at || j >= width) z[j] = -INFINITY;
-          }
-          most = fmaxf(most, z[j]);
-        }
-        if (PLAIN && p.zsum != nullptr) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) zs += z[j];
-        }
-        if (most > top) {
-          sum *= exp2_approx(top - most);
-          top = most;
-        }
-        const float base = top == -INFINITY ? 0.0f : top;
-        float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          s0 += exp2_approx(z[j] - base);
-          s1 += exp2_approx(z[j + 1] - base);
-        }
-        sum += s0 + s1;
-      } else {
-        uint32_t w[16];
-        float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          float e[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float slope;
-            const float z = ce_logit<CAP>(__uint_as_float(v[j + h]), p.lg, slope);
-            float x = exp2_approx(CAP ? z - ref2 : fmaf(__uint_as_float(v[j + h]), p.lg.k2, -ref2));
-            if (!PLAIN) {
-              if (p.zsum != nullptr && j + h < width) zs += z;
-              if (j + h == at) p.zlab[row] = z;
-              if (j + h == at || j + h >= width) x = 0.0f;
-              else top = fmaxf(top, z);
-            } else {
-              top = fmaxf(top, z);
-            }
-            (h ? s1 : s0) += x;
-            e[h] = CAP ? (x - p.minus) * slope : x;
-            if (!PLAIN && (j + h == at || j + h >= width)) e[h] = 0.0f;
-            if (PLAIN && p.zsum != nullptr) zs += z;
-          }
-          w[j / 2] = pack_bf16x2(e[0], e[1]);
-        }
-        sum += s0 + s1;
-        if (ok) {
-          __nv_bfloat16* dst = p.e + static_cast<long long>(row) * p.lde + col0;
-          if (col0 + 32 <= p.lde) {
-            st_global_v8(dst, w);
-            st_global_v8(dst + 16, w + 8);
-          } else {
-            st_global_v8(dst, w);                // lde is a multiple of 16
-          }
-        }
-      }
-    };
-    if (plain) chunk(ActTag<1>{}); else chunk(ActTag<0>{});
+    tmem_ld32(from + c + 32, vb);
+    ce_chunk<KIND, CAP>(p, va, first + c, row, ok, label, ref2, top, sum, zs);
+    tmem_ld_wait_for(vb);
+    __syncwarp();
+    if (c + 64 < kSpan) {
+      tmem_ld32(from + c + 64, va);
+    } else {
+      release();
+    }
+    ce_chunk<KIND, CAP>(p, vb, first + c + 32, row, ok, label, ref2, top, sum, zs);
   }
   if (ok) {
-    const long long at = (static_cast<long long>(U.tn) * kCeSlots + part) * p.ldp + row;
-    p.part[at] = make_float2(top, sum);
+    const long long at = (static_cast<long long>(U.tn) * kSlots + part) * p.ldp + row;
+    if (KIND == CE_STATS) p.part[at] = make_float2(top, sum); else p.psum[at] = sum;
     if (p.zsum != nullptr) p.zsum[at] = zs;
   }
 }
 
-template <int KIND>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarps), 1)
+template <int KIND, int WARPS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(WARPS), 1)
     ce_gemm_kernel(const __grid_constant__ CeGemmParams p) {
   constexpr int STAGES = kCeStages;
   constexpr bool B_MN = KIND == CE_PART;
-  using C = PairCfg<STAGES, kCeWarps>;
+  using C = PairCfg<STAGES, WARPS>;
   constexpr int BN = C::BN;
+  if (p.when_redo) {                      // the second try, seldom needed: leave before taking anything
+    pdl_wait();
+    if (__ldcg(&p.piece->redo) == 0) return;
+  }
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -297,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 2 * kCeWarps);
+      mbar_init(tempty_bar(a), 2 * WARPS);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -317,9 +369,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();                             // the previous kernels' writes are visible from here
   pdl_launch_dependents();
-  // every thread of the launch reads the same three words: all roles walk the same units
-  const int live = p.when_redo && __ldcg(&p.piece->redo) == 0 ? 0 : __ldcg(&p.piece->live);
-  const int splits = KIND == CE_PART ? __ldcg(&p.piece->splits) : 1;
+  // every thread of the launch reads the same words: all roles walk the same units
+  const int live = __ldcg(&p.piece->live);
+  const int whole = KIND == CE_PART ? __ldcg(&p.piece->whole) : -1, splits = KIND == CE_PART ? __ldcg(&p.piece->splits) : 1;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
@@ -329,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
       int armed[STAGES];
       for (int s = 0; s < STAGES; ++s) armed[s] = -1;
       bool ok = true, first_stage = true;
-      CeIter it(p, live, splits, pair, npairs);
+      CeIter it(p, live, whole, splits, pair, npairs);
       CeUnit U;
       while (ok && it.next(p, U)) {
         const int a_row = U.tm * (2 * kBM) + static_cast<int>(rank) * kBM;
@@ -351,7 +403,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
           const uint32_t fb_even = mapa_shared(fb, 0);
           const uint32_t sa = sbase + stage * C::kStageBytes;
           const uint32_t sb = sa + C::kABytes;
-          tma_load_2d_pair(sa, &p.a, fb_even, kc, a_row);
+          if (KIND == CE_PART) {
+            tma_load_2d_pair(sa, &p.a, fb_even, 0, ((U.tm * 2 + static_cast<int>(rank)) * p.blocks + j) * kBM);
+          } else {
+            tma_load_2d_pair(sa, &p.a, fb_even, kc, a_row);
+          }
           if (!B_MN) {
             tma_load_2d_pair(sb, &p.b, fb_even, kc, b_row);
           } else {
@@ -384,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      CeIter it(p, live, splits, pair, npairs);
+      CeIter it(p, live, whole, splits, pair, npairs);
       CeUnit U;
       while (ok && it.next(p, U)) {
         if (!ce_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p)) { ok = false; break; }
@@ -436,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
     const uint32_t tempty_even[2] = {mapa_shared(tempty_bar(0), 0), mapa_shared(tempty_bar(1), 0)};
     int acc = 0;
     uint32_t acc_phase = 0;
-    CeIter it(p, live, splits, pair, npairs);
+    CeIter it(p, live, whole, splits, pair, npairs);
     CeUnit U;
     while (it.next(p, U)) {
       const bool ready = ce_wait(tfull_bar(acc), acc_phase, abort_flag, p);
@@ -444,9 +500,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
       tc_fence_after_sync();
       const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
       const int row = U.tm * (2 * kBM) + row_in_tile;
+      // the accumulator has been read: the MMAs of the tile after next may overwrite it
+      auto release = [&]() {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive_read(tempty_even[acc]);
+      };
       if constexpr (KIND == CE_PART) {
-        constexpr int kSpan = BN / kCeSlots;
-        float* dst = p.slab + ((static_cast<long long>(U.split) * it.tiles + U.tm * p.tiles_n + U.tn) * (2 * kBM) + row_in_tile) * BN;
+        constexpr int kSpan = BN / ce_slots(WARPS);
+        float* dst = p.slab + (static_cast<long long>(U.u) * (2 * kBM) + row_in_tile) * BN;
 #pragma unroll 1
         for (int c = part * kSpan; c < (part + 1) * kSpan; c += 32) {
           uint32_t v[32];
@@ -458,16 +520,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
             for (int j = 0; j < 32; j += 8) st_global_v8(dst + c + j, v + j);
           }
         }
+        release();
       } else {
         if (p.lg.cap2 > 0.0f) {
-          ce_rows<KIND, true>(p, U, tacc, row, row < live, part);
+          ce_rows<KIND, WARPS, true>(p, U, tacc, row, row < live, part, release);
         } else {
-          ce_rows<KIND, false>(p, U, tacc, row, row < live, part);
+          ce_rows<KIND, WARPS, false>(p, U, tacc, row, row < live, part, release);
         }
       }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty_even[acc]);
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
   }

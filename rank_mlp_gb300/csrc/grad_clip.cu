@@ -262,6 +262,7 @@ template <int CAP>
 struct ExampleSumArgs {
   const float* sq;
   int n_examples;
+  int shares;                             // blocks that shared out an example's chunks for its norm; 0: none
   float max_norm, scale;
   ListArgs<CAP> list;
 };
@@ -364,8 +365,15 @@ __global__ void __launch_bounds__(kClipThreads, 6) example_sum_kernel(const __gr
   pdl_wait();
   pdl_launch_dependents();
   __shared__ float keep[kClipThreads];
-  const int c = blockIdx.x;                          // a block has one chunk: its tensor by bisection
-  int lo = 0, hi = p.list.n;                         // t[lo].first <= c < t[hi].first
+  // A block has one chunk.  After the norms' launch: the last chunk of each of its shares, then the
+  // chunks before them, and so on: what was read last is still in L2.
+  int c = blockIdx.x;
+  if (p.shares > 0) {
+    const int k = blockIdx.x / p.shares, s = blockIdx.x - k * p.shares;
+    c = share_begin(p.list.chunks, s + 1, p.shares) - 1 - k;
+    if (c < share_begin(p.list.chunks, s, p.shares)) return;
+  }
+  int lo = 0, hi = p.list.n;                         // its tensor: t[lo].first <= c < t[hi].first
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (p.list.t[mid].first <= c) lo = mid; else hi = mid;
@@ -519,7 +527,7 @@ static lora_status_t example_norms(int64_t n, const lora_tensor_t* grads, int64_
 
 template <int CAP>
 static lora_status_t example_sums(int64_t n, const lora_tensor_t* grads, int64_t n_examples, const lora_tensor_t* out,
-                                  float max_norm, float scale, const float* sq, cudaStream_t st) {
+                                  float max_norm, float scale, const float* sq, bool read, cudaStream_t st) {
   ExampleSumArgs<CAP> p;
   p.sq = sq;
   p.n_examples = static_cast<int>(n_examples);
@@ -528,8 +536,10 @@ static lora_status_t example_sums(int64_t n, const lora_tensor_t* grads, int64_t
   for (int64_t i = 0; i < n;) {
     i = fill_list(p.list, i, n, grads, out, n_examples);
     if (p.list.n == 0) break;
-    LGB_TRY(launch_counted(example_sum_kernel<CAP>, dim3(static_cast<unsigned>(p.list.chunks)), dim3(kClipThreads), 0,
-                           LORA_KIND_CLIP, st, p));
+    p.shares = read ? static_cast<int>(list_grid(p.list.chunks, example_parts(n_examples))) : 0;
+    const int64_t grid = read ? ceil_div(p.list.chunks, p.shares) * p.shares : p.list.chunks;
+    LGB_TRY(launch_counted(example_sum_kernel<CAP>, dim3(static_cast<unsigned>(grid)), dim3(kClipThreads), 0, LORA_KIND_CLIP,
+                           st, p));
   }
   return LORA_OK;
 }
@@ -621,6 +631,6 @@ extern "C" lora_status_t lora_clip_examples(int64_t n, const lora_tensor_t* grad
     LGB_TRY(n <= kListFew ? example_norms<kListFew>(n, grads, n_examples, sq_norms, part, stream)
                           : example_norms<kListMax>(n, grads, n_examples, sq_norms, part, stream));
   }
-  return n <= kListFew ? example_sums<kListFew>(n, grads, n_examples, out, max_norm, scale, sq_norms, stream)
-                       : example_sums<kListMax>(n, grads, n_examples, out, max_norm, scale, sq_norms, stream);
+  return n <= kListFew ? example_sums<kListFew>(n, grads, n_examples, out, max_norm, scale, sq_norms, !norms_given, stream)
+                       : example_sums<kListMax>(n, grads, n_examples, out, max_norm, scale, sq_norms, !norms_given, stream);
 }

@@ -3,16 +3,15 @@
 //
 // A call packs the labelled rows, then takes them piece by piece:
 //   loss alone     CE_STATS, join of the row's partial results
-//   with dx        reference z_y + 40 for each row (a dot product), CE_GRAD, join, [CE_GRAD and
-//                  join again where a row's logits stand 60 above its reference or more],
-//                  CE_PART over the exponentials, join of the k-ranges with the label's row of W
-//   capped and smoothed at once: CE_STATS, join, CE_GRAD with the sum as its reference, CE_PART
+//   with dx        reference z_y + 40 for each row (a dot product), CE_GRAD, join, CE_PART over the
+//                  exponentials, join of the k-ranges with the label's row of W
+//   capped and smoothed at once: CE_STATS, join, CE_GRAD with lse as its reference, CE_PART
 //                  (the smoothing's part of the gradient then depends on each logit's slope)
 // A row's largest logit is at least its label's.  So the reference, 40 above the label's logit,
 // leaves the largest exponential between e^-40 and, where the largest logit stands less than 100
 // above the label's, e^60: it, the sums and the product stay inside the range of f32 and bf16
 // (a weight below 2^-68 of the label's counts as zero).  A row beyond that is seen by its sum,
-// and its piece's second try takes the row's maximum itself for the reference.
+// and its piece is taken again the last way.
 #include "gemm_ce.cuh"
 #include "serve.cuh"
 
@@ -22,11 +21,13 @@ constexpr float kCeAhead = 40.0f * kLog2e;         // the reference above the la
 constexpr float kCeMost = 1.5474250491067253e26f;  // 2^87: a row's sum of exponentials past it is taken again
 constexpr int64_t kCeGradBytes = int64_t(1) << 30; // exponentials of a piece
 constexpr int64_t kCeStatBytes = int64_t(1) << 28; // partial results of a piece (the loss alone)
+constexpr int64_t kCeMaxVocab = int64_t(1) << 24;   // (256 rows' exponentials stay in a TMA map's reach)
 constexpr int kCeColumnBlocks = 304;               // row ranges of W for its column sums
 
 // The rows of a call as the kernels see them; arrays over packed rows but for pos.
 struct CeRows {
   int* count;              // labelled rows
+  unsigned* joined;        // [2] blocks of the last piece's joins that are done
   int* pos;                // [M] place of a token among them, -1: none
   int* idx;                // token of a packed row
   int* label;
@@ -36,15 +37,32 @@ struct CeRows {
   float* coef;
 };
 
-struct CePackArgs {
-  const long long* labels;
-  long long M;
-  long long ignore;
-  long long vocab;
-  CeRows r;
+// What the pieces' descriptions are made of.
+struct CePieces {
   CePiece* piece;
   int pieces, piece_rows;
   int tiles_n, kb, pairs;  // of CE_PART
+};
+__device__ __forceinline__ void write_pieces(const CePieces& p, const CeRows& r, int n) {
+  if (threadIdx.x == 0) {
+    *r.count = n;
+    r.joined[0] = r.joined[1] = 0;
+  }
+  for (int k = threadIdx.x; k < p.pieces; k += blockDim.x) {
+    const long long left = n - static_cast<long long>(k) * p.piece_rows;
+    p.piece[k] = ce_piece(left <= 0 ? 0 : left < p.piece_rows ? static_cast<int>(left) : p.piece_rows, p.tiles_n, p.kb, p.pairs);
+  }
+}
+
+struct CeLabels {
+  const long long* y;
+  long long M, ignore, vocab;
+};
+
+struct CePackArgs {
+  CeLabels labels;
+  CeRows r;
+  CePieces plan;
   unsigned* status;
 };
 
@@ -55,16 +73,16 @@ __global__ void __launch_bounds__(1024) ce_pack_kernel(const __grid_constant__ C
   __shared__ int warps[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int n = 0;
-  for (long long base = 0; base < p.M; base += 4096) {
+  for (long long base = 0; base < p.labels.M; base += 4096) {
     const long long m = base + 4 * threadIdx.x;
     long long y[4];
     bool seen[4];
     int mine = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      y[j] = m + j < p.M ? __ldg(p.labels + m + j) : p.ignore;
-      seen[j] = y[j] != p.ignore && m + j < p.M;
-      if (seen[j] && (y[j] < 0 || y[j] >= p.vocab)) {
+      y[j] = m + j < p.labels.M ? __ldg(p.labels.y + m + j) : p.labels.ignore;
+      seen[j] = y[j] != p.labels.ignore;
+      if (seen[j] && (y[j] < 0 || y[j] >= p.labels.vocab)) {
         atomicOr(p.status, kStatusInput);
         seen[j] = false;
       }
@@ -91,7 +109,7 @@ __global__ void __launch_bounds__(1024) ce_pack_kernel(const __grid_constant__ C
     int at = n + before + upto - mine;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (m + j >= p.M) break;
+      if (m + j >= p.labels.M) break;
       p.r.pos[m + j] = seen[j] ? at : -1;
       if (!seen[j]) continue;
       p.r.idx[at] = static_cast<int>(m + j);
@@ -100,40 +118,74 @@ __global__ void __launch_bounds__(1024) ce_pack_kernel(const __grid_constant__ C
     }
     n += total;
   }
-  if (threadIdx.x == 0) *p.r.count = n;
-  for (int k = threadIdx.x; k < p.pieces; k += 1024) {
-    const long long left = n - static_cast<long long>(k) * p.piece_rows;
-    CePiece q;
-    q.live = left <= 0 ? 0 : left < p.piece_rows ? static_cast<int>(left) : p.piece_rows;
-    q.splits = ce_splits((q.live + 255) / 256 * p.tiles_n, p.kb, p.pairs);
-    q.redo = 0;
-    q.pad = 0;
-    p.piece[k] = q;
-  }
+  write_pieces(p.plan, p.r, n);
 }
 
 struct CeGatherArgs {
   const bf16* x;
   const bf16* W;
-  long long M;
   int h;
+  CeLabels labels;
   CeRows r;
+  CePieces plan;
   bf16* packed;            // [count][h]
   CeLogit lg;
   int want_ref;
   float* loss;
   float* lse;              // NULL: not wanted
   bf16* dx;                // NULL: the loss alone
+  unsigned* status;
 };
 
 // A warp a token: packs its row and takes the reference from its label's logit, or clears what
-// an unlabelled token has.
+// an unlabelled token has.  ALONE (few tokens): no ce_pack_kernel has run; a block counts the labelled
+// tokens before its own eight by itself.
+constexpr int kCeAloneRows = 2048;
+template <bool ALONE>
 __global__ void __launch_bounds__(256) ce_gather_kernel(const __grid_constant__ CeGatherArgs p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  for (long long m = blockIdx.x * 8ll + (threadIdx.x >> 5); m < p.M; m += 8ll * gridDim.x) {
-    const int at = __ldcg(p.r.pos + m);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int at_alone = -1, label_alone = 0;
+  if constexpr (ALONE) {
+    __shared__ int upto[8], all[8];
+    const int M = static_cast<int>(p.labels.M), first = blockIdx.x * 8;
+    int n = 0, total = 0;                            // labelled tokens before the block's, and in all
+    for (int m = threadIdx.x; m < (blockIdx.x == 0 ? M : first); m += 256) {
+      const long long y = __ldg(p.labels.y + m);
+      const bool seen = y != p.labels.ignore && y >= 0 && y < p.labels.vocab;
+      n += seen && m < first;
+      total += seen;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      n += __shfl_xor_sync(0xffffffffu, n, d);
+      total += __shfl_xor_sync(0xffffffffu, total, d);
+    }
+    if (lane == 0) upto[warp] = n, all[warp] = total;
+    __syncthreads();
+    n = total = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) n += upto[k], total += all[k];
+    if (blockIdx.x == 0) write_pieces(p.plan, p.r, total);
+    // the block's own eight: lane k of each warp looks at token k
+    const int m = first + (lane & 7);
+    const long long y = m < M ? __ldg(p.labels.y + m) : p.labels.ignore;
+    bool seen = y != p.labels.ignore;
+    if (seen && (y < 0 || y >= p.labels.vocab)) {
+      if (threadIdx.x < 8) atomicOr(p.status, kStatusInput);
+      seen = false;
+    }
+    const unsigned mask = __ballot_sync(0xffffffffu, seen) & 0xFFu;
+    label_alone = static_cast<int>(__shfl_sync(0xffffffffu, y, warp));
+    at_alone = (mask >> warp) & 1u ? n + __popc(mask & ((1u << warp) - 1u)) : -1;
+    if (at_alone >= 0 && lane == 0) {
+      p.r.idx[at_alone] = first + warp;
+      p.r.label[at_alone] = label_alone;
+    }
+  }
+  for (long long m = blockIdx.x * 8ll + warp; m < p.labels.M; m += 8ll * gridDim.x) {
+    const int at = ALONE ? at_alone : __ldcg(p.r.pos + m);
     if (at < 0) {
       if (lane == 0) {
         p.loss[m] = 0.0f;
@@ -144,19 +196,29 @@ __global__ void __launch_bounds__(256) ce_gather_kernel(const __grid_constant__ 
       continue;
     }
     const bf16* x = p.x + m * p.h;
-    const bf16* w = p.W + static_cast<long long>(__ldcg(p.r.label + at)) * p.h;
+    const bf16* w = p.W + static_cast<long long>(ALONE ? label_alone : __ldcg(p.r.label + at)) * p.h;
     bf16* out = p.packed + static_cast<long long>(at) * p.h;
     float dot = 0.0f;
-#pragma unroll 4
-    for (int c = 8 * lane; c < p.h; c += 256) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + c));
-      *reinterpret_cast<uint4*>(out + c) = v;
-      if (p.want_ref) {
-        float a[8], b[8];
-        unpack8(v, a);
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w + c)), b);
+    for (int c0 = 8 * lane; c0 < p.h; c0 += 1024) {  // four pieces of both rows on their way at a time
+      uint4 v[4], u[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dot = fmaf(a[e], b[e], dot);
+      for (int k = 0; k < 4; ++k) {
+        const int c = c0 + 256 * k < p.h ? c0 + 256 * k : c0;
+        v[k] = __ldg(reinterpret_cast<const uint4*>(x + c));
+        if (p.want_ref) u[k] = __ldg(reinterpret_cast<const uint4*>(w + c));
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = c0 + 256 * k;
+        if (c >= p.h) break;
+        *reinterpret_cast<uint4*>(out + c) = v[k];
+        if (p.want_ref) {
+          float a[8], b[8];
+          unpack8(v[k], a);
+          unpack8(u[k], b);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot = fmaf(a[e], b[e], dot);
+        }
       }
     }
     if (!p.want_ref) continue;
@@ -169,55 +231,54 @@ __global__ void __launch_bounds__(256) ce_gather_kernel(const __grid_constant__ 
   }
 }
 
-enum CeJoin : int { CE_JOIN_LOSS = 0, CE_JOIN_EXACT = 1, CE_JOIN_GRAD = 2, CE_JOIN_REDO = 3 };
+enum CeJoin : int { CE_JOIN_LOSS = 0, CE_JOIN_EXACT = 1, CE_JOIN_GRAD = 2 };
 struct CeJoinArgs {
   CePiece* piece;
   int mode;
-  CeRows r;                // at the piece's first row (count: the call's)
-  const float2* part;
+  int when_redo;           // 1: only if the piece's `redo` is set
+  CeRows r;                // at the piece's first row (count, joined: the call's)
+  const float2* part;      // CE_JOIN_LOSS, CE_JOIN_EXACT
+  const float* psum;       // CE_JOIN_GRAD
   const float* zsum;
   long long ldp;
   int slots;
   int vocab;
   float cap2;              // 0: no cap
-  float scale, smoothing;
+  float scale, smoothing, minus;
   int mean;
   float* loss;             // by token
   float* lse;
+  float* total;            // of the last piece: the call's total; else NULL
+  long long M;
 };
 
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 32;
 
-// The partial results of 32 rows, a lane a row, shared out over the block's warps and joined in
-// a fixed order; then the row's loss and its factors.
-__global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(const __grid_constant__ CeJoinArgs p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  __shared__ float tops[kJoinWarps][32], sums[kJoinWarps][32], zs[kJoinWarps][32];
-  const int live = __ldcg(&p.piece->live);
+// Rows [32 blockIdx.x, + 32) of a piece: a lane a row, their partial results are shared out over the
+// block's warps; then a warp a row, the warps' shares are joined, in a fixed order, and the row's
+// loss and factors follow.
+template <int MODE>
+__device__ __forceinline__ void ce_join_rows(const CeJoinArgs& p, int live) {
+  __shared__ float tops[kJoinWarps][33], sums[kJoinWarps][33], zs[kJoinWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.x * 32 + lane;
-  if (static_cast<int>(blockIdx.x) * 32 >= live) return;
-  if (p.mode == CE_JOIN_REDO && __ldcg(&p.piece->redo) == 0) return;
-  const bool ok = row < live, relative = p.mode <= CE_JOIN_EXACT;
+  constexpr bool kRelative = MODE != CE_JOIN_GRAD;   // sums relative to their own maxima
   float top = -INFINITY, sum = 0.0f, z = 0.0f;
   auto add = [&](float t, float s) {
-    if (!relative) {
-      sum += s;
-      top = fmaxf(top, t);
-      return;
-    }
-    // sums relative to their own maxima; an empty one (no column but the label's) adds nothing
-    if (t == -INFINITY && s == 0.0f) return;
+    if (t == -INFINITY && s == 0.0f) return;         // no column but the label's
     const float most = fmaxf(top, t);
     sum = sum * exp2f(top - most) + s * exp2f(t - most);
     top = most;
   };
-  if (ok) {
+  if (static_cast<int>(blockIdx.x) * 32 + lane < live) {
+    const int row = blockIdx.x * 32 + lane;
 #pragma unroll 8
     for (int k = warp; k < p.slots; k += kJoinWarps) {
-      const float2 o = __ldcg(p.part + k * p.ldp + row);
-      add(o.x, o.y);
+      if constexpr (kRelative) {
+        const float2 o = __ldcg(p.part + k * p.ldp + row);
+        add(o.x, o.y);
+      } else {
+        sum += __ldcg(p.psum + k * p.ldp + row);
+      }
       if (p.zsum != nullptr) z += __ldcg(p.zsum + k * p.ldp + row);
     }
   }
@@ -225,16 +286,28 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(const __grid_c
   sums[warp][lane] = sum;
   zs[warp][lane] = z;
   __syncthreads();
-  if (warp != 0 || !ok) return;
-  for (int k = 1; k < kJoinWarps; ++k) {
-    add(tops[k][lane], sums[k][lane]);
-    z += zs[k][lane];
+  const int row = blockIdx.x * 32 + warp;
+  if (row >= live) return;
+  top = tops[lane][warp];
+  sum = sums[lane][warp];
+  z = zs[lane][warp];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    if constexpr (kRelative) {
+      // (both lanes of a pair take the same order: the same bits)
+      const float t = __shfl_xor_sync(0xffffffffu, top, d), o = __shfl_xor_sync(0xffffffffu, sum, d), most = fmaxf(top, t);
+      const float mine = sum == 0.0f && top == -INFINITY ? 0.0f : sum * exp2f(top - most);
+      const float theirs = o == 0.0f && t == -INFINITY ? 0.0f : o * exp2f(t - most);
+      sum = mine + theirs;
+      top = most;
+    } else {
+      sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    }
+    z += __shfl_xor_sync(0xffffffffu, z, d);
   }
-  const float zl = __ldcg(p.r.zlab + row), ref2 = relative ? top : p.r.ref2[row];
-  if (p.mode == CE_JOIN_GRAD && sum > kCeMost) {     // the row's place is off: take it again from its maximum
-    p.r.ref2[row] = top;
-    p.piece->redo = 1;                               // (every writer writes the same)
-  }
+  if (lane != 0) return;
+  const float zl = __ldcg(p.r.zlab + row), ref2 = kRelative ? top : __ldcg(p.r.ref2 + row);
+  if (MODE == CE_JOIN_GRAD && sum > kCeMost) p.piece->redo = 1;     // (every writer writes the same)
   // d: the others' log-sum over the label's logit, in units of ln 2
   const float others = ref2 + log2f(sum), d = others - zl;
   const float tail = log1pf(exp2f(-fabsf(d)));
@@ -243,23 +316,69 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(const __grid_c
   const float eps = p.smoothing;
   p.loss[token] = p.zsum != nullptr ? ce + eps * kLn2 * (zl - z / p.vocab) : ce;
   if (p.lse != nullptr) p.lse[token] = fmaf(zl, kLn2, ce);
-  if (p.mode == CE_JOIN_LOSS) return;
-  const int n = __ldcg(p.r.count);
-  const float g = p.scale / (p.mean ? static_cast<float>(n) : 1.0f);
+  if (MODE == CE_JOIN_LOSS) return;
+  const float g = p.scale / (p.mean ? static_cast<float>(__ldcg(p.r.count)) : 1.0f);
   float slope = 1.0f;
   if (p.cap2 > 0.0f) {
     const float t = zl / p.cap2;
     slope = 1.0f - t * t;
   }
   const float away = expm1f(-ce);                    // p_label - 1
-  if (p.mode == CE_JOIN_EXACT) {
-    p.r.ref2[row] = fmaf(zl, 1.0f, ce * kLog2e);
+  if (MODE == CE_JOIN_EXACT) {
+    p.r.ref2[row] = fmaf(ce, kLog2e, zl);
     p.r.rs[row] = g;
-    p.r.coef[row] = g * slope * (away + eps - eps / p.vocab);
+    p.r.coef[row] = g * slope * (away + eps - p.minus);
   } else {
     p.r.rs[row] = g / (sum + exp2f(zl - ref2));
     p.r.coef[row] = g * slope * (away + eps);
   }
+}
+
+// The block that is the last of its launch to get here sums the losses of all tokens, in a fixed order.
+__device__ __forceinline__ void ce_total(const CeJoinArgs& p) {
+  __shared__ float slots[kJoinWarps];
+  __shared__ int last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(p.r.joined + p.when_redo, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  if (p.mode == CE_JOIN_GRAD && __ldcg(&p.piece->redo) != 0) return;      // left to the second try
+  float v = 0.0f;
+  for (long long m = threadIdx.x; m < p.M;) {        // 32 losses at a time: short chains
+    float part = 0.0f;
+#pragma unroll 8
+    for (int k = 0; k < 32 && m < p.M; ++k, m += 32 * kJoinWarps) part += __ldcg(p.loss + m);
+    v += part;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  v = slots[threadIdx.x];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  const int n = __ldcg(p.r.count);
+  if (threadIdx.x == 0) *p.total = v / static_cast<float>(p.mean && n > 0 ? n : 1);
+}
+
+__global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(const __grid_constant__ CeJoinArgs p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  if (p.when_redo && __ldcg(&p.piece->redo) == 0) return;
+  const int live = __ldcg(&p.piece->live);
+  if (static_cast<int>(blockIdx.x) * 32 < live) {
+    if (p.mode == CE_JOIN_GRAD) {
+      ce_join_rows<CE_JOIN_GRAD>(p, live);
+    } else if (p.mode == CE_JOIN_EXACT) {
+      ce_join_rows<CE_JOIN_EXACT>(p, live);
+    } else {
+      ce_join_rows<CE_JOIN_LOSS>(p, live);
+    }
+  }
+  if (p.total != nullptr) ce_total(p);
 }
 
 struct CeColumnArgs {
@@ -310,7 +429,7 @@ struct CeDxArgs {
   const CePiece* piece;
   CeRows r;                // at the piece's first row
   const float* slab;
-  int tiles_n, h;
+  int tiles_n, band, h;
   const bf16* W;
   const float* column;     // column sums of W, or NULL
   float scale, share;      // logit scale, smoothing / vocab
@@ -322,20 +441,22 @@ struct CeDxArgs {
 __global__ void __launch_bounds__(256) ce_dx_kernel(const __grid_constant__ CeDxArgs p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int live = __ldcg(&p.piece->live), splits = __ldcg(&p.piece->splits);
-  const int per = p.h / 8;
-  const long long tiles = static_cast<long long>((live + 255) / 256) * p.tiles_n, total = static_cast<long long>(live) * per;
-  const int n = __ldcg(p.r.count);
-  const float flat = p.column == nullptr ? 0.0f : p.scale * p.share / (p.mean ? static_cast<float>(n) : 1.0f);
+  const int live = __ldcg(&p.piece->live), whole = __ldcg(&p.piece->whole), splits = __ldcg(&p.piece->splits);
+  const int per = p.h / 8, tiles_m = (live + 255) / 256, cut = tiles_m * p.tiles_n - whole;
+  const long long total = static_cast<long long>(live) * per;
+  const float flat = p.column == nullptr ? 0.0f : p.scale * p.share / (p.mean ? static_cast<float>(__ldcg(p.r.count)) : 1.0f);
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += 256ll * gridDim.x) {
     const int row = static_cast<int>(i / per), c = 8 * static_cast<int>(i - static_cast<long long>(row) * per);
-    const float* src = p.slab + ((static_cast<long long>(row >> 8) * p.tiles_n + (c >> 8)) * 256 + (row & 255)) * 256 + (c & 255);
+    const int place = ce_tile_place(row >> 8, c >> 8, tiles_m, p.tiles_n, p.band);
+    const int parts = place < whole ? 1 : splits;
+    const float* src = p.slab + static_cast<long long>(place) * 65536 + (row & 255) * 256 + (c & 255);
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
 #pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      const uint4 a = ld_global_cg_v4(src + s * tiles * 65536), b = ld_global_cg_v4(src + s * tiles * 65536 + 4);
+    for (int s = 0; s < parts; ++s) {
+      const float* from = src + static_cast<long long>(s) * cut * 65536;
+      const uint4 a = ld_global_cg_v4(from), b = ld_global_cg_v4(from + 4);
       const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] += __uint_as_float(v[e]);
@@ -353,54 +474,23 @@ __global__ void __launch_bounds__(256) ce_dx_kernel(const __grid_constant__ CeDx
   }
 }
 
-struct CeTotalArgs {
-  const float* loss;
-  long long M;
-  const int* count;        // NULL: no tokens
-  int mean;
-  float* total;
-};
-__global__ void __launch_bounds__(1024) ce_total_kernel(const __grid_constant__ CeTotalArgs p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  __shared__ float slots[32];
-  float v = 0.0f;
-  for (long long m = threadIdx.x; m < p.M;) {        // 32 losses at a time: short chains
-    float part = 0.0f;
-#pragma unroll 8
-    for (int k = 0; k < 32 && m < p.M; ++k, m += 1024) part += __ldcg(p.loss + m);
-    v += part;
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
-  __syncthreads();
-  if (threadIdx.x >= 32) return;
-  v = slots[threadIdx.x];
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  const int n = p.count != nullptr ? __ldcg(p.count) : 0;
-  if (threadIdx.x == 0) *p.total = v / static_cast<float>(p.mean && n > 0 ? n : 1);
-}
-
 // ---------------------------------------------------------------- host
 
 struct CePlan {
-  int64_t rows = 0, pieces = 0, slots = 0, lde = 0, slab_tiles = 0;
+  int64_t rows = 0, pieces = 0, slots = 0, blocks = 0, slab_tiles = 0;
   bool exact = false, columns = false;
 };
 static CePlan ce_plan(int64_t M, int64_t h, int64_t vocab, const lora_ce_t& o, bool want_dx) {
   CePlan P;
-  P.slots = ceil_div(vocab, 256) * kCeSlots;
-  P.lde = round_up(vocab, 16);
-  const int64_t per = want_dx ? 2 * P.lde : P.slots * 8;
+  P.slots = ceil_div(vocab, 256) * ce_slots(ce_warps(static_cast<int>(ceil_div(h, kBK))));
+  P.blocks = ceil_div(vocab, kBK);
+  const int64_t per = want_dx ? 2 * kBK * P.blocks : P.slots * 8;
   int64_t most = (want_dx ? kCeGradBytes : kCeStatBytes) / per / 256 * 256;
   if (most < 256) most = 256;
   P.pieces = ceil_div(M, most);
   P.rows = P.pieces > 0 ? round_up(ceil_div(M, P.pieces), 256) : 0;
   const int64_t tiles = P.rows / 256 * ceil_div(h, 256);
-  const int64_t cut = tiles * kCeMaxSplits < kCeSlabTiles ? tiles * kCeMaxSplits : kCeSlabTiles;
-  P.slab_tiles = tiles > cut ? tiles : cut;
+  P.slab_tiles = tiles + (tiles * kCeMaxSplits < kCeTailUnits ? tiles * kCeMaxSplits : kCeTailUnits);
   P.exact = want_dx && o.smoothing > 0.0f && o.softcap > 0.0f;
   P.columns = want_dx && o.smoothing > 0.0f && o.softcap == 0.0f;
   return P;
@@ -412,6 +502,7 @@ struct CeSpace {
   float* loss;
   bf16* packed;
   float2* part;
+  float* psum;
   float* zsum;
   float* column_part;
   float* column;
@@ -422,6 +513,7 @@ static size_t ce_carve(void* ws, int64_t M, int64_t h, const lora_ce_t& o, bool 
   Carve c(ws);
   c.take(kWsHeader);
   s.r.count = c.take_n<int>(1);
+  s.r.joined = c.take_n<unsigned>(2);
   s.piece = c.take_n<CePiece>(P.pieces);
   s.r.pos = c.take_n<int>(M);
   s.r.idx = c.take_n<int>(M);
@@ -433,10 +525,11 @@ static size_t ce_carve(void* ws, int64_t M, int64_t h, const lora_ce_t& o, bool 
   s.loss = c.take_n<float>(M);
   s.packed = c.take_n<bf16>(M * h);
   s.part = c.take_n<float2>(P.slots * P.rows);
+  s.psum = reinterpret_cast<float*>(s.part);       // (never both at a time)
   s.zsum = o.smoothing > 0.0f ? c.take_n<float>(P.slots * P.rows) : nullptr;
   s.column_part = P.columns ? c.take_n<float>(kCeColumnBlocks * h) : nullptr;
   s.column = P.columns ? c.take_n<float>(h) : nullptr;
-  s.e = want_dx ? c.take_n<bf16>(P.rows * P.lde) : nullptr;
+  s.e = want_dx ? c.take_n<bf16>(P.rows * kBK * P.blocks) : nullptr;
   s.slab = want_dx ? c.take_n<float>(P.slab_tiles * 65536) : nullptr;
   return c.off;
 }
@@ -461,7 +554,7 @@ static lora_status_t check_ce(int64_t M, int64_t h, int64_t vocab, const lora_ce
     return LORA_ERR_INVALID_ARG;
   const CeLogit lg = ce_logit_of(*o);
   if (!std::isfinite(lg.k2) || !std::isfinite(lg.cap2) || !std::isfinite(lg.kc)) return LORA_ERR_INVALID_ARG;
-  if (st != LORA_OK || M > kMaxExtent) return LORA_ERR_UNSUPPORTED;
+  if (st != LORA_OK || M > kMaxExtent || vocab > kCeMaxVocab) return LORA_ERR_UNSUPPORTED;
   return h % 8 ? LORA_ERR_ALIGNMENT : LORA_OK;
 }
 
@@ -501,152 +594,156 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
   const CePlan P = ce_plan(M, h, vocab, o, want);
   CeSpace s;
   LGB_TRY(check_ws(ws, ws_bytes, ce_carve(ws, M, h, o, want, P, s)));
-  CeTotalArgs t;
-  t.loss = loss != nullptr ? loss : s.loss;
-  t.M = M;
-  t.count = M > 0 ? s.r.count : nullptr;
-  t.mean = mean;
-  t.total = total;
-  if (M > 0) {
-    unsigned* status = static_cast<unsigned*>(ws);
-    const int tiles_n = static_cast<int>(ceil_div(vocab, 256)), tiles_h = static_cast<int>(ceil_div(h, 256));
-    const int kb_h = static_cast<int>(ceil_div(h, kBK)), kb_v = static_cast<int>(ceil_div(vocab, kBK));
-    const CeLogit lg = ce_logit_of(o);
+  if (M == 0) return cudaMemsetAsync(total, 0, sizeof(float), stream) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+  if (loss == nullptr) loss = s.loss;
+  unsigned* status = static_cast<unsigned*>(ws);
+  const int tiles_n = static_cast<int>(ceil_div(vocab, 256)), tiles_h = static_cast<int>(ceil_div(h, 256));
+  const int kb_h = static_cast<int>(ceil_div(h, kBK)), kb_v = static_cast<int>(ceil_div(vocab, kBK));
+  const CeLogit lg = ce_logit_of(o);
+  const float share = o.smoothing / static_cast<float>(vocab);
 
+  CeGatherArgs gather;
+  gather.x = static_cast<const bf16*>(x);
+  gather.W = static_cast<const bf16*>(W);
+  gather.h = static_cast<int>(h);
+  gather.labels = CeLabels{reinterpret_cast<const long long*>(labels), M, o.ignore_index, vocab};
+  gather.r = s.r;
+  gather.plan = CePieces{s.piece, static_cast<int>(P.pieces), static_cast<int>(P.rows), tiles_h, kb_v, num_sms() / 2};
+  gather.packed = s.packed;
+  gather.lg = lg;
+  gather.want_ref = want && !P.exact;
+  gather.loss = loss;
+  gather.lse = lse;
+  gather.dx = static_cast<bf16*>(dx);
+  gather.status = status;
+  const bool alone = M <= kCeAloneRows;
+  if (!alone) {
     CePackArgs pack;
-    pack.labels = reinterpret_cast<const long long*>(labels);
-    pack.M = M;
-    pack.ignore = o.ignore_index;
-    pack.vocab = vocab;
+    pack.labels = gather.labels;
     pack.r = s.r;
-    pack.piece = s.piece;
-    pack.pieces = static_cast<int>(P.pieces);
-    pack.piece_rows = static_cast<int>(P.rows);
-    pack.tiles_n = tiles_h;
-    pack.kb = kb_v;
-    pack.pairs = num_sms() / 2;
+    pack.plan = gather.plan;
     pack.status = status;
     LGB_TRY(launch_counted(ce_pack_kernel, dim3(1), dim3(1024), 0, LORA_KIND_LOSS, stream, pack));
-
-    CeGatherArgs gather;
-    gather.x = static_cast<const bf16*>(x);
-    gather.W = static_cast<const bf16*>(W);
-    gather.M = M;
-    gather.h = static_cast<int>(h);
-    gather.r = s.r;
-    gather.packed = s.packed;
-    gather.lg = lg;
-    gather.want_ref = want && !P.exact;
-    gather.loss = const_cast<float*>(t.loss);
-    gather.lse = lse;
-    gather.dx = static_cast<bf16*>(dx);
-    const int64_t rows8 = ceil_div(M, 8);
-    LGB_TRY(launch_counted(ce_gather_kernel, dim3(static_cast<unsigned>(rows8 < (1 << 20) ? rows8 : (1 << 20))), dim3(256), 0,
-                           LORA_KIND_LOSS, stream, gather));
-    if (P.columns) {
-      CeColumnArgs ca;
-      ca.W = gather.W;
-      ca.vocab = vocab;
-      ca.h = gather.h;
-      ca.part = s.column_part;
-      ca.sum = s.column;
-      LGB_TRY(launch_counted(ce_column_kernel, dim3(static_cast<unsigned>(ceil_div(h, 1024)), kCeColumnBlocks), dim3(128), 0,
-                             LORA_KIND_LOSS, stream, ca));
-      LGB_TRY(launch_counted(ce_column_join_kernel, dim3(static_cast<unsigned>(ceil_div(h, 32))), dim3(256), 0, LORA_KIND_LOSS,
-                             stream, ca));
-    }
-    for (int64_t k = 0; k < P.pieces; ++k) {
-      const int64_t row0 = k * P.rows;
-      const int64_t rows = M - row0 < P.rows ? M - row0 : P.rows;
-      if (rows <= 0) break;
-      CeRows r = s.r;
-      r.idx += row0;
-      r.label += row0;
-      r.ref2 += row0;
-      r.zlab += row0;
-      r.rs += row0;
-      r.coef += row0;
-      CeGemmParams g;
-      std::memset(static_cast<void*>(&g), 0, sizeof(g));
-      if (!encode_map(&g.a, s.packed + row0 * h, h, rows, h, kBK, kBM) || !encode_map(&g.b, W, h, vocab, h, kBK, 128))
-        return LORA_ERR_CUDA;
-      g.piece = s.piece + k;
-      g.kb_total = kb_h;
-      g.kvalid = static_cast<int>(h);
-      g.tiles_n = tiles_n;
-      g.band = raster_band();
-      g.status = status;
-      g.vocab = static_cast<int>(vocab);
-      g.lg = lg;
-      g.label = r.label;
-      g.ref2 = r.ref2;
-      g.part = s.part;
-      g.zsum = s.zsum;
-      g.zlab = r.zlab;
-      g.ldp = P.rows;
-      g.e = s.e;
-      g.lde = P.lde;
-      g.minus = P.exact ? o.smoothing / static_cast<float>(vocab) : 0.0f;
-      CeJoinArgs j;
-      j.piece = s.piece + k;
-      j.r = r;
-      j.part = s.part;
-      j.zsum = s.zsum;
-      j.ldp = P.rows;
-      j.slots = static_cast<int>(P.slots);
-      j.vocab = static_cast<int>(vocab);
-      j.cap2 = lg.cap2;
-      j.scale = o.logit_scale;
-      j.smoothing = o.smoothing;
-      j.mean = mean;
-      j.loss = const_cast<float*>(t.loss);
-      j.lse = lse;
-      auto join = [&](int mode) {
-        j.mode = mode;
-        return launch_counted(ce_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 32))), dim3(32 * kJoinWarps), 0,
-                              LORA_KIND_LOSS, stream, j);
-      };
-      if (!want || P.exact) {
-        LGB_TRY(ce_gemm(CE_STATS, g, stream));
-        LGB_TRY(join(want ? CE_JOIN_EXACT : CE_JOIN_LOSS));
-      }
-      if (!want) continue;
-      if (P.exact) g.zsum = nullptr;
-      LGB_TRY(ce_gemm(CE_GRAD, g, stream));
-      if (!P.exact) {
-        LGB_TRY(join(CE_JOIN_GRAD));
-        g.when_redo = 1;
-        LGB_TRY(ce_gemm(CE_GRAD, g, stream));
-        LGB_TRY(join(CE_JOIN_REDO));
-      }
-      CeGemmParams d;
-      std::memset(static_cast<void*>(&d), 0, sizeof(d));
-      if (!encode_map(&d.a, s.e, vocab, rows, P.lde, kBK, kBM) || !encode_map(&d.b, W, h, vocab, h, 64, 64))
-        return LORA_ERR_CUDA;
-      d.piece = s.piece + k;
-      d.kb_total = kb_v;
-      d.kvalid = static_cast<int>(vocab);
-      d.tiles_n = tiles_h;
-      d.band = raster_band();
-      d.status = status;
-      d.slab = s.slab;
-      LGB_TRY(ce_gemm(CE_PART, d, stream));
-      CeDxArgs a;
-      a.piece = s.piece + k;
-      a.r = r;
-      a.slab = s.slab;
-      a.tiles_n = tiles_h;
-      a.h = static_cast<int>(h);
-      a.W = gather.W;
-      a.column = s.column;
-      a.scale = o.logit_scale;
-      a.share = o.smoothing / static_cast<float>(vocab);
-      a.mean = mean;
-      a.dx = gather.dx;
-      const int64_t blocks = ceil_div(rows * (h / 8), 256);
-      LGB_TRY(launch_counted(ce_dx_kernel, dim3(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20))), dim3(256), 0,
-                             LORA_KIND_LOSS, stream, a));
-    }
   }
-  return launch_counted(ce_total_kernel, dim3(1), dim3(1024), 0, LORA_KIND_LOSS, stream, t);
+  const int64_t rows8 = ceil_div(M, 8);
+  LGB_TRY(launch_counted(alone ? ce_gather_kernel<true> : ce_gather_kernel<false>,
+                         dim3(static_cast<unsigned>(rows8 < (1 << 20) ? rows8 : (1 << 20))), dim3(256), 0, LORA_KIND_LOSS,
+                         stream, gather));
+  if (P.columns) {
+    CeColumnArgs ca;
+    ca.W = gather.W;
+    ca.vocab = vocab;
+    ca.h = gather.h;
+    ca.part = s.column_part;
+    ca.sum = s.column;
+    LGB_TRY(launch_counted(ce_column_kernel, dim3(static_cast<unsigned>(ceil_div(h, 1024)), kCeColumnBlocks), dim3(128), 0,
+                           LORA_KIND_LOSS, stream, ca));
+    LGB_TRY(launch_counted(ce_column_join_kernel, dim3(static_cast<unsigned>(ceil_div(h, 32))), dim3(256), 0, LORA_KIND_LOSS,
+                           stream, ca));
+  }
+  for (int64_t k = 0; k < P.pieces; ++k) {
+    const int64_t row0 = k * P.rows;
+    const int64_t rows = M - row0 < P.rows ? M - row0 : P.rows;
+    if (rows <= 0) break;
+    CeRows r = s.r;
+    r.idx += row0;
+    r.label += row0;
+    r.ref2 += row0;
+    r.zlab += row0;
+    r.rs += row0;
+    r.coef += row0;
+    CeGemmParams g;
+    std::memset(static_cast<void*>(&g), 0, sizeof(g));
+    if (!encode_map(&g.a, s.packed + row0 * h, h, rows, h, kBK, kBM) || !encode_map(&g.b, W, h, vocab, h, kBK, 128))
+      return LORA_ERR_CUDA;
+    g.piece = s.piece + k;
+    g.kb_total = kb_h;
+    g.kvalid = static_cast<int>(h);
+    g.tiles_n = tiles_n;
+    g.band = raster_band();
+    g.status = status;
+    g.vocab = static_cast<int>(vocab);
+    g.lg = lg;
+    g.label = r.label;
+    g.ref2 = r.ref2;
+    g.part = s.part;
+    g.psum = s.psum;
+    g.zlab = r.zlab;
+    g.ldp = P.rows;
+    g.e = s.e;
+    g.blocks = static_cast<int>(P.blocks);
+    g.minus = P.exact ? share : 0.0f;
+    CeJoinArgs j;
+    j.piece = s.piece + k;
+    j.r = r;
+    j.part = s.part;
+    j.psum = s.psum;
+    j.zsum = s.zsum;
+    j.ldp = P.rows;
+    j.slots = static_cast<int>(P.slots);
+    j.vocab = static_cast<int>(vocab);
+    j.cap2 = lg.cap2;
+    j.scale = o.logit_scale;
+    j.smoothing = o.smoothing;
+    j.minus = g.minus;
+    j.mean = mean;
+    j.loss = loss;
+    j.lse = lse;
+    j.total = row0 + rows == M ? total : nullptr;
+    j.M = M;
+    auto join = [&](int mode, int when_redo) {
+      j.mode = mode;
+      j.when_redo = when_redo;
+      return launch_counted(ce_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 32))), dim3(32 * kJoinWarps), 0,
+                            LORA_KIND_LOSS, stream, j);
+    };
+    // the row's sum on its own, then (for dx) exponentials relative to it
+    auto exact = [&](int when_redo) {
+      g.when_redo = when_redo;
+      g.zsum = s.zsum;
+      LGB_TRY(ce_gemm(CE_STATS, g, stream));
+      LGB_TRY(join(want ? CE_JOIN_EXACT : CE_JOIN_LOSS, when_redo));
+      g.zsum = nullptr;
+      return want ? ce_gemm(CE_GRAD, g, stream) : LORA_OK;
+    };
+    if (!want || P.exact) {
+      LGB_TRY(exact(0));
+    } else {
+      g.zsum = s.zsum;
+      LGB_TRY(ce_gemm(CE_GRAD, g, stream));
+      LGB_TRY(join(CE_JOIN_GRAD, 0));
+      LGB_TRY(exact(1));
+    }
+    if (!want) continue;
+    CeGemmParams d;
+    std::memset(static_cast<void*>(&d), 0, sizeof(d));
+    if (!encode_map(&d.a, s.e, kBK, P.rows * P.blocks, kBK, kBK, kBM) || !encode_map(&d.b, W, h, vocab, h, 64, 64))
+      return LORA_ERR_CUDA;
+    d.piece = s.piece + k;
+    d.blocks = static_cast<int>(P.blocks);
+    d.kb_total = kb_v;
+    d.kvalid = static_cast<int>(vocab);
+    d.tiles_n = tiles_h;
+    d.band = raster_band();
+    d.status = status;
+    d.slab = s.slab;
+    LGB_TRY(ce_gemm(CE_PART, d, stream));
+    CeDxArgs a;
+    a.piece = s.piece + k;
+    a.r = r;
+    a.slab = s.slab;
+    a.tiles_n = tiles_h;
+    a.band = d.band;
+    a.h = static_cast<int>(h);
+    a.W = gather.W;
+    a.column = s.column;
+    a.scale = o.logit_scale;
+    a.share = share;
+    a.mean = mean;
+    a.dx = gather.dx;
+    const int64_t blocks = ceil_div(rows * (h / 8), 256);
+    LGB_TRY(launch_counted(ce_dx_kernel, dim3(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20))), dim3(256), 0,
+                           LORA_KIND_LOSS, stream, a));
+  }
+  return LORA_OK;
 }

@@ -95,7 +95,7 @@ def test_norm_workspace_query(L):
 @pytest.mark.usefixtures("nothing_is_launched")
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), INVALID), (dict(h=0), INVALID), (dict(V=0), INVALID), (dict(h=60), ALIGNMENT), (dict(M=1 << 31), UNSUPPORTED),
-    (dict(V=1 << 31), UNSUPPORTED), (dict(h=1 << 31), UNSUPPORTED), (dict(x=None), INVALID), (dict(W=None), INVALID),
+    (dict(V=1 << 31), UNSUPPORTED), (dict(V=(1 << 24) + 1), UNSUPPORTED), (dict(h=1 << 31), UNSUPPORTED), (dict(x=None), INVALID), (dict(W=None), INVALID),
     (dict(labels=None), INVALID), (dict(opts=None), INVALID), (dict(total=None), INVALID), (dict(scale=0.0), INVALID),
     (dict(scale=NAN), INVALID), (dict(scale=INF), INVALID), (dict(softcap=-1.0), INVALID), (dict(softcap=NAN), INVALID),
     (dict(softcap=1e-45), INVALID), (dict(softcap=3e38), INVALID), (dict(smoothing=-0.1), INVALID), (dict(smoothing=1.0), INVALID),
