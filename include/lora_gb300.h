@@ -487,7 +487,7 @@ typedef struct {
 /* The norm of all tensors of a list together: (sum g^2)^(1/2) (LORA_GRAD_NORM_2) or max |g|
  * (LORA_GRAD_NORM_INF; a NaN if there is one), f32 [1], 0 for a list of nothing.  Squares and their
  * sums are f32, in short chains whose order depends on the counts and the tensors' alignment
- * alone: the first kind is infinite beyond 1.8e19.
+ * alone: the first kind is infinite beyond 1.8e19, and elements below 1e-23 count as zero.
  * lora_clip_grads: out_i = g_i * min(1, max_norm / (norm + 1e-6)), rounded once to its type;
  * norm receives the norm before it.  A norm that is not finite goes into the factor as it is:
  * infinite gives 0 (and NaN for an infinite element), NaN gives NaN.  out: NULL (in place, and

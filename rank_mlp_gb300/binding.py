@@ -933,6 +933,8 @@ class TensorList:
             flat += (t.data_ptr(), t.numel(), dtype)
         self._bytes = _pack_tensors(flat)
         self._examples = None
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for t in self.tensors if t.numel())
+        self.overlap = any(a[1] > b[0] for a, b in zip(spans, spans[1:]))
 
     def __len__(self):
         return len(self.tensors)
@@ -987,12 +989,15 @@ def grad_norm(grads, *, norm_type=2.0, ws=None):
 
 def clip_grad_norm(grads, max_norm, *, norm_type=2.0, out=None, ws=None):
     """Scales all gradients by min(1, max_norm / (norm + 1e-6)), in place or into out (a list of the same shapes and
-    types).  Returns their norm before that, f32, 0-dim."""
+    types).  Returns their norm before that, f32, 0-dim.  What is written must not overlap: a gradient twice in the
+    list would be scaled twice."""
     lib = _LIB or load()
     grads = tensor_list(grads)
     t = _list_device(grads)
+    out = None if out is None else tensor_list(out)
+    if (out or grads).overlap:
+        raise ValueError("tensors that are written overlap")
     if out is not None:
-        out = tensor_list(out)
         if len(out) != len(grads):                   # (sizes and types are compared in the library)
             raise ValueError("out must match the gradients, tensor by tensor")
         if out.tensors:
@@ -1025,6 +1030,8 @@ def clip_examples(grads, max_norm, *, sq_norms=None, scale=1.0, out=None, ws=Non
         out = tensor_list(out)
         if len(out) != len(grads) or any(o.shape != sh or o.dtype != torch.float32 for o, sh in zip(out.tensors, shapes)):
             raise ValueError("out must be f32 tensors of one example's shapes")
+        if out.overlap:
+            raise ValueError("tensors that are written overlap")
         sums, packed = list(out.tensors), out._bytes
     given = sq_norms is not None
     if not given:

@@ -691,7 +691,7 @@ extern "C" const char* lora_status_string(lora_status_t status) {
     case LORA_OK: return "ok";
     case LORA_ERR_INVALID_ARG: return "invalid argument";
     case LORA_ERR_ALIGNMENT: return "alignment: pointers 16-byte (ws/saved 256-byte), feature sizes multiples of 8";
-    case LORA_ERR_UNSUPPORTED: return "unsupported: rank too large for the fold";
+    case LORA_ERR_UNSUPPORTED: return "unsupported: a size or rank beyond the limits";
     case LORA_ERR_WORKSPACE: return "workspace smaller than the size query";
     case LORA_ERR_CUDA: return "CUDA runtime or launch failure";
     case LORA_ERR_TIMEOUT: return "a kernel's bounded wait expired";

@@ -78,6 +78,26 @@ def test_neighbours_are_left_alone(lib):
     assert not torch.equal(flat, before)
 
 
+def test_overlapping_outputs_are_refused(lib):
+    """The norm of a list may see a tensor twice; nothing is written twice."""
+    t = rnd(100, dtype=torch.float32)
+    want = norm64([t, t], 2.0)
+    assert abs(float(lib.grad_norm([t, t])) - want) <= 256 * F32 * want
+    before = t.clone()
+    for bad in ([t, t], [t, t[50:]], [t[:60], t[59:]]):
+        with pytest.raises(ValueError, match="overlap"):
+            lib.clip_grad_norm(bad, 1e-3)
+    with pytest.raises(ValueError, match="overlap"):
+        lib.clip_grad_norm([t, t], 1e-3, out=[before, before])
+    g, o = rnd(2, 30), torch.zeros(30, device=DEV)
+    with pytest.raises(ValueError, match="overlap"):
+        lib.clip_examples([g, g], 1.0, out=[o, o])
+    assert torch.equal(t, before)
+    a, b = torch.empty_like(t), torch.empty_like(t)
+    lib.clip_grad_norm([t, t], 1e-3, out=[a, b])
+    assert torch.equal(a, b) and not torch.equal(a, t)
+
+
 def test_types_and_alignments_mixed(lib):
     """bf16 and f32 in one list; an output at another distance from a 16-byte boundary than its input."""
     b, f = rnd(5000), rnd(5000, seed=1, dtype=torch.float32)
