@@ -54,6 +54,7 @@ struct CeGemmParams {
   int when_redo;           // 1: only if the piece's `redo` is set
   int kb_total, kvalid;    // 64-wide k-blocks, valid K
   int tiles_n, band;
+  int narrow;              // CE_PART: 1 if the last n-tile is 128 columns wide
   unsigned* status;
   unsigned long long timeout_ns;
   int inject_stall;
@@ -160,19 +161,25 @@ struct CeUnit {
   int u, tm, tn, kb0, kb1;
 };
 struct CeIter {
-  int u, step, end, whole, tail, tiles_m, splits;
+  int q, turn, step, end, whole, tail, tiles_m, splits;
   __device__ __forceinline__ CeIter(const CeGemmParams& p, int live, int whole_, int splits_, int pair, int npairs) {
     tiles_m = (live + 2 * kBM - 1) / (2 * kBM);
     const int tiles = tiles_m * p.tiles_n;
     whole = whole_ < 0 ? tiles : min(whole_, tiles);
     tail = tiles - whole;
     splits = splits_;
-    u = pair;
+    q = pair;
+    turn = 0;
     step = npairs;
     end = whole + tail * splits;
   }
+  // Dealt round-robin, each round starting one pair further: a pair's units then fall on different
+  // n-tiles, and the narrow one is every pair's in turn.
   __device__ __forceinline__ bool next(const CeGemmParams& p, CeUnit& U) {
+    const int u = turn * step + q;
     if (u >= end) return false;
+    ++turn;
+    if (++q == step) q = 0;
     int t = u;
     U.u = u;
     U.kb0 = 0;
@@ -188,7 +195,6 @@ struct CeIter {
     const int nb = min(p.band, p.tiles_n - b * p.band);
     U.tm = rem / nb;
     U.tn = b * p.band + rem % nb;
-    u += step;
     return true;
   }
 };
@@ -385,7 +391,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(WARPS),
       CeUnit U;
       while (ok && it.next(p, U)) {
         const int a_row = U.tm * (2 * kBM) + static_cast<int>(rank) * kBM;
-        const int b_row = U.tn * BN + static_cast<int>(rank) * C::kBLocal;
+        const bool narrow = KIND == CE_PART && p.narrow && U.tn == p.tiles_n - 1;
+        const int b_row = U.tn * BN + static_cast<int>(rank) * (narrow ? C::kBLocal / 2 : C::kBLocal);
         for (int j = U.kb0; j < U.kb1; ++j) {
           const int kc = j * kBK;
           if (!ce_wait(empty_bar(stage), phase ^ 1u, abort_flag, p)) { ok = false; break; }
@@ -397,7 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(WARPS),
           }
           first_stage = false;
           if (leader) {
-            mbar_arrive_expect_tx(fb, C::kTxBytes);
+            mbar_arrive_expect_tx(fb, narrow ? C::kTxBytes - C::kBBytes : C::kTxBytes);
             armed[stage] = static_cast<int>(phase);
           }
           const uint32_t fb_even = mapa_shared(fb, 0);
@@ -412,7 +419,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(WARPS),
             tma_load_2d_pair(sb, &p.b, fb_even, kc, b_row);
           } else {
 #pragma unroll
-            for (int c = 0; c < C::kBLocal / 64; ++c) tma_load_2d_pair(sb + c * 8192u, &p.b, fb_even, b_row + c * 64, kc);
+            for (int c = 0; c < C::kBLocal / 64; ++c)
+              if (c == 0 || !narrow) tma_load_2d_pair(sb + c * 8192u, &p.b, fb_even, b_row + c * 64, kc);
           }
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
@@ -427,7 +435,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(WARPS),
     if (leader && lane == 0) {
       // kept lean as in the projections' kernel: descriptors are stage 0's plus constants, the
       // next stage is tested before this stage's last MMA
-      constexpr uint32_t idesc = idesc_bf16_f32(2 * kBM, BN, 0, B_MN ? 1 : 0);
+      constexpr uint32_t idesc_full = idesc_bf16_f32(2 * kBM, BN, 0, B_MN ? 1 : 0);
+      constexpr uint32_t idesc_narrow = idesc_bf16_f32(2 * kBM, BN / 2, 0, B_MN ? 1 : 0);
       const uint64_t adesc0 = smem_desc_sw128(sbase, 16u, 1024u);
       const uint64_t bdesc0 = B_MN ? smem_desc_sw128(sbase + C::kABytes, 8192u, 1024u)
                                    : smem_desc_sw128(sbase + C::kABytes, 16u, 1024u);
@@ -446,6 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(WARPS),
         if (!ce_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p)) { ok = false; break; }
         tc_fence_after_sync();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+        const uint32_t idesc = KIND == CE_PART && p.narrow && U.tn == p.tiles_n - 1 ? idesc_narrow : idesc_full;
         uint32_t accumulate = 0;
         for (int j = U.kb0; j < U.kb1; ++j) {
           const int kc = j * kBK;
@@ -510,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(WARPS),
         constexpr int kSpan = BN / ce_slots(WARPS);
         float* dst = p.slab + (static_cast<long long>(U.u) * (2 * kBM) + row_in_tile) * BN;
 #pragma unroll 1
-        for (int c = part * kSpan; c < (part + 1) * kSpan; c += 32) {
+        for (int c = part * kSpan; c < (part + 1) * kSpan && (c < BN / 2 || !p.narrow || U.tn < p.tiles_n - 1); c += 32) {
           uint32_t v[32];
           __syncwarp();
           tmem_ld32(tacc + c, v);

@@ -285,8 +285,16 @@ __device__ __forceinline__ void ce_join_rows(const CeJoinArgs& p, int live) {
   tops[warp][lane] = top;
   sums[warp][lane] = sum;
   zs[warp][lane] = z;
-  __syncthreads();
   const int row = blockIdx.x * 32 + warp;
+  float zl = 0.0f, ref2 = 0.0f;                      // (on their way across the barrier)
+  int token = 0, count = 1;
+  if (row < live) {
+    zl = __ldcg(p.r.zlab + row);
+    if (!kRelative) ref2 = __ldcg(p.r.ref2 + row);
+    token = __ldg(p.r.idx + row);
+    count = __ldcg(p.r.count);
+  }
+  __syncthreads();
   if (row >= live) return;
   top = tops[lane][warp];
   sum = sums[lane][warp];
@@ -306,18 +314,17 @@ __device__ __forceinline__ void ce_join_rows(const CeJoinArgs& p, int live) {
     z += __shfl_xor_sync(0xffffffffu, z, d);
   }
   if (lane != 0) return;
-  const float zl = __ldcg(p.r.zlab + row), ref2 = kRelative ? top : __ldcg(p.r.ref2 + row);
+  if (kRelative) ref2 = top;
   if (MODE == CE_JOIN_GRAD && sum > kCeMost) p.piece->redo = 1;     // (every writer writes the same)
   // d: the others' log-sum over the label's logit, in units of ln 2
   const float others = ref2 + log2f(sum), d = others - zl;
   const float tail = log1pf(exp2f(-fabsf(d)));
   const float ce = d > 0.0f ? fmaf(d, kLn2, tail) : tail;
-  const int token = __ldg(p.r.idx + row);
   const float eps = p.smoothing;
   p.loss[token] = p.zsum != nullptr ? ce + eps * kLn2 * (zl - z / p.vocab) : ce;
   if (p.lse != nullptr) p.lse[token] = fmaf(zl, kLn2, ce);
   if (MODE == CE_JOIN_LOSS) return;
-  const float g = p.scale / (p.mean ? static_cast<float>(__ldcg(p.r.count)) : 1.0f);
+  const float g = p.scale / (p.mean ? static_cast<float>(count) : 1.0f);
   float slope = 1.0f;
   if (p.cap2 > 0.0f) {
     const float t = zl / p.cap2;
@@ -724,6 +731,7 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
     d.kb_total = kb_v;
     d.kvalid = static_cast<int>(vocab);
     d.tiles_n = tiles_h;
+    d.narrow = h - (tiles_h - 1) * int64_t(256) <= 128;
     d.band = raster_band();
     d.status = status;
     d.slab = s.slab;
