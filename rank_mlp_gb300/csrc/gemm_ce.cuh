@@ -16,6 +16,11 @@
 //
 // Rows are the labelled tokens, packed; their number is on the device, so a launch covers the
 // most rows there can be and its units follow from the number it finds.
+//
+// Bound by the matrix units and, at 14 k-blocks a tile, by what the epilogue adds: 3686 rows x 896
+// against 131072 words take 600 us (1.44 PFLOP/s), 538 without the stores of the exponentials, 558 with
+// them all in one place (so their way to memory costs most), 505 with no epilogue.  At 64 k-blocks
+// capped logits run at 1.5 to 1.6 PFLOP/s, the loss alone at 1.75; CE_PART at 1.55 to 1.75.
 #pragma once
 
 #include "gemm_pair.cuh"
@@ -25,10 +30,10 @@ namespace lgb {
 enum CeKind : int { CE_STATS = 0, CE_GRAD = 1, CE_PART = 2 };
 
 constexpr int kCeStages = 6;
-// Epilogue warps: one or two for each TMEM lane quarter, and so partial results of a row in one tile.
-constexpr int kCeShortKb = 32;           // logits of at most this many k-blocks take eight
-constexpr int ce_warps(int kb) { return kb <= kCeShortKb ? 8 : 4; }
-constexpr int ce_slots(int warps) { return warps / 4; }
+// Eight epilogue warps, two for each TMEM lane quarter, and so two partial results of a row in a tile.
+// (Four took as long at 14 and at 64 k-blocks a tile: 1275 and 5282 us for 1271 and 5306 with eight.)
+constexpr int kCeWarps = 8;
+constexpr int kCeSlots = kCeWarps / 4;
 constexpr int kCeMaxSplits = 32;
 constexpr int kCeTailUnits = 304;        // units of a launch at most that are parts of tiles
 constexpr float kLog2e = 1.4426950408889634f;
@@ -63,9 +68,9 @@ struct CeGemmParams {
   CeLogit lg;
   const int* label;
   const float* ref2;
-  float2* part;            // CE_STATS: [tiles_n * slots][ldp] (maximum, sum), both without the label
+  float2* part;            // CE_STATS: [tiles_n * kCeSlots][ldp] (maximum, sum), both without the label
   float* psum;             // CE_GRAD: the sums alone
-  float* zsum;             // [tiles_n * slots][ldp] sums of z2, label included, or NULL
+  float* zsum;             // [tiles_n * kCeSlots][ldp] sums of z2, label included, or NULL
   float* zlab;             // the label's z2
   long long ldp;
   __nv_bfloat16* e;        // [rows / 128][blocks][128][64]: what one CTA takes of a k-block together
@@ -283,10 +288,10 @@ __device__ __forceinline__ void ce_chunk(const CeGemmParams& p, const uint32_t (
 // The epilogue of one tile row: the warp's share `part` of the tile's columns, 32 at a time, each read
 // from tensor memory while those before are worked on; release() once all have been read.
 // Warp-collective; `ok`: the row is one of the piece's.
-template <int KIND, int WARPS, bool CAP, typename F>
+template <int KIND, bool CAP, typename F>
 __device__ __forceinline__ void ce_rows(const CeGemmParams& p, const CeUnit& U, uint32_t tacc, int row, bool ok, int part,
                                         F&& release) {
-  constexpr int BN = 256, kSlots = ce_slots(WARPS), kSpan = BN / kSlots;
+  constexpr int BN = 256, kSpan = BN / kCeSlots;
   const uint32_t from = tacc + part * kSpan;
   const int first = U.tn * BN + part * kSpan;
   uint32_t va[32], vb[32];
@@ -311,18 +316,18 @@ __device__ __forceinline__ void ce_rows(const CeGemmParams& p, const CeUnit& U, 
     ce_chunk<KIND, CAP>(p, vb, first + c + 32, row, ok, label, ref2, top, sum, zs);
   }
   if (ok) {
-    const long long at = (static_cast<long long>(U.tn) * kSlots + part) * p.ldp + row;
+    const long long at = (static_cast<long long>(U.tn) * kCeSlots + part) * p.ldp + row;
     if (KIND == CE_STATS) p.part[at] = make_float2(top, sum); else p.psum[at] = sum;
     if (p.zsum != nullptr) p.zsum[at] = zs;
   }
 }
 
-template <int KIND, int WARPS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(WARPS), 1)
+template <int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarps), 1)
     ce_gemm_kernel(const __grid_constant__ CeGemmParams p) {
   constexpr int STAGES = kCeStages;
   constexpr bool B_MN = KIND == CE_PART;
-  using C = PairCfg<STAGES, WARPS>;
+  using C = PairCfg<STAGES, kCeWarps>;
   constexpr int BN = C::BN;
   if (p.when_redo) {                      // the second try, seldom needed: leave before taking anything
     pdl_wait();
@@ -355,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(WARPS),
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 2 * WARPS);
+      mbar_init(tempty_bar(a), 2 * kCeWarps);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -517,7 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(WARPS),
         if (lane == 0) arrive_read(tempty_even[acc]);
       };
       if constexpr (KIND == CE_PART) {
-        constexpr int kSpan = BN / ce_slots(WARPS);
+        constexpr int kSpan = BN / kCeSlots;
         float* dst = p.slab + (static_cast<long long>(U.u) * (2 * kBM) + row_in_tile) * BN;
 #pragma unroll 1
         for (int c = part * kSpan; c < (part + 1) * kSpan && (c < BN / 2 || !p.narrow || U.tn < p.tiles_n - 1); c += 32) {
@@ -533,9 +538,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(WARPS),
         release();
       } else {
         if (p.lg.cap2 > 0.0f) {
-          ce_rows<KIND, WARPS, true>(p, U, tacc, row, row < live, part, release);
+          ce_rows<KIND, true>(p, U, tacc, row, row < live, part, release);
         } else {
-          ce_rows<KIND, WARPS, false>(p, U, tacc, row, row < live, part, release);
+          ce_rows<KIND, false>(p, U, tacc, row, row < live, part, release);
         }
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }

@@ -489,7 +489,7 @@ struct CePlan {
 };
 static CePlan ce_plan(int64_t M, int64_t h, int64_t vocab, const lora_ce_t& o, bool want_dx) {
   CePlan P;
-  P.slots = ceil_div(vocab, 256) * ce_slots(ce_warps(static_cast<int>(ceil_div(h, kBK))));
+  P.slots = ceil_div(vocab, 256) * kCeSlots;
   P.blocks = ceil_div(vocab, kBK);
   const int64_t per = want_dx ? 2 * kBK * P.blocks : P.slots * 8;
   int64_t most = (want_dx ? kCeGradBytes : kCeStatBytes) / per / 256 * 256;

