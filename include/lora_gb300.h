@@ -456,8 +456,8 @@ lora_status_t lora_rms_norm_backward(int64_t M, int dim, const lora_heads_t* dy,
  * NULL (the loss alone).  dx may not be x.
  * Logits, their exponentials and all sums are f32.  For dx the exponentials of all but the
  * label's are rounded to bf16 on their way to the product with W, the label's stays f32.
- * Tokens are taken in pieces of up to 1 GiB of such exponentials, which live in the
- * workspace.  h a multiple of 8; vocab at most 2^24; x, W, dx 16-byte aligned.  logit_scale finite, not 0;
+ * Tokens are taken in pieces of up to 1 GiB of such exponentials and as much of f32 sums, which live
+ * in the workspace.  h a multiple of 8; vocab at most 2^24; x, W, dx 16-byte aligned.  logit_scale finite, not 0;
  * softcap finite, >= 0; 0 <= smoothing < 1.
  * ws: lora_linear_ce_workspace_bytes (0 for sizes or options that the call refuses), which
  * grows with M by x's own size and the pieces. */

@@ -274,8 +274,7 @@ __device__ __forceinline__ void ce_chunk(const CeGemmParams& p, const uint32_t (
       }
       sum += s0 + s1;
       if (ok) {
-        // (row by row the same stores, 64 bytes each a whole row of the vocabulary apart, took a sixth
-        // of the launch)
+        // (the same stores into rows of the whole vocabulary: 635 us for 608)
         __nv_bfloat16* dst = p.e + (static_cast<long long>(row >> 7) * p.blocks + (col0 >> 6)) * 8192 + (row & 127) * 64 + (col0 & 63);
         st_global_v8(dst, w);
         st_global_v8(dst + 16, w + 8);

@@ -19,7 +19,7 @@ namespace lgb {
 
 constexpr float kCeAhead = 40.0f * kLog2e;         // the reference above the label's logit
 constexpr float kCeMost = 1.5474250491067253e26f;  // 2^87: a row's sum of exponentials past it is taken again
-constexpr int64_t kCeGradBytes = int64_t(1) << 30; // exponentials of a piece
+constexpr int64_t kCeGradBytes = int64_t(1) << 30; // exponentials of a piece, and its product's sums
 constexpr int64_t kCeStatBytes = int64_t(1) << 28; // partial results of a piece (the loss alone)
 constexpr int64_t kCeMaxVocab = int64_t(1) << 24;   // (256 rows' exponentials stay in a TMA map's reach)
 constexpr int kCeColumnBlocks = 304;               // row ranges of W for its column sums
@@ -493,6 +493,8 @@ static CePlan ce_plan(int64_t M, int64_t h, int64_t vocab, const lora_ce_t& o, b
   P.blocks = ceil_div(vocab, kBK);
   const int64_t per = want_dx ? 2 * kBK * P.blocks : P.slots * 8;
   int64_t most = (want_dx ? kCeGradBytes : kCeStatBytes) / per / 256 * 256;
+  const int64_t sums = kCeGradBytes / (4 * round_up(h, 256)) / 256 * 256;
+  if (want_dx && most > sums) most = sums;
   if (most < 256) most = 256;
   P.pieces = ceil_div(M, most);
   P.rows = P.pieces > 0 ? round_up(ceil_div(M, P.pieces), 256) : 0;

@@ -138,6 +138,20 @@ def test_the_largest_lists_keep_their_precision(lib):
     assert abs(float(lib.grad_norm([t])) - want) <= 256 * F32 * want
 
 
+def test_a_tensor_beyond_32_bit_offsets(lib):
+    """2^31 + 5 elements, and an example's gradients of which the last start past 2^31."""
+    t = torch.zeros((1 << 31) + 5, dtype=torch.bfloat16, device=DEV)
+    t[-3:] = torch.tensor([3.0, -4.0, 12.0], device=DEV)
+    assert float(lib.grad_norm([t])) == 13.0
+    lib.clip_grad_norm([t], 6.5)
+    within(t[-3:], torch.tensor([1.5, -2.0, 6.0], device=DEV).double(), 2 * BF16 * 6.0)
+    del t
+    g = torch.zeros(3, 1 << 30, dtype=torch.bfloat16, device=DEV)
+    g[:, -1] = torch.tensor([1.0, 2.0, 4.0], device=DEV)
+    (s,), sq = lib.clip_examples([g], 2.0)
+    assert sq.tolist() == [1.0, 4.0, 16.0] and float(s[-1]) == 5.0 and not bool(s[:-1].any())
+
+
 def test_lists_are_kept_and_replayed(lib):
     """A list built once serves later calls and a captured one, whose launch keeps its own copy."""
     _, ts = flat_list([4096, 4096, 30], torch.bfloat16)

@@ -155,6 +155,46 @@ def test_pieces(lib, grad):
         assert abs(float(total) - float(loss.double().sum()) / n) <= 4 * F32 * float(loss.double().sum()) / n
 
 
+def test_pieces_of_a_small_vocabulary(lib):
+    """The product's f32 sums bound the piece: 512 tokens at the widest rows here."""
+    M, h, V = 1100, 1 << 19, 24
+    g = torch.Generator(device=DEV).manual_seed(3)
+    W = (torch.randn(V, h, generator=g, device=DEV) * h ** -0.5).to(torch.bfloat16)
+    x = (2 * torch.randn(M, h, generator=g, device=DEV)).to(torch.bfloat16)
+    y = torch.randint(0, V, (M,), generator=g, device=DEV)
+    y[::9] = -100
+    total, loss, lse, dx = lib.linear_cross_entropy(x, W, y)
+    n = int((y != -100).sum())
+    for part in (slice(0, 40), slice(560, 600), slice(1080, 1100)):
+        _, l64, s64, d64, off, slack = ce64(x[part], W, y[part], reduction="sum")
+        within(loss[part], l64, off + 4 * F32 * l64.abs(), "loss")
+        within(dx[part], d64 / n, slack / n, "dx")
+    assert lib.poll_status() == 0
+
+
+def test_a_head_beyond_32_bit_offsets(lib):
+    """2.5G weights: rows far past 2^31 elements, for the logits, the label's row and the gradient."""
+    M, h, V = 40, 4096, 600_000
+    g = torch.Generator(device=DEV).manual_seed(4)
+    W = torch.empty(V, h, dtype=torch.bfloat16, device=DEV)
+    for a in range(0, V, 50_000):
+        W[a:a + 50_000] = torch.randn(50_000, h, generator=g, device=DEV) * h ** -0.5
+    y = torch.randint(0, V, (M,), generator=g, device=DEV)
+    y[0], y[1] = V - 1, 0
+    x = (torch.randn(M, h, generator=g, device=DEV) + 12 * W[y].float()).to(torch.bfloat16)
+    total, loss, lse, dx = lib.linear_cross_entropy(x, W, y, reduction="sum")
+    z = torch.cat([x.double() @ W[a:a + 50_000].double().T for a in range(0, V, 50_000)], 1)
+    s64 = torch.logsumexp(z, 1)
+    # (off as in ce64: 256 + 16 roundings of the running sum of up to |x| |w| in 16-product steps)
+    off = 2 * (h / 16 + 16) * 4 * F32 * float((x[:4].double().abs() @ W[:2000].double().abs().T).max()) + 1e-4
+    within(lse, s64, off, "lse")
+    within(loss, s64 - z.gather(1, y[:, None])[:, 0], off, "loss")
+    p = torch.exp(z - s64[:, None]).scatter_add(1, y[:, None], torch.full((M, 1), -1.0, dtype=torch.float64, device=DEV))
+    d64 = sum(p[:, a:a + 50_000] @ W[a:a + 50_000].double() for a in range(0, V, 50_000))
+    assert float((dx.double() - d64).norm()) <= (2 * BF16 + 2 * off) * float(d64.norm())
+    assert lib.poll_status() == 0
+
+
 def test_same_bits_every_time_and_inside_its_rows(lib):
     x, W, y = problem(200, 128, 3000, hide=0.2)
     a = lib.linear_cross_entropy(x, W, y)

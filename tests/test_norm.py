@@ -148,6 +148,20 @@ def test_outputs_stay_inside_their_rows(lib):
         assert bool((buf[0] == 7).all()) and bool((buf[-1] == 7).all()) and not bool((buf[1:-1] == 7).all())
 
 
+def test_rows_beyond_32_bit_offsets(lib):
+    """2.4G elements: the last rows lie past 2^31 elements and 2^32 bytes."""
+    t, dim = 600_000, 4096
+    x, w = torch.empty(t, dim, dtype=torch.bfloat16, device=DEV), rnd(dim, seed=2)
+    x.normal_(generator=torch.Generator(device=DEV).manual_seed(1))
+    y, _, rstd = lib.rms_norm(x, w, training=True)
+    codes, scale = lib.rms_norm(x, w, format="fp8")[0]
+    last = slice(t - 50, t)
+    check_norm(y[last], x[last], rstd[last], x[last], w)
+    check_norm((codes[last], scale[last]), x[last], rstd[last], x[last], w)
+    dx = lib.rms_norm_backward(y, x, w, rstd, dweight=False)[0]
+    check_norm_grad(dx[last], None, y[last], x[last], w, rstd[last])
+
+
 def test_in_a_graph_and_on_another_stream(lib):
     x, r, w, dy = rows(70, 896), rows(70, 896, 5), rnd(896, seed=2), rnd(70, 896, seed=6)
     s = torch.cuda.Stream()

@@ -123,6 +123,9 @@ def test_cross_entropy_workspace_is_bounded_by_pieces(L):
     assert 0 < b - a <= (3 << 16) * (2 * 1024 + 64) + (1 << 24)
     assert b < (1 << 30) + (1 << 28) + (1 << 18) * (2 * 1024 + 64) + (1 << 24)
     assert q(1 << 18, 0) < (1 << 28) + (1 << 18) * (2 * 1024 + 64) + (1 << 24)
+    # a small vocabulary: the product's f32 sums bound the piece
+    a, b = q(1 << 18, V=1000), q(1 << 20, V=1000)
+    assert 0 < b - a <= (3 << 18) * (2 * 1024 + 64) + (1 << 24) and a < (1 << 31) + (1 << 28) + (1 << 18) * (2 * 1024 + 64)
     assert q(16) < 1 << 28 and q(0) > 0 and q(-1) == 0 and q(16, V=0) == 0
     assert q(16, opts=_b().LoraCe(1.0, -1.0, 0.0, 1, -100)) == 0
 
