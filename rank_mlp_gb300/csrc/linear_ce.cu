@@ -138,9 +138,10 @@ struct CeGatherArgs {
 };
 
 // A warp a token: packs its row and takes the reference from its label's logit, or clears what
-// an unlabelled token has.  ALONE (few tokens): no ce_pack_kernel has run; a block counts the labelled
-// tokens before its own eight by itself.
-constexpr int kCeAloneRows = 2048;
+// an unlabelled token has.  ALONE (fewer tokens than kCeAloneRows): no ce_pack_kernel has run; a block
+// counts the labelled tokens before its own eight by itself.  (A head of 4096 x 896: 64 tokens 36.0 us
+// instead of 38.3, 8192 140 instead of 147, 16384 248 instead of 257, 32768 the same.)
+constexpr int kCeAloneRows = 16384;
 template <bool ALONE>
 __global__ void __launch_bounds__(256) ce_gather_kernel(const __grid_constant__ CeGatherArgs p) {
   pdl_wait();
@@ -444,40 +445,73 @@ struct CeDxArgs {
   bf16* dx;
 };
 // dx rows of a piece: the k-ranges' sums times the row's factor, the label's row of W, and the
-// smoothing's part.  A thread takes eight features.
-__global__ void __launch_bounds__(256) ce_dx_kernel(const __grid_constant__ CeDxArgs p) {
+// smoothing's part.  An item is eight features of a row; a thread has kDxItems on their way.
+constexpr int kDxItems = 2;
+constexpr int kDxAhead = 6;              // and a cut tile's further k-ranges of an item likewise
+constexpr int kDxBlocks = 3;             // resident blocks an SM
+__global__ void __launch_bounds__(256, kDxBlocks) ce_dx_kernel(const __grid_constant__ CeDxArgs p) {
   pdl_wait();
   pdl_launch_dependents();
   const int live = __ldcg(&p.piece->live), whole = __ldcg(&p.piece->whole), splits = __ldcg(&p.piece->splits);
-  const int per = p.h / 8, tiles_m = (live + 255) / 256, cut = tiles_m * p.tiles_n - whole;
-  const long long total = static_cast<long long>(live) * per;
+  const unsigned per = p.h / 8;
+  const int tiles_m = (live + 255) / 256;
+  const long long cut = static_cast<long long>(tiles_m * p.tiles_n - whole) * 65536;
+  const unsigned long long total = static_cast<unsigned long long>(live) * per, step = 256ull * gridDim.x;
   const float flat = p.column == nullptr ? 0.0f : p.scale * p.share / (p.mean ? static_cast<float>(__ldcg(p.r.count)) : 1.0f);
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += 256ll * gridDim.x) {
-    const int row = static_cast<int>(i / per), c = 8 * static_cast<int>(i - static_cast<long long>(row) * per);
-    const int place = ce_tile_place(row >> 8, c >> 8, tiles_m, p.tiles_n, p.band);
-    const int parts = place < whole ? 1 : splits;
-    const float* src = p.slab + static_cast<long long>(place) * 65536 + (row & 255) * 256 + (c & 255);
-    float acc[8];
+  for (unsigned long long i0 = blockIdx.x * 256ull + threadIdx.x; i0 < total; i0 += kDxItems * step) {
+    int row[kDxItems], c[kDxItems], label[kDxItems], token[kDxItems], parts[kDxItems];
+    float rs[kDxItems], coef[kDxItems];
+    const float* src[kDxItems];
+    uint4 v[kDxItems][2], w[kDxItems];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-    for (int s = 0; s < parts; ++s) {
-      const float* from = src + static_cast<long long>(s) * cut * 65536;
-      const uint4 a = ld_global_cg_v4(from), b = ld_global_cg_v4(from + 4);
-      const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += __uint_as_float(v[e]);
+    for (int k = 0; k < kDxItems; ++k) {
+      const unsigned long long i = i0 + k * step < total ? i0 + k * step : i0;
+      const unsigned r = total <= 0xffffffffull ? static_cast<unsigned>(i) / per : static_cast<unsigned>(i / per);
+      row[k] = static_cast<int>(r);
+      c[k] = 8 * static_cast<int>(i - static_cast<unsigned long long>(r) * per);
+      label[k] = __ldcg(p.r.label + row[k]);
+      rs[k] = __ldcg(p.r.rs + row[k]);
+      coef[k] = __ldcg(p.r.coef + row[k]);
+      token[k] = __ldcg(p.r.idx + row[k]);
+      const int place = ce_tile_place(row[k] >> 8, c[k] >> 8, tiles_m, p.tiles_n, p.band);
+      parts[k] = place < whole ? 1 : splits;
+      src[k] = p.slab + static_cast<long long>(place) * 65536 + (row[k] & 255) * 256 + (c[k] & 255);
+      v[k][0] = __ldcg(reinterpret_cast<const uint4*>(src[k]));
+      v[k][1] = __ldcg(reinterpret_cast<const uint4*>(src[k]) + 1);
     }
-    const float rs = __ldcg(p.r.rs + row), coef = __ldcg(p.r.coef + row);
-    float w[8];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(p.W + static_cast<long long>(__ldcg(p.r.label + row)) * p.h + c)), w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = fmaf(rs, acc[e], coef * w[e]);
-    if (p.column != nullptr) {
+    for (int k = 0; k < kDxItems; ++k)
+      w[k] = __ldg(reinterpret_cast<const uint4*>(p.W + static_cast<long long>(label[k]) * p.h + c[k]));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(-flat, __ldcg(p.column + c + e), acc[e]);
+    for (int k = 0; k < kDxItems; ++k) {
+      if (i0 + k * step >= total) break;
+      float acc[8] = {__uint_as_float(v[k][0].x), __uint_as_float(v[k][0].y), __uint_as_float(v[k][0].z), __uint_as_float(v[k][0].w),
+                      __uint_as_float(v[k][1].x), __uint_as_float(v[k][1].y), __uint_as_float(v[k][1].z), __uint_as_float(v[k][1].w)};
+      for (int s = 1; s < parts[k]; s += kDxAhead) {
+        float4 u[kDxAhead][2];                       // past the last: it again, left out
+#pragma unroll
+        for (int j = 0; j < kDxAhead; ++j) {
+          const float4* from = reinterpret_cast<const float4*>(src[k] + min(s + j, parts[k] - 1) * cut);
+          u[j][0] = __ldcg(from);
+          u[j][1] = __ldcg(from + 1);
+        }
+#pragma unroll
+        for (int j = 0; j < kDxAhead; ++j) {
+          if (s + j >= parts[k]) break;
+          acc[0] += u[j][0].x, acc[1] += u[j][0].y, acc[2] += u[j][0].z, acc[3] += u[j][0].w;
+          acc[4] += u[j][1].x, acc[5] += u[j][1].y, acc[6] += u[j][1].z, acc[7] += u[j][1].w;
+        }
+      }
+      float x[8];
+      unpack8(w[k], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(rs[k], acc[e], coef[k] * x[e]);
+      if (p.column != nullptr) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(-flat, __ldcg(p.column + c[k] + e), acc[e]);
+      }
+      *reinterpret_cast<uint4*>(p.dx + static_cast<long long>(token[k]) * p.h + c[k]) = pack8(acc);
     }
-    *reinterpret_cast<uint4*>(p.dx + static_cast<long long>(__ldcg(p.r.idx + row)) * p.h + c) = pack8(acc);
   }
 }
 
@@ -751,8 +785,8 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
     a.share = share;
     a.mean = mean;
     a.dx = gather.dx;
-    const int64_t blocks = ceil_div(rows * (h / 8), 256);
-    LGB_TRY(launch_counted(ce_dx_kernel, dim3(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20))), dim3(256), 0,
+    const int64_t blocks = ceil_div(rows * (h / 8), 256), most = kDxBlocks * num_sms();
+    LGB_TRY(launch_counted(ce_dx_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0,
                            LORA_KIND_LOSS, stream, a));
   }
   return LORA_OK;

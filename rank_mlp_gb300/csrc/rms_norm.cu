@@ -7,7 +7,7 @@
 // row and its use; T grows with the row so that a thread has two to eight loads in flight.
 // Measured: 8192 rows of 4096, residual added, e4m3 out, 235 MB in 38.3 us (6.1 TB/s, 91% of a copy's
 // rate; 256 threads with 2 pieces, 38.5 with 128 and 4, 46.4 with 512 and 1); 131,168 rows of 128 as
-// slices of a packed buffer, 68 MB in 14.8 us (17.8 with one row a group of threads); 16 rows of 896
+// slices of a packed buffer, 68 MB in 14.3 us (17.8 with one row a group of threads); 16 rows of 896
 // 2.1 us in a graph.  The gradient of 4095 rows of 4096 with ds and dweight, 134 MB in 27.2 us (4.9
 // TB/s, 74%; 32.8 with the next row's loads in registers), 3 of them the join of the blocks' dweight.
 #include "serve.cuh"
@@ -460,7 +460,7 @@ extern "C" lora_status_t lora_rms_norm(int64_t M, int dim, const lora_heads_t* x
   p.rstd = rstd;
   return norm_shape(dim, [&](auto t, auto nv) {
     constexpr int T = decltype(t)::value, NV = decltype(nv)::value, K = norm_threads(T) / T;
-    constexpr int R = T <= 32 ? 4 / NV : 1;
+    constexpr int R = NV == 1 ? 2 : 1;               // (four: 14.8 us instead of 14.3, eight 18.7)
     // several rows a group once that leaves the GPU full
     const bool many = R > 1 && p.rows >= static_cast<int64_t>(num_sms()) * 8 * K * R;
     const unsigned grid = static_cast<unsigned>(ceil_div(p.rows, many ? K * R : K));
