@@ -474,6 +474,12 @@ lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, const void* x,
                              const int64_t* labels, const lora_ce_t* opts, float* loss, float* lse, float* total,
                              void* dx, void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* y_m = g[m * g_stride] * x_m, rounded once: rows of bf16 [M x h], factors f32 (g_stride 1: one a row, 0:
+ * one for all).  What autograd does with lora_linear_ce's dx when the loss's own gradient arrives.
+ * y may be x.  h a multiple of 8, x and y 16-byte aligned.  ws: at least 256 bytes. */
+lora_status_t lora_scale_rows(int64_t M, int64_t h, const void* x, const float* g, int g_stride, void* y, void* ws,
+                              size_t ws_bytes, cudaStream_t stream);
+
 /* A tensor of a list: count elements, one after the other, aligned to their own size.  The
  * list itself is host memory and is copied by the call (into the launch, so that a captured
  * call keeps it). */

@@ -4,7 +4,8 @@ call ``loss.backward()``.
 They only route tensors: the forward and backward of each function are one call each
 of ``lora_mlp_forward/backward``, ``lora_qkvo_forward/backward`` (the Q/K/V half),
 ``lora_linear_forward/backward``, ``lora_rotary`` (both ways), ``lora_rms_norm`` and its
-backward, and ``lora_linear_ce``, whose one call gives the loss and the gradient.  The base weights W are frozen ("Model Patches and
+backward, and ``lora_linear_ce``, whose one call gives the loss and the gradient, which
+``lora_scale_rows`` scales by the loss's own.  The base weights W are frozen ("Model Patches and
 Kernels": a frozen weight gets no gradient), so they never receive a gradient; the
 adapters A, B and the input x do.  Inputs may carry leading batch dimensions
 ([..., features]); every tensor is bf16 on the GPU.
@@ -162,7 +163,7 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
     def backward(ctx, g):
         dx, = ctx.saved_tensors
         # one rounding more where g is no power of two
-        dx = (dx * g.reshape(-1, 1)).to(torch.bfloat16) if ctx.none else dx * g
+        dx = binding.scale_rows(dx, g.float().reshape(-1 if ctx.none else ()).contiguous())
         return dx.reshape(ctx.xshape), None, None, None, None, None, None, None
 
 

@@ -131,6 +131,7 @@ _SIGS = {
     "lora_rms_norm_backward": (_INT, [_I64, _INT, _VP, _VP, _VP, _F32, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "lora_linear_ce_workspace_bytes": (_SZ, [_I64, _I64, _I64, _VP, _INT]),
     "lora_linear_ce": (_INT, [_I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "lora_scale_rows": (_INT, [_I64, _I64, _VP, _VP, _INT, _VP, _VP, _SZ, _VP]),
     "lora_grad_norm_workspace_bytes": (_SZ, [_I64]),
     "lora_grad_norm": (_INT, [_I64, _VP, _INT, _VP, _VP, _SZ, _VP]),
     "lora_clip_grads": (_INT, [_I64, _VP, _VP, _INT, _F32, _VP, _VP, _SZ, _VP]),
@@ -912,6 +913,23 @@ def linear_cross_entropy(x, W, labels, *, scale=1.0, softcap=0.0, smoothing=0.0,
     _check(lib.lora_linear_ce(tokens, h, vocab, *args, _at(opts), loss.data_ptr(), lse.data_ptr(), total.data_ptr(),
                               _opt(dx, "dx"), wp, wn, stream), "lora_linear_ce")
     return total, loss, lse, dx
+
+
+def scale_rows(x, g, *, out=None, ws=None):
+    """g * x of bf16 rows [tokens, h], rounded once: g f32, 0-dim (one factor for all) or [tokens].  out may be x."""
+    lib = _LIB or load()
+    if x.dim() != 2:
+        raise ValueError("x must be [tokens, h]")
+    tokens, h = x.shape
+    if out is None:
+        out = torch.empty(tokens, h, dtype=_BF16, device=x.device)
+    elif out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    args = (_dev(x, "x"), _ints(g, torch.float32, () if g.dim() == 0 else (tokens,), "g"), int(g.dim() != 0), _dev(out, "out"))
+    _together(x, g, out, ws)
+    stream, wp, wn = _call(x, 256, ws)
+    _check(lib.lora_scale_rows(tokens, h, *args, wp, wn, stream), "lora_scale_rows")
+    return out
 
 
 class TensorList:

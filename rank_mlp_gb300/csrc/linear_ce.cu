@@ -1,5 +1,5 @@
-// Cross entropy of a frozen head with its gradient (lora_linear_ce); include/lora_gb300.h is
-// the contract, gemm_ce.cuh has the GEMMs and the mathematics they share with this file.
+// Cross entropy of a frozen head with its gradient (lora_linear_ce), and the scaling of that gradient
+// (lora_scale_rows); include/lora_gb300.h is the contract, gemm_ce.cuh has the GEMMs and the mathematics they share with this file.
 //
 // A call packs the labelled rows, then takes them piece by piece:
 //   loss alone     CE_STATS, join of the row's partial results
@@ -515,6 +515,31 @@ __global__ void __launch_bounds__(256, kDxBlocks) ce_dx_kernel(const __grid_cons
   }
 }
 
+struct ScaleArgs {
+  const bf16* x;
+  const float* g;
+  int g_stride;
+  bf16* y;
+  long long M;
+  int h;
+};
+// Rows times their factors, a 16-byte piece a thread and step: bound by memory.
+__global__ void __launch_bounds__(256) scale_rows_kernel(const __grid_constant__ ScaleArgs p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const unsigned per = p.h / 8;
+  const unsigned long long total = static_cast<unsigned long long>(p.M) * per;
+  for (unsigned long long i = blockIdx.x * 256ull + threadIdx.x; i < total; i += 256ull * gridDim.x) {
+    const long long m = p.g_stride == 0 ? 0 : total <= 0xffffffffull ? static_cast<unsigned>(i) / per : static_cast<long long>(i / per);
+    const float g = __ldg(p.g + m);
+    float v[8];
+    unpack8(reinterpret_cast<const uint4*>(p.x)[i], v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= g;
+    reinterpret_cast<uint4*>(p.y)[i] = pack8(v);
+  }
+}
+
 // ---------------------------------------------------------------- host
 
 struct CePlan {
@@ -790,4 +815,24 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
                            LORA_KIND_LOSS, stream, a));
   }
   return LORA_OK;
+}
+
+extern "C" lora_status_t lora_scale_rows(int64_t M, int64_t h, const void* x, const float* g, int g_stride, void* y, void* ws,
+                                         size_t ws_bytes, cudaStream_t stream) {
+  NvtxRange nvtx_range("lora_scale_rows");
+  if (M < 0 || h < 1 || (g_stride != 0 && g_stride != 1) || (M > 0 && (!x || !g || !y))) return LORA_ERR_INVALID_ARG;
+  if (M > kMaxExtent || h > kMaxExtent) return LORA_ERR_UNSUPPORTED;
+  if (h % 8 || !aligned(x, 16) || !aligned(y, 16) || !aligned(g, 4)) return LORA_ERR_ALIGNMENT;
+  LGB_TRY(check_ws(ws, ws_bytes, kWsHeader));
+  if (M == 0) return LORA_OK;
+  ScaleArgs p;
+  p.x = static_cast<const bf16*>(x);
+  p.g = g;
+  p.g_stride = g_stride;
+  p.y = static_cast<bf16*>(y);
+  p.M = M;
+  p.h = static_cast<int>(h);
+  const int64_t blocks = ceil_div(M * (h / 8), 256);          // below 2^59
+  return launch_counted(scale_rows_kernel, dim3(static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30))), dim3(256), 0,
+                        LORA_KIND_LOSS, stream, p);
 }

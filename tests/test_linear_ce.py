@@ -251,6 +251,17 @@ def test_two_streams_at_once(lib):
         assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
 
 
+@pytest.mark.parametrize("M,h", [(0, 64), (1, 8), (7, 72), (300, 896), (5000, 4096)])
+def test_scaled_rows(lib, M, h):
+    x, g = rnd(M, h), rnd(M, seed=1, dtype=torch.float32)
+    for f in (g, g.sum() + 1.5):
+        want = x.double() * (f.double()[:, None] if f.dim() else f.double())
+        within(lib.scale_rows(x, f), want, BF16 * want.abs() + 1e-40)
+    y = x.clone()
+    assert lib.scale_rows(y, g, out=y) is y and torch.equal(y, lib.scale_rows(x, g))
+    assert torch.equal(lib.scale_rows(x, torch.ones((), device=DEV)), x)
+
+
 @pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
 def test_autograd(lib, reduction):
     from rank_mlp_gb300.autograd import lora_linear_cross_entropy

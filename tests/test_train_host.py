@@ -130,6 +130,18 @@ def test_cross_entropy_workspace_is_bounded_by_pieces(L):
     assert q(16, opts=_b().LoraCe(1.0, -1.0, 0.0, 1, -100)) == 0
 
 
+@pytest.mark.usefixtures("nothing_is_launched")
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), INVALID), (dict(h=0), INVALID), (dict(x=None), INVALID), (dict(g=None), INVALID), (dict(y=None), INVALID),
+    (dict(stride=2), INVALID), (dict(stride=-1), INVALID), (dict(M=1 << 31), UNSUPPORTED), (dict(h=1 << 31), UNSUPPORTED),
+    (dict(h=60), ALIGNMENT), (dict(x=ALIGNED + 8), ALIGNMENT), (dict(y=ALIGNED + 2), ALIGNMENT), (dict(g=ALIGNED + 2), ALIGNMENT),
+    (dict(ws=None), INVALID), (dict(ws=ALIGNED + 16), ALIGNMENT), (dict(ws_bytes=255), WORKSPACE),
+])
+def test_scale_rows_refuses(L, kw, code):
+    assert L.lora_scale_rows(kw.get("M", 4), kw.get("h", 64), kw.get("x", ALIGNED), kw.get("g", ALIGNED), kw.get("stride", 1),
+                             kw.get("y", ALIGNED), kw.get("ws", ALIGNED), kw.get("ws_bytes", 256), None) == code
+
+
 def tensors(*specs):
     arr = (_b().LoraTensor * max(1, len(specs)))()
     for i, s in enumerate(specs):
@@ -222,7 +234,7 @@ def calls(monkeypatch):
                 seen.append(name)
             return 0
         return f
-    names = [n for n in b.EXPORTS if any(k in n for k in ("norm", "linear_ce", "clip"))]
+    names = [n for n in b.EXPORTS if any(k in n for k in ("norm", "linear_ce", "clip", "scale_rows"))]
     monkeypatch.setattr(b, "_LIB", types.SimpleNamespace(**{n: entry(n) for n in names}))
     monkeypatch.setattr(b, "_call", lambda t, n, ws: (0, 256, 256))
     monkeypatch.setattr(b, "_current_device", lambda: 0)
@@ -241,6 +253,7 @@ CALLS = {
     "rms_norm_backward": (("x", "w", "s", "rstd", "ds", "dx", "ws"), lambda b, t: b.rms_norm_backward(
         t["x"], t["s"], t["w"], t["rstd"], ds=t["ds"], dx=t["dx"], ws=t["ws"])),
     "linear_ce": (("x", "W", "y", "dx", "ws"), lambda b, t: b.linear_cross_entropy(t["x"], t["W"], t["y"], dx=t["dx"], ws=t["ws"])),
+    "scale_rows": (("x", "rstd", "out", "ws"), lambda b, t: b.scale_rows(t["x"], t["rstd"], out=t["out"], ws=t["ws"])),
     "grad_norm": (("g0", "g1", "ws"), lambda b, t: b.grad_norm([t["g0"], t["g1"]], ws=t["ws"])),
     "clip_grads": (("g0", "g1", "o0", "o1", "ws"), lambda b, t: b.clip_grad_norm(
         [t["g0"], t["g1"]], 1.0, out=[t["o0"], t["o1"]], ws=t["ws"])),
