@@ -602,11 +602,20 @@ static size_t ce_carve(void* ws, int64_t M, int64_t h, const lora_ce_t& o, bool 
   return c.off;
 }
 
-static CeLogit ce_logit_of(const lora_ce_t& o) {
+// The matrix units cut what falls below the last place of their running sum, always toward zero, so
+// that a logit comes out short by a share of itself that grows with the products it sums.  Of dense rows
+// that share is about 1e-9 a feature (measured at h = 256 to 8192 against 64 bits: 0.9 to 1.1 for
+// normal and for heavy-tailed rows, 1.4 to 1.6 for rows of one sign; 0.07 where 19 of 20 features are
+// zero), and the logits are scaled up by it: at h = 4096 the loss is off by 0.8e-6 of itself instead
+// of 2.1e-6, normal rows; f32 products give 0.5e-6.  (Rows mostly of zeros lose by it: 1.5e-6 for 0.15e-6.)
+constexpr float kCeCut = 1.0e-9f;
+
+static CeLogit ce_logit_of(const lora_ce_t& o, int64_t h) {
+  const float up = 1.0f + kCeCut * static_cast<float>(h);
   CeLogit lg;
-  lg.k2 = o.logit_scale * kLog2e;
+  lg.k2 = o.logit_scale * kLog2e * up;
   lg.cap2 = o.softcap * kLog2e;
-  lg.kc = o.softcap > 0.0f ? 2.0f * kLog2e * (o.logit_scale / o.softcap) : 0.0f;
+  lg.kc = o.softcap > 0.0f ? 2.0f * kLog2e * (o.logit_scale / o.softcap) * up : 0.0f;
   return lg;
 }
 
@@ -620,7 +629,7 @@ static lora_status_t check_ce(int64_t M, int64_t h, int64_t vocab, const lora_ce
       !(o->smoothing >= 0.0f && o->smoothing < 1.0f) ||
       (o->reduction != LORA_LOSS_SUM && o->reduction != LORA_LOSS_MEAN))
     return LORA_ERR_INVALID_ARG;
-  const CeLogit lg = ce_logit_of(*o);
+  const CeLogit lg = ce_logit_of(*o, h);
   if (!std::isfinite(lg.k2) || !std::isfinite(lg.cap2) || !std::isfinite(lg.kc)) return LORA_ERR_INVALID_ARG;
   if (st != LORA_OK || M > kMaxExtent || vocab > kCeMaxVocab) return LORA_ERR_UNSUPPORTED;
   return h % 8 ? LORA_ERR_ALIGNMENT : LORA_OK;
@@ -667,7 +676,7 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
   unsigned* status = static_cast<unsigned*>(ws);
   const int tiles_n = static_cast<int>(ceil_div(vocab, 256)), tiles_h = static_cast<int>(ceil_div(h, 256));
   const int kb_h = static_cast<int>(ceil_div(h, kBK)), kb_v = static_cast<int>(ceil_div(vocab, kBK));
-  const CeLogit lg = ce_logit_of(o);
+  const CeLogit lg = ce_logit_of(o, h);
   const float share = o.smoothing / static_cast<float>(vocab);
 
   CeGatherArgs gather;
