@@ -454,8 +454,9 @@ lora_status_t lora_rms_norm_backward(int64_t M, int dim, const lora_heads_t* dy,
  * x is not used.  So has one whose label is outside [0, vocab), which is reported
  * (LORA_ERR_DEVICE_INPUT).  loss, lse f32 [M], or NULL; total f32 [1]; dx bf16 [M x h], or
  * NULL (the loss alone).  dx may not be x.
- * Logits, their exponentials and all sums are f32 (what the matrix units' rounding toward zero takes off
- * a dense row's logits is put back on average).  For dx the exponentials of all but the
+ * Logits, their exponentials and all sums are f32.  Logits are scaled by 1 + 1e-9 h, which makes up on
+ * average for what the matrix units' rounding toward zero takes off dense rows; logits of mostly
+ * zero rows come out too large by about that much.  For dx the exponentials of all but the
  * label's are rounded to bf16 on their way to the product with W, the label's stays f32.
  * Tokens are taken in pieces of up to 1 GiB of such exponentials and as much of f32 sums, which live
  * in the workspace.  h a multiple of 8; vocab at most 2^24; x, W, dx 16-byte aligned.  logit_scale finite, not 0;

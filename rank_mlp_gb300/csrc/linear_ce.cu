@@ -603,11 +603,18 @@ static size_t ce_carve(void* ws, int64_t M, int64_t h, const lora_ce_t& o, bool 
 }
 
 // The matrix units cut what falls below the last place of their running sum, always toward zero, so
-// that a logit comes out short by a share of itself that grows with the products it sums.  Of dense rows
-// that share is about 1e-9 a feature (measured at h = 256 to 8192 against 64 bits: 0.9 to 1.1 for
-// normal and for heavy-tailed rows, 1.4 to 1.6 for rows of one sign; 0.07 where 19 of 20 features are
-// zero), and the logits are scaled up by it: at h = 4096 the loss is off by 0.8e-6 of itself instead
-// of 2.1e-6, normal rows; f32 products give 0.5e-6.  (Rows mostly of zeros lose by it: 1.5e-6 for 0.15e-6.)
+// that a logit comes out short by a share of itself that grows with the products it sums.  The share
+// depends on the rows, so one constant makes up for it on average only; it is fitted, not derived.
+// Measured against 64 bits at h = 896 and 4096, in 1e-9 a feature, and what the scaling does to the
+// loss's relative error at h = 4096 (1e-6, before -> after; f32 products):
+//   normal               0.86, 0.87    1.85 -> 0.43   (0.15)
+//   heavy-tailed         1.11, 0.95    4.74 -> 2.48   (1.07)
+//   pulled to the label  0.97, 1.01    2.12 -> 0.81   (0.54)   at h = 256 to 8192 1.00 to 1.02: the fit
+//   sorted, one sign     1.40, 1.63    10.1 -> 8.4    (3.5)
+//   all of one sign      1.47, 2.86    0.49 -> 0.46   (1.25)   too little by far: lse 6.7 -> 4.4
+//   19 of 20 zero        0.07, 0.07    0.15 -> 1.47   (0.05)   too much: ten times worse
+// Rows that reach a head are dense, so it is done; a row whose products are summed exactly gets
+// logits that are 1e-9 h too large.
 constexpr float kCeCut = 1.0e-9f;
 
 static CeLogit ce_logit_of(const lora_ce_t& o, int64_t h) {
