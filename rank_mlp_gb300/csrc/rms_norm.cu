@@ -10,6 +10,8 @@
 // slices of a packed buffer, 68 MB in 14.3 us (17.8 with one row a group of threads); 16 rows of 896
 // 2.1 us in a graph.  The gradient of 4095 rows of 4096 with ds and dweight, 134 MB in 27.2 us (4.9
 // TB/s, 74%; 32.8 with the next row's loads in registers), 3 of them the join of the blocks' dweight.
+// Narrow rows' gradient with dweight, L2 flushed between replays: 131,168 rows of 128 36.0 us, of 256
+// 52.4 (42.1 and 62.6 while the block's join had shared memory of its own and seven blocks an SM fitted).
 #include "serve.cuh"
 
 namespace lgb {
@@ -300,9 +302,13 @@ __global__ void __launch_bounds__(norm_threads(T), norm_grad_blocks_sm(T)) norm_
   }
   if constexpr (DW) {
     // the block's row groups, summed in their order
-    __shared__ float join[kRows > 1 ? kRows : 1][kRows > 1 ? 8 * T * NV : 1];
     float* out = p.part + static_cast<long long>(blockIdx.x) * p.dim;
     if constexpr (kRows > 1) {
+      // (in the ring, whose copies have all been waited for: 4 KB more would cost the SM's eighth block)
+      static_assert(kRows * 8 * T * NV * 4 <= norm_grad_smem(T, NV));
+      auto* join = reinterpret_cast<float (*)[8 * T * NV]>(ring);
+      copy_async_wait<0>();
+      __syncthreads();
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
