@@ -14,6 +14,10 @@
 // out of e and S: it joins in f32 from the label's logit, where 1 - p_y keeps its precision
 // however near p_y is to 1.
 //
+// Rounding the weights to bf16 moves their sum, and what a head's rows have in common is multiplied by
+// that sum: it would no longer be what the label's term takes off.  So the weights' sums before and
+// after the rounding are kept beside S, and ce_balance makes the second one the first.
+//
 // Rows are the labelled tokens, packed; their number is on the device, so a launch covers the
 // most rows there can be and its units follow from the number it finds.
 //
@@ -69,7 +73,9 @@ struct CeGemmParams {
   const int* label;
   const float* ref2;
   float2* part;            // CE_STATS: [tiles_n * kCeSlots][ldp] (maximum, sum), both without the label
-  float* psum;             // CE_GRAD: the sums alone
+  float* psum;             // CE_GRAD: the sums alone,
+  float* wsum;             // those of the weights as they are stored in e,
+  float* tsum;             // and before their rounding (with a cap; without, they are psum)
   float* zsum;             // [tiles_n * kCeSlots][ldp] sums of z2, label included, or NULL
   float* zlab;             // the label's z2
   long long ldp;
@@ -78,6 +84,11 @@ struct CeGemmParams {
   float minus;             // CE_GRAD: taken off each exponential before the tanh's slope
   // CE_PART
   float* slab;             // [units][256][256]
+  int balance;             // rows' factors follow the weights' sums here: 0 no, 1 yes, 2 if the piece's `redo` is set
+  int slots;
+  float limit;
+  float* rs;
+  float* coef;
 };
 
 // The product with the head has few tiles and a long K.  Whole waves of tiles on the CTA pairs are
@@ -126,6 +137,17 @@ __device__ __forceinline__ float ce_logit(float v, const CeLogit& lg, float& slo
     const float q = __fdividef(2.0f, 1.0f + exp2_approx(v * lg.kc));
     slope = q * (2.0f - q);
     return fmaf(-lg.cap2, q, lg.cap2);
+  }
+}
+
+// Factors of a row (rs: of its weights' product with W, coef: of the label's row of W) for weights that
+// summed to t and, rounded, to w.  All weights are multiplied by t / w; where their signs differ and
+// they cancel (t not above `limit`; the smoothing's part, with a cap) the difference goes to the label instead.
+__device__ __forceinline__ void ce_balance(float t, float w, float limit, float& rs, float& coef) {
+  if (t > limit && w > 0.0f) {
+    rs *= t / w;
+  } else {
+    coef = fmaf(rs, t - w, coef);
   }
 }
 
@@ -210,10 +232,11 @@ __device__ __forceinline__ int ce_tile_place(int tm, int tn, int tiles_m, int ti
 }
 
 // 32 logits of a row, columns [col0, col0 + 32): into the row's running (top, sum, zs), the label's
-// own into zlab, and for CE_GRAD their exponentials into e.  Whole warps call it.
+// own into zlab, and for CE_GRAD their weights into e and the weights' sums, rounded and not, into ws and
+// (with a cap) ts.  Whole warps call it.
 template <int KIND, bool CAP>
 __device__ __forceinline__ void ce_chunk(const CeGemmParams& p, const uint32_t (&v)[32], int col0, int row, bool ok, int label,
-                                         float ref2, float& top, float& sum, float& zs) {
+                                         float ref2, float& top, float& sum, float& zs, float& ws, float& ts) {
   if (col0 >= p.vocab) return;                   // wholly past the vocabulary
   const int at = label - col0;                   // the label's place in the chunk
   const int width = p.vocab - col0;              // columns below the vocabulary's size
@@ -252,7 +275,7 @@ __device__ __forceinline__ void ce_chunk(const CeGemmParams& p, const uint32_t (
       sum += s0 + s1;
     } else {
       uint32_t w[16];
-      float s0 = 0.0f, s1 = 0.0f;
+      float s0 = 0.0f, s1 = 0.0f, r0 = 0.0f, r1 = 0.0f, t0 = 0.0f, t1 = 0.0f;
 #pragma unroll
       for (int j = 0; j < 32; j += 2) {
         float e[2];
@@ -271,8 +294,13 @@ __device__ __forceinline__ void ce_chunk(const CeGemmParams& p, const uint32_t (
           if (CAP && !PLAIN && (j + h == at || j + h >= width)) e[h] = 0.0f;
         }
         w[j / 2] = pack_bf16x2(e[0], e[1]);
+        r0 += __uint_as_float(w[j / 2] << 16);
+        r1 += __uint_as_float(w[j / 2] & 0xFFFF0000u);
+        if (CAP) t0 += e[0], t1 += e[1];
       }
       sum += s0 + s1;
+      ws += r0 + r1;
+      if (CAP) ts += t0 + t1;
       if (ok) {
         // (the same stores into rows of the whole vocabulary: 635 us for 608)
         __nv_bfloat16* dst = p.e + (static_cast<long long>(row >> 7) * p.blocks + (col0 >> 6)) * 8192 + (row & 127) * 64 + (col0 & 63);
@@ -298,13 +326,13 @@ __device__ __forceinline__ void ce_rows(const CeGemmParams& p, const CeUnit& U, 
   tmem_ld32(from, va);
   const int label = ok ? __ldg(p.label + row) : -1;
   const float ref2 = KIND == CE_GRAD && ok ? __ldcg(p.ref2 + row) : 0.0f;
-  float top = -INFINITY, sum = 0.0f, zs = 0.0f;
+  float top = -INFINITY, sum = 0.0f, zs = 0.0f, ws = 0.0f, ts = 0.0f;
 #pragma unroll 1
   for (int c = 0; c < kSpan; c += 64) {
     tmem_ld_wait_for(va);
     __syncwarp();
     tmem_ld32(from + c + 32, vb);
-    ce_chunk<KIND, CAP>(p, va, first + c, row, ok, label, ref2, top, sum, zs);
+    ce_chunk<KIND, CAP>(p, va, first + c, row, ok, label, ref2, top, sum, zs, ws, ts);
     tmem_ld_wait_for(vb);
     __syncwarp();
     if (c + 64 < kSpan) {
@@ -312,11 +340,17 @@ __device__ __forceinline__ void ce_rows(const CeGemmParams& p, const CeUnit& U, 
     } else {
       release();
     }
-    ce_chunk<KIND, CAP>(p, vb, first + c + 32, row, ok, label, ref2, top, sum, zs);
+    ce_chunk<KIND, CAP>(p, vb, first + c + 32, row, ok, label, ref2, top, sum, zs, ws, ts);
   }
   if (ok) {
     const long long at = (static_cast<long long>(U.tn) * kCeSlots + part) * p.ldp + row;
-    if (KIND == CE_STATS) p.part[at] = make_float2(top, sum); else p.psum[at] = sum;
+    if (KIND == CE_STATS) {
+      p.part[at] = make_float2(top, sum);
+    } else {
+      p.psum[at] = sum;
+      p.wsum[at] = ws;
+      if (CAP) p.tsum[at] = ts;
+    }
     if (p.zsum != nullptr) p.zsum[at] = zs;
   }
 }
@@ -504,6 +538,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
     const int part = (warp - 2) >> 2;
     const int row_in_tile = static_cast<int>(rank) * kBM + q * 32 + lane;
     const uint32_t tempty_even[2] = {mapa_shared(tempty_bar(0), 0), mapa_shared(tempty_bar(1), 0)};
+    if constexpr (KIND == CE_PART) {
+      // the first tile is some time off: a warp a row, where the rows' factors were made before their weights
+      if (p.balance == 1 || (p.balance == 2 && __ldcg(&p.piece->redo) != 0)) {
+        const int step = static_cast<int>(gridDim.x) * kCeWarps;
+        for (int row = static_cast<int>(blockIdx.x) * kCeWarps + warp - 2; row < live; row += step) {
+          float t = 0.0f, w = 0.0f;
+          for (int k = lane; k < p.slots; k += 32) {
+            t += __ldcg(p.tsum + k * p.ldp + row);
+            w += __ldcg(p.wsum + k * p.ldp + row);
+          }
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) {
+            t += __shfl_xor_sync(0xffffffffu, t, d);
+            w += __shfl_xor_sync(0xffffffffu, w, d);
+          }
+          if (lane == 0) {
+            float rs = __ldcg(p.rs + row), coef = __ldcg(p.coef + row);
+            ce_balance(t, w, p.limit, rs, coef);
+            p.rs[row] = rs;
+            p.coef[row] = coef;
+          }
+        }
+        __syncwarp();
+      }
+    }
     int acc = 0;
     uint32_t acc_phase = 0;
     CeIter it(p, live, whole, splits, pair, npairs);

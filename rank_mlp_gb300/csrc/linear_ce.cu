@@ -6,7 +6,8 @@
 //   with dx        reference z_y + 40 for each row (a dot product), CE_GRAD, join, CE_PART over the
 //                  exponentials, join of the k-ranges with the label's row of W
 //   capped and smoothed at once: CE_STATS, join, CE_GRAD with lse as its reference, CE_PART
-//                  (the smoothing's part of the gradient then depends on each logit's slope)
+//                  (the smoothing's part of the gradient then depends on each logit's slope); the
+//                  weights' sums, which come after the join, are joined by CE_PART's epilogue warps
 // A row's largest logit is at least its label's.  So the reference, 40 above the label's logit,
 // leaves the largest exponential between e^-40 and, where the largest logit stands less than 100
 // above the label's, e^60: it, the sums and the product stay inside the range of f32 and bf16
@@ -240,6 +241,8 @@ struct CeJoinArgs {
   CeRows r;                // at the piece's first row (count, joined: the call's)
   const float2* part;      // CE_JOIN_LOSS, CE_JOIN_EXACT
   const float* psum;       // CE_JOIN_GRAD
+  const float* wsum;
+  const float* tsum;       // (psum itself without a cap)
   const float* zsum;
   long long ldp;
   int slots;
@@ -261,9 +264,11 @@ constexpr int kJoinWarps = 32;
 template <int MODE>
 __device__ __forceinline__ void ce_join_rows(const CeJoinArgs& p, int live) {
   __shared__ float tops[kJoinWarps][33], sums[kJoinWarps][33], zs[kJoinWarps][33];
+  __shared__ float weights[MODE == CE_JOIN_GRAD ? 2 : 1][MODE == CE_JOIN_GRAD ? kJoinWarps : 1][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr bool kRelative = MODE != CE_JOIN_GRAD;   // sums relative to their own maxima
-  float top = -INFINITY, sum = 0.0f, z = 0.0f;
+  float top = -INFINITY, sum = 0.0f, z = 0.0f, t = 0.0f, w = 0.0f;
+  const bool own = MODE == CE_JOIN_GRAD && p.tsum != p.psum;       // sums of the weights that are not those of the loss
   auto add = [&](float t, float s) {
     if (t == -INFINITY && s == 0.0f) return;         // no column but the label's
     const float most = fmaxf(top, t);
@@ -279,13 +284,19 @@ __device__ __forceinline__ void ce_join_rows(const CeJoinArgs& p, int live) {
         add(o.x, o.y);
       } else {
         sum += __ldcg(p.psum + k * p.ldp + row);
+        w += __ldcg(p.wsum + k * p.ldp + row);
       }
       if (p.zsum != nullptr) z += __ldcg(p.zsum + k * p.ldp + row);
+    }
+    if (own) {
+#pragma unroll 8
+      for (int k = warp; k < p.slots; k += kJoinWarps) t += __ldcg(p.tsum + k * p.ldp + row);
     }
   }
   tops[warp][lane] = top;
   sums[warp][lane] = sum;
   zs[warp][lane] = z;
+  if constexpr (MODE == CE_JOIN_GRAD) weights[0][warp][lane] = w, weights[1][warp][lane] = t;
   const int row = blockIdx.x * 32 + warp;
   float zl = 0.0f, ref2 = 0.0f;                      // (on their way across the barrier)
   int token = 0, count = 1;
@@ -300,17 +311,20 @@ __device__ __forceinline__ void ce_join_rows(const CeJoinArgs& p, int live) {
   top = tops[lane][warp];
   sum = sums[lane][warp];
   z = zs[lane][warp];
+  if constexpr (MODE == CE_JOIN_GRAD) w = weights[0][lane][warp], t = weights[1][lane][warp];
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
     if constexpr (kRelative) {
       // (both lanes of a pair take the same order: the same bits)
-      const float t = __shfl_xor_sync(0xffffffffu, top, d), o = __shfl_xor_sync(0xffffffffu, sum, d), most = fmaxf(top, t);
+      const float at = __shfl_xor_sync(0xffffffffu, top, d), o = __shfl_xor_sync(0xffffffffu, sum, d), most = fmaxf(top, at);
       const float mine = sum == 0.0f && top == -INFINITY ? 0.0f : sum * exp2f(top - most);
-      const float theirs = o == 0.0f && t == -INFINITY ? 0.0f : o * exp2f(t - most);
+      const float theirs = o == 0.0f && at == -INFINITY ? 0.0f : o * exp2f(at - most);
       sum = mine + theirs;
       top = most;
     } else {
       sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      w += __shfl_xor_sync(0xffffffffu, w, d);
+      t += __shfl_xor_sync(0xffffffffu, t, d);
     }
     z += __shfl_xor_sync(0xffffffffu, z, d);
   }
@@ -337,8 +351,10 @@ __device__ __forceinline__ void ce_join_rows(const CeJoinArgs& p, int live) {
     p.r.rs[row] = g;
     p.r.coef[row] = g * slope * (away + eps - p.minus);
   } else {
-    p.r.rs[row] = g / (sum + exp2f(zl - ref2));
-    p.r.coef[row] = g * slope * (away + eps);
+    float rs = g / (sum + exp2f(zl - ref2)), coef = g * slope * (away + eps);
+    ce_balance(own ? t : sum, w, 0.0f, rs, coef);
+    p.r.rs[row] = rs;
+    p.r.coef[row] = coef;
   }
 }
 
@@ -571,6 +587,8 @@ struct CeSpace {
   bf16* packed;
   float2* part;
   float* psum;
+  float* wsum;
+  float* tsum;
   float* zsum;
   float* column_part;
   float* column;
@@ -594,6 +612,8 @@ static size_t ce_carve(void* ws, int64_t M, int64_t h, const lora_ce_t& o, bool 
   s.packed = c.take_n<bf16>(M * h);
   s.part = c.take_n<float2>(P.slots * P.rows);
   s.psum = reinterpret_cast<float*>(s.part);       // (never both at a time)
+  s.wsum = s.psum + P.slots * P.rows;
+  s.tsum = want_dx && o.softcap > 0.0f ? c.take_n<float>(P.slots * P.rows) : s.psum;
   s.zsum = o.smoothing > 0.0f ? c.take_n<float>(P.slots * P.rows) : nullptr;
   s.column_part = P.columns ? c.take_n<float>(kCeColumnBlocks * h) : nullptr;
   s.column = P.columns ? c.take_n<float>(h) : nullptr;
@@ -752,6 +772,8 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
     g.ref2 = r.ref2;
     g.part = s.part;
     g.psum = s.psum;
+    g.wsum = s.wsum;
+    g.tsum = s.tsum;
     g.zlab = r.zlab;
     g.ldp = P.rows;
     g.e = s.e;
@@ -762,6 +784,8 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
     j.r = r;
     j.part = s.part;
     j.psum = s.psum;
+    j.wsum = s.wsum;
+    j.tsum = s.tsum;
     j.zsum = s.zsum;
     j.ldp = P.rows;
     j.slots = static_cast<int>(P.slots);
@@ -812,6 +836,15 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
     d.band = raster_band();
     d.status = status;
     d.slab = s.slab;
+    d.balance = P.exact ? 1 : 2;
+    d.tsum = s.tsum;
+    d.wsum = s.wsum;
+    d.ldp = P.rows;
+    d.slots = static_cast<int>(P.slots);
+    // weights of unlike signs: the negative ones come to the smoothing at most
+    d.limit = P.exact ? 2.0f * o.smoothing : 0.0f;
+    d.rs = r.rs;
+    d.coef = r.coef;
     LGB_TRY(ce_gemm(CE_PART, d, stream));
     CeDxArgs a;
     a.piece = s.piece + k;

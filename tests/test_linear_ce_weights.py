@@ -1,0 +1,104 @@
+"""The gradient's weights of a head whose rows share a direction or are alike: what bf16 takes off or adds to
+each weight may not add up along what the rows have in common.
+
+With weights w_v (1 + d_v), |d_v| <= 2^-8, whose sum is made that of the w_v again, the error of a row of dx is
+sum_v (d_v - D) w_v W_v, D = sum d_v w_v / sum w_v.  Its terms' factors sum to zero, so W_v may be replaced by
+W_v - U with the same U throughout: the bound below has the rows' distances from their weighted mean, not
+their lengths."""
+
+import pytest
+import torch
+
+from train_ref import BF16, DEV, F32
+
+pytestmark = pytest.mark.gpu
+
+M, H, V = 200, 256, 4096
+
+
+def problem(head, gap, seed=0):
+    """A competing word beside the label: `gap` above it for the first row, up to 2 more for the last."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    y = torch.randperm(V, generator=g, device=DEV)[:2 * M]
+    y, other = y[:M], y[M:]
+    W = r(V, H) * H ** -0.5
+    if "near" in head:
+        W[other] = W[y] + 0.1 * r(M, H) * H ** -0.5
+    own = W.clone()
+    if "common" in head:
+        W = W + 5.0 * r(1, H) * H ** -0.5
+    W = W.to(torch.bfloat16)
+    # two equations for x: 14 on the label's row, the gap along the rows' difference
+    d = own[other] - own[y]
+    x = 0.5 * r(M, H)
+    want = torch.stack([torch.full((M,), 14.0, device=DEV), gap + torch.linspace(-1, 2, M, device=DEV)], 1)
+    A = torch.stack([own[y], d], 1)                                          # [M, 2, H]
+    rest = want - torch.einsum("mkh,mh->mk", A, x)
+    x = x + torch.einsum("mkh,mk->mh", A, torch.linalg.solve(A @ A.transpose(1, 2), rest))
+    return x.to(torch.bfloat16), W, y
+
+
+def rows64(x, W, y, scale=1.0, softcap=0.0, smoothing=0.0):
+    """(dx, bound of each row's error)."""
+    w64 = W.double()
+    v = scale * (x.double() @ w64.T)
+    z = softcap * torch.tanh(v / softcap) if softcap else v
+    p = torch.softmax(z, 1)
+    slope = 1 - (z / softcap) ** 2 if softcap else torch.ones_like(z)
+    flat = torch.full_like(z, smoothing / V)
+    dz = (p - flat) * slope
+    at = y[:, None]
+    dz.scatter_add_(1, at, -(1 - smoothing) * slope.gather(1, at))
+    dx = scale * (dz @ w64)
+    # what is rounded: all but the label's, with the smoothing's part where there is a cap too
+    signed = bool(softcap and smoothing)
+    w = ((p - flat) * slope if signed else p * slope).scatter(1, at, 0.0)
+    mean = (w @ w64) / w.sum(1, keepdim=True)
+    far = lambda u: (w64.square().sum(1) - 2 * u @ w64.T + u.square().sum(1, keepdim=True)).clamp(min=0).sqrt()  # noqa: E731
+    away = far(mean)
+    if signed:                                       # (the label's row takes the difference where weights cancel)
+        away = torch.maximum(away, far(w64[y]))
+    spread = (w.abs() * away).sum(1)
+    # logits move by 2e-6 of the largest at this h and 2^-22 (their exponentials); with a cap by its last
+    # places; the matrix units sum V / 16 steps, up to 2^-23 of the sum each
+    worst = 4e-6 * v.abs().amax(1) + 4 * F32 + 32 * F32 * softcap
+    size = (w.abs() * w64.norm(dim=1)).sum(1)
+    steps = (V / 16 + 64) * 2 * F32
+    d = dx.norm(dim=1)
+    slack = abs(scale) * ((3 if signed else 2) * BF16 + 2 * worst) * spread + (BF16 + 4 * worst) * d
+    slack = slack + abs(scale) * (steps + 16 * F32) * size
+    if smoothing:                                    # the flat part: f32 sums of V rows, and slopes that move
+        slack = slack + abs(scale) * smoothing * ((V + 400) * F32 + 4 * worst) * w64.norm(dim=1).mean()
+    if softcap:
+        slack = slack + 4 * abs(scale) * worst / softcap * (size + w64[y].norm(dim=1) * (1 - p.gather(1, at)[:, 0]))
+    return dx, slack
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(smoothing=0.1), dict(softcap=30.0), dict(softcap=30.0, smoothing=0.1), dict(scale=0.5)],
+                         ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()) or "plain")
+@pytest.mark.parametrize("gap", [0.0, 4.0])
+@pytest.mark.parametrize("head", ["independent", "common", "near", "near common"])
+def test_rows_that_share_a_direction(lib, head, gap, kw):
+    x, W, y = problem(head, gap)
+    d64, slack = rows64(x, W, y, **kw)
+    dx = lib.linear_cross_entropy(x, W, y, reduction="sum", **kw)[3]
+    err = (dx.double() - d64).norm(dim=1)
+    over = err / slack
+    assert bool((over <= 1).all()), f"{int((over > 1).sum())} rows, {float(over.max()):.1f} times what is allowed"
+    assert lib.poll_status() == 0
+
+
+@pytest.mark.parametrize("head", ["common", "near common"])
+def test_a_piece_that_is_taken_again(lib, head):
+    """One label far below its row's largest logit: the whole piece's weights come from the second try."""
+    x, W, y = problem(head, 2.0)
+    far = torch.randn(H, generator=torch.Generator(device=DEV).manual_seed(5), device=DEV)
+    x[17] = (400.0 * torch.sign(far)).to(torch.bfloat16)
+    y[17] = int((x[17].double() @ W.double().T).argmin())
+    z = x.double() @ W.double().T
+    assert float(z[17].max() - z[17, y[17]]) > 110
+    d64, slack = rows64(x, W, y)
+    dx = lib.linear_cross_entropy(x, W, y, reduction="sum")[3]
+    assert bool(((dx.double() - d64).norm(dim=1) <= slack).all())
+    assert lib.poll_status() == 0
