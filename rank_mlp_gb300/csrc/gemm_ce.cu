@@ -4,9 +4,9 @@
 
 namespace lgb {
 
-template <int KIND>
+template <int KIND, bool LONG>
 static cudaError_t launch_kind(const CeGemmParams& p, int grid, cudaStream_t st) {
-  auto* k = ce_gemm_kernel<KIND>;
+  auto* k = ce_gemm_kernel<KIND, LONG>;
   constexpr int smem = PairCfg<kCeStages, kCeWarps>::kSmemBytes;
   static std::atomic<unsigned long long> configured{0};
   const cudaError_t e = ensure_smem_limit(k, smem, configured);
@@ -15,10 +15,11 @@ static cudaError_t launch_kind(const CeGemmParams& p, int grid, cudaStream_t st)
 }
 
 cudaError_t launch_ce_gemm(int kind, const CeGemmParams& p, int grid, cudaStream_t st) {
+  const bool parts = p.kb_total > kCeRangeKb;
   switch (kind) {
-    case CE_STATS: return launch_kind<CE_STATS>(p, grid, st);
-    case CE_GRAD: return launch_kind<CE_GRAD>(p, grid, st);
-    case CE_PART: return launch_kind<CE_PART>(p, grid, st);
+    case CE_STATS: return parts ? launch_kind<CE_STATS, true>(p, grid, st) : launch_kind<CE_STATS, false>(p, grid, st);
+    case CE_GRAD: return parts ? launch_kind<CE_GRAD, true>(p, grid, st) : launch_kind<CE_GRAD, false>(p, grid, st);
+    case CE_PART: return launch_kind<CE_PART, false>(p, grid, st);
     default: return cudaErrorInvalidValue;
   }
 }

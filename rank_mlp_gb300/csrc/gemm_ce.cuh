@@ -38,6 +38,18 @@ constexpr int kCeStages = 6;
 // (Four took as long at 14 and at 64 k-blocks a tile: 1275 and 5282 us for 1271 and 5306 with eight.)
 constexpr int kCeWarps = 8;
 constexpr int kCeSlots = kCeWarps / 4;
+// k-blocks that a logit is summed over in tensor memory at most.  The matrix units cut what falls below the
+// last place of their running sum, always toward zero, so that a logit comes out short by a share of
+// itself that grows with the products it sums.  Longer rows are taken in parts that are joined in f32
+// in the epilogue's registers.  The loss's error at h = 4096 over 5003 words, in 1e-6 of itself, without parts, with
+// parts of 16 (h = 896; f32 products at 4096):
+//   normal         1.85   0.40   (0.36, 0.15)
+//   heavy-tailed   4.74   1.38   (1.18, 1.07)
+//   label-pulled   2.12   0.48   (0.46, 0.54)
+//   lse, one sign  6.7    0.87   (0.73)
+// 2048 tokens x 4096 against 50,257 words, the loss alone: 490 us without parts, 496 with parts of 32
+// k-blocks, 508 with 16, 535 with 8; 4096 capped rows with dx the same within 1% but for parts of 8 (2% more).
+constexpr int kCeRangeKb = 16;
 constexpr int kCeMaxSplits = 32;
 constexpr int kCeTailUnits = 304;        // units of a launch at most that are parts of tiles
 constexpr float kLog2e = 1.4426950408889634f;
@@ -62,6 +74,7 @@ struct CeGemmParams {
   const CePiece* piece;
   int when_redo;           // 1: only if the piece's `redo` is set
   int kb_total, kvalid;    // 64-wide k-blocks, valid K
+  int kb_range;            // CE_STATS, CE_GRAD: k-blocks of a part of the sums
   int tiles_n, band;
   int narrow;              // CE_PART: 1 if the last n-tile is 128 columns wide
   unsigned* status;
@@ -312,37 +325,25 @@ __device__ __forceinline__ void ce_chunk(const CeGemmParams& p, const uint32_t (
   if (plain) chunk(ActTag<1>{}); else chunk(ActTag<0>{});
 }
 
-// The epilogue of one tile row: the warp's share `part` of the tile's columns, 32 at a time, each read
-// from tensor memory while those before are worked on; release() once all have been read.
-// Warp-collective; `ok`: the row is one of the piece's.
-template <int KIND, bool CAP, typename F>
-__device__ __forceinline__ void ce_rows(const CeGemmParams& p, const CeUnit& U, uint32_t tacc, int row, bool ok, int part,
-                                        F&& release) {
-  constexpr int BN = 256, kSpan = BN / kCeSlots;
-  const uint32_t from = tacc + part * kSpan;
-  const int first = U.tn * BN + part * kSpan;
-  uint32_t va[32], vb[32];
-  __syncwarp();
-  tmem_ld32(from, va);
-  const int label = ok ? __ldg(p.label + row) : -1;
-  const float ref2 = KIND == CE_GRAD && ok ? __ldcg(p.ref2 + row) : 0.0f;
+// What the epilogue of one tile row has on its way: the row's running results over the warp's share `part`
+// of the tile's columns.
+template <int KIND, bool CAP>
+struct CeRow {
+  static constexpr int kSpan = 256 / kCeSlots;
+  int row, label, first;
+  bool ok;                 // the row is one of the piece's
+  float ref2;
   float top = -INFINITY, sum = 0.0f, zs = 0.0f, ws = 0.0f, ts = 0.0f;
-#pragma unroll 1
-  for (int c = 0; c < kSpan; c += 64) {
-    tmem_ld_wait_for(va);
-    __syncwarp();
-    tmem_ld32(from + c + 32, vb);
-    ce_chunk<KIND, CAP>(p, va, first + c, row, ok, label, ref2, top, sum, zs, ws, ts);
-    tmem_ld_wait_for(vb);
-    __syncwarp();
-    if (c + 64 < kSpan) {
-      tmem_ld32(from + c + 64, va);
-    } else {
-      release();
-    }
-    ce_chunk<KIND, CAP>(p, vb, first + c + 32, row, ok, label, ref2, top, sum, zs, ws, ts);
+  __device__ __forceinline__ CeRow(const CeGemmParams& p, const CeUnit& U, int row_, bool ok_, int part) : row(row_), ok(ok_) {
+    first = U.tn * 256 + part * kSpan;
+    label = ok ? __ldg(p.label + row) : -1;
+    ref2 = KIND == CE_GRAD && ok ? __ldcg(p.ref2 + row) : 0.0f;
   }
-  if (ok) {
+  __device__ __forceinline__ void chunk(const CeGemmParams& p, const uint32_t (&v)[32], int c) {
+    ce_chunk<KIND, CAP>(p, v, first + c, row, ok, label, ref2, top, sum, zs, ws, ts);
+  }
+  __device__ __forceinline__ void store(const CeGemmParams& p, const CeUnit& U, int part) const {
+    if (!ok) return;
     const long long at = (static_cast<long long>(U.tn) * kCeSlots + part) * p.ldp + row;
     if (KIND == CE_STATS) {
       p.part[at] = make_float2(top, sum);
@@ -353,9 +354,50 @@ __device__ __forceinline__ void ce_rows(const CeGemmParams& p, const CeUnit& U, 
     }
     if (p.zsum != nullptr) p.zsum[at] = zs;
   }
+};
+
+// The epilogue of one tile row, 32 columns at a time, each read from tensor memory while those before are
+// worked on; release() once all have been read.  Warp-collective.
+template <int KIND, bool CAP, typename F>
+__device__ __forceinline__ void ce_rows(const CeGemmParams& p, const CeUnit& U, uint32_t tacc, int row, bool ok, int part,
+                                        F&& release) {
+  constexpr int kSpan = CeRow<KIND, CAP>::kSpan;
+  const uint32_t from = tacc + part * kSpan;
+  uint32_t va[32], vb[32];
+  __syncwarp();
+  tmem_ld32(from, va);
+  CeRow<KIND, CAP> r(p, U, row, ok, part);
+#pragma unroll 1
+  for (int c = 0; c < kSpan; c += 64) {
+    tmem_ld_wait_for(va);
+    __syncwarp();
+    tmem_ld32(from + c + 32, vb);
+    r.chunk(p, va, c);
+    tmem_ld_wait_for(vb);
+    __syncwarp();
+    if (c + 64 < kSpan) {
+      tmem_ld32(from + c + 64, va);
+    } else {
+      release();
+    }
+    r.chunk(p, vb, c + 32);
+  }
+  r.store(p, U, part);
 }
 
-template <int KIND>
+// The same for logits summed in parts, which have been joined in registers.
+template <int KIND, bool CAP>
+__device__ __forceinline__ void ce_rows_joined(const CeGemmParams& p, const CeUnit& U,
+                                               const uint32_t (&z)[CeRow<KIND, CAP>::kSpan / 32][32], int row, bool ok, int part) {
+  CeRow<KIND, CAP> r(p, U, row, ok, part);
+#pragma unroll
+  for (int c = 0; c < CeRow<KIND, CAP>::kSpan / 32; ++c) r.chunk(p, z[c], 32 * c);
+  r.store(p, U, part);
+}
+
+// LONG (CE_STATS, CE_GRAD): rows of more than kCeRangeKb k-blocks.  A tile's parts take the two accumulators in
+// turn, as tiles do otherwise.
+template <int KIND, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarps), 1)
     ce_gemm_kernel(const __grid_constant__ CeGemmParams p) {
   constexpr int STAGES = kCeStages;
@@ -489,13 +531,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
       bool ok = true;
       CeIter it(p, live, whole, splits, pair, npairs);
       CeUnit U;
-      while (ok && it.next(p, U)) {
+      int upto = 0;                                          // k-blocks of the tile that are done
+      bool more = false;
+      while (ok && (more || it.next(p, U))) {
         if (!ce_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p)) { ok = false; break; }
         tc_fence_after_sync();
+        const int from = more ? upto : U.kb0;
+        upto = LONG ? min(from + p.kb_range, U.kb1) : U.kb1;
+        more = upto < U.kb1;
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
         const uint32_t idesc = KIND == CE_PART && p.narrow && U.tn == p.tiles_n - 1 ? idesc_narrow : idesc_full;
         uint32_t accumulate = 0;
-        for (int j = U.kb0; j < U.kb1; ++j) {
+        for (int j = from; j < upto; ++j) {
           const int kc = j * kBK;
           if (!landed && !ce_wait(full_bar(stage), phase, abort_flag, p)) { ok = false; break; }
           tc_fence_after_sync();
@@ -524,7 +571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
           phase = nphase;
         }
         if (!ok) break;
-        tc_commit_pair_multicast(tfull_bar(acc), 0x3);       // both halves of the tile ready
+        tc_commit_pair_multicast(tfull_bar(acc), 0x3);       // both halves of the tile, or of its part, ready
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
       if (!ok) {
@@ -567,13 +614,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
     uint32_t acc_phase = 0;
     CeIter it(p, live, whole, splits, pair, npairs);
     CeUnit U;
-    while (it.next(p, U)) {
+    auto landed = [&]() {
       const bool ready = ce_wait(tfull_bar(acc), acc_phase, abort_flag, p);
-      if (!__all_sync(0xffffffffu, ready)) break;
+      if (!__all_sync(0xffffffffu, ready)) return false;
       tc_fence_after_sync();
-      const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
+      return true;
+    };
+    while (it.next(p, U)) {
+      if (!landed()) break;
       const int row = U.tm * (2 * kBM) + row_in_tile;
-      // the accumulator has been read: the MMAs of the tile after next may overwrite it
+      uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
+      // the accumulator has been read: the MMAs of the tile or part after next may overwrite it
       auto release = [&]() {
         tc_fence_before_sync();
         __syncwarp();
@@ -594,6 +645,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
           }
         }
         release();
+      } else if constexpr (LONG) {
+        constexpr int kSpan = BN / kCeSlots;
+        uint32_t z[kSpan / 32][32];              // (zeros first, as a case of its own in the loop spilled registers)
+#pragma unroll
+        for (int c = 0; c < kSpan; ++c) z[c / 32][c % 32] = 0u;
+        bool ok = true;
+        for (int kb = 0; kb < U.kb1; kb += p.kb_range) {
+          if (kb > 0) {
+            if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+            ok = landed();
+            if (!ok) break;
+            tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
+          }
+#pragma unroll
+          for (int c = 0; c < kSpan; c += 16) {
+            uint32_t v[16];
+            __syncwarp();
+            tmem_ld16(tacc + part * kSpan + c, v);
+            tmem_ld_wait_for(v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              uint32_t& sum = z[c / 32][c % 32 + j];
+              sum = __float_as_uint(__uint_as_float(sum) + __uint_as_float(v[j]));
+            }
+          }
+          release();
+        }
+        if (!ok) break;
+        if (p.lg.cap2 > 0.0f) {
+          ce_rows_joined<KIND, true>(p, U, z, row, row < live, part);
+        } else {
+          ce_rows_joined<KIND, false>(p, U, z, row, row < live, part);
+        }
       } else {
         if (p.lg.cap2 > 0.0f) {
           ce_rows<KIND, true>(p, U, tacc, row, row < live, part, release);

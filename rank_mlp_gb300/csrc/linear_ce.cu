@@ -622,27 +622,11 @@ static size_t ce_carve(void* ws, int64_t M, int64_t h, const lora_ce_t& o, bool 
   return c.off;
 }
 
-// The matrix units cut what falls below the last place of their running sum, always toward zero, so
-// that a logit comes out short by a share of itself that grows with the products it sums.  The share
-// depends on the rows, so one constant makes up for it on average only; it is fitted, not derived.
-// Measured against 64 bits at h = 896 and 4096, in 1e-9 a feature, and what the scaling does to the
-// loss's relative error at h = 4096 (1e-6, before -> after; f32 products):
-//   normal               0.86, 0.87    1.85 -> 0.43   (0.15)
-//   heavy-tailed         1.11, 0.95    4.74 -> 2.48   (1.07)
-//   pulled to the label  0.97, 1.01    2.12 -> 0.81   (0.54)   at h = 256 to 8192 1.00 to 1.02: the fit
-//   sorted, one sign     1.40, 1.63    10.1 -> 8.4    (3.5)
-//   all of one sign      1.47, 2.86    0.49 -> 0.46   (1.25)   too little by far: lse 6.7 -> 4.4
-//   19 of 20 zero        0.07, 0.07    0.15 -> 1.47   (0.05)   too much: ten times worse
-// Rows that reach a head are dense, so it is done; a row whose products are summed exactly gets
-// logits that are 1e-9 h too large.
-constexpr float kCeCut = 1.0e-9f;
-
-static CeLogit ce_logit_of(const lora_ce_t& o, int64_t h) {
-  const float up = 1.0f + kCeCut * static_cast<float>(h);
+static CeLogit ce_logit_of(const lora_ce_t& o) {
   CeLogit lg;
-  lg.k2 = o.logit_scale * kLog2e * up;
+  lg.k2 = o.logit_scale * kLog2e;
   lg.cap2 = o.softcap * kLog2e;
-  lg.kc = o.softcap > 0.0f ? 2.0f * kLog2e * (o.logit_scale / o.softcap) * up : 0.0f;
+  lg.kc = o.softcap > 0.0f ? 2.0f * kLog2e * (o.logit_scale / o.softcap) : 0.0f;
   return lg;
 }
 
@@ -656,7 +640,7 @@ static lora_status_t check_ce(int64_t M, int64_t h, int64_t vocab, const lora_ce
       !(o->smoothing >= 0.0f && o->smoothing < 1.0f) ||
       (o->reduction != LORA_LOSS_SUM && o->reduction != LORA_LOSS_MEAN))
     return LORA_ERR_INVALID_ARG;
-  const CeLogit lg = ce_logit_of(*o, h);
+  const CeLogit lg = ce_logit_of(*o);
   if (!std::isfinite(lg.k2) || !std::isfinite(lg.cap2) || !std::isfinite(lg.kc)) return LORA_ERR_INVALID_ARG;
   if (st != LORA_OK || M > kMaxExtent || vocab > kCeMaxVocab) return LORA_ERR_UNSUPPORTED;
   return h % 8 ? LORA_ERR_ALIGNMENT : LORA_OK;
@@ -703,7 +687,7 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
   unsigned* status = static_cast<unsigned*>(ws);
   const int tiles_n = static_cast<int>(ceil_div(vocab, 256)), tiles_h = static_cast<int>(ceil_div(h, 256));
   const int kb_h = static_cast<int>(ceil_div(h, kBK)), kb_v = static_cast<int>(ceil_div(vocab, kBK));
-  const CeLogit lg = ce_logit_of(o, h);
+  const CeLogit lg = ce_logit_of(o);
   const float share = o.smoothing / static_cast<float>(vocab);
 
   CeGatherArgs gather;
@@ -762,6 +746,7 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
       return LORA_ERR_CUDA;
     g.piece = s.piece + k;
     g.kb_total = kb_h;
+    g.kb_range = static_cast<int>(ceil_div(kb_h, ceil_div(kb_h, kCeRangeKb)));
     g.kvalid = static_cast<int>(h);
     g.tiles_n = tiles_n;
     g.band = raster_band();
