@@ -456,7 +456,7 @@ lora_status_t lora_rms_norm_backward(int64_t M, int dim, const lora_heads_t* dy,
  * NULL (the loss alone).  dx may not be x.
  * Logits, their exponentials and all sums are f32.  The matrix units sum up to 1024 features of a logit and
  * cut what falls below the last place (1e-6 of a logit whose products have one sign); such parts join
- * in f32.  For dx the weights of all but the label's word are rounded to bf16 on their way to the
+ * in f32.  A cap costs a logit 24 units of 2^-24 of itself at most.  For dx the weights of all but the label's word are rounded to bf16 on their way to the
  * product with W, and scaled so that their sum stays what it was; the label's stays f32.
  * Tokens are taken in pieces of up to 1 GiB of such exponentials and as much of f32 sums, which live
  * in the workspace.  h a multiple of 8; vocab at most 2^24; x, W, dx 16-byte aligned.  logit_scale finite, not 0;

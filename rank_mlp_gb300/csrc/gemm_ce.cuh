@@ -63,8 +63,7 @@ struct CePiece {
   unsigned redo;           // CE_GRAD's sums left their range: the launches of the second try run
 };
 
-// Logits in units of ln 2 from accumulator values: z2 = v * k2, or cap2 * tanh with
-// v * kc = 2 log2(e) x, x the tanh's argument.
+// Logits in units of ln 2 from accumulator values: z2 = v * k2, or cap2 * tanh(v * kc).
 struct CeLogit {
   float k2, cap2, kc;
 };
@@ -139,17 +138,29 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// z2 of an accumulator value, and with a cap the tanh's slope 1 - tanh^2:
-// q = 2 / (1 + e^(2x)): tanh x = 1 - q, 1 - tanh^2 x = q (2 - q).
-template <bool CAP>
+// z2 of an accumulator value, and with a cap the tanh's slope 1 - tanh^2.  From 0.55 on both come from
+// q = 2 / (1 + e^(2|x|)): tanh |x| = 1 - q, 1 - tanh^2 x = q (2 - q).  Below it 1 - q would keep the last places of 1,
+// so a logit those of its cap; there tanh x = x + x^3 R(x^2), R fitted to within 4e-8 of tanh itself.
+enum CeCap : int { CE_NO_CAP = 0, CE_CAP = 1, CE_CAP_LOW = 2 };      // LOW: |x| is below 0.55
+constexpr float kCeLow = 0.55f;
+template <int CAP>
 __device__ __forceinline__ float ce_logit(float v, const CeLogit& lg, float& slope) {
-  if constexpr (!CAP) {
+  if constexpr (CAP == CE_NO_CAP) {
     slope = 1.0f;
     return v * lg.k2;
   } else {
-    const float q = __fdividef(2.0f, 1.0f + exp2_approx(v * lg.kc));
-    slope = q * (2.0f - q);
-    return fmaf(-lg.cap2, q, lg.cap2);
+    const float x = v * lg.kc, u = x * x;
+    const float r = fmaf(fmaf(fmaf(0.016437581f, u, -0.052671812f), u, 0.13320725f), u, -0.33332947f);
+    const float low = fmaf(x * u, r, x);
+    if constexpr (CAP == CE_CAP_LOW) {
+      slope = fmaf(-low, low, 1.0f);
+      return lg.cap2 * low;
+    } else {
+      const float q = __fdividef(2.0f, 1.0f + exp2_approx(fabsf(x) * (2.0f * kLog2e)));
+      const bool small = fabsf(x) < kCeLow;
+      slope = small ? fmaf(-low, low, 1.0f) : q * (2.0f - q);
+      return lg.cap2 * (small ? low : copysignf(1.0f - q, x));
+    }
   }
 }
 
@@ -255,14 +266,15 @@ __device__ __forceinline__ void ce_chunk(const CeGemmParams& p, const uint32_t (
   const int width = p.vocab - col0;              // columns below the vocabulary's size
   const bool plain = !__any_sync(0xffffffffu, static_cast<unsigned>(at) < 32u) && width >= 32;
   // the label's column and those past the vocabulary leave the sums
-  auto chunk = [&](auto tag) {
-    constexpr bool PLAIN = decltype(tag)::value != 0;
+  auto chunk = [&](auto plain_tag, auto cap_tag) {
+    constexpr bool PLAIN = decltype(plain_tag)::value != 0;
+    constexpr int LOGIT = decltype(cap_tag)::value;
     if constexpr (KIND == CE_STATS) {
       float z[32], most = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         float slope;
-        z[j] = ce_logit<CAP>(__uint_as_float(v[j]), p.lg, slope);
+        z[j] = ce_logit<LOGIT>(__uint_as_float(v[j]), p.lg, slope);
         if (!PLAIN) {
           if (p.zsum != nullptr && j < width) zs += z[j];
           if (j == at) p.zlab[row] = z[j];
@@ -295,7 +307,7 @@ __device__ __forceinline__ void ce_chunk(const CeGemmParams& p, const uint32_t (
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float slope = 1.0f, z = 0.0f;
-          if (CAP || !PLAIN || p.zsum != nullptr) z = ce_logit<CAP>(__uint_as_float(v[j + h]), p.lg, slope);
+          if (CAP || !PLAIN || p.zsum != nullptr) z = ce_logit<LOGIT>(__uint_as_float(v[j + h]), p.lg, slope);
           float x = exp2_approx(CAP ? z - ref2 : fmaf(__uint_as_float(v[j + h]), p.lg.k2, -ref2));
           if (p.zsum != nullptr && (PLAIN || j + h < width)) zs += z;
           if (!PLAIN) {
@@ -322,7 +334,25 @@ __device__ __forceinline__ void ce_chunk(const CeGemmParams& p, const uint32_t (
       }
     }
   };
-  if (plain) chunk(ActTag<1>{}); else chunk(ActTag<0>{});
+  if constexpr (CAP) {
+    // Where all of a chunk's logits are far enough below the cap, as most are, neither the exponential nor the
+    // quotient is needed.  (4096 tokens x 4096 x 131,072 words, cap 30: 5.25 ms; 5.65 with the general form
+    // throughout, 5.11 with the exponential's form alone.)
+    float most = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) most = fmaxf(most, fabsf(__uint_as_float(v[j])));
+    if (!plain) {
+      chunk(ActTag<0>{}, ActTag<CE_CAP>{});
+    } else if (__all_sync(0xffffffffu, most * fabsf(p.lg.kc) < kCeLow)) {
+      chunk(ActTag<1>{}, ActTag<CE_CAP_LOW>{});
+    } else {
+      chunk(ActTag<1>{}, ActTag<CE_CAP>{});
+    }
+  } else if (plain) {
+    chunk(ActTag<1>{}, ActTag<CE_NO_CAP>{});
+  } else {
+    chunk(ActTag<0>{}, ActTag<CE_NO_CAP>{});
+  }
 }
 
 // What the epilogue of one tile row has on its way: the row's running results over the warp's share `part`

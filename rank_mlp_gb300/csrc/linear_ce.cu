@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(256) ce_gather_kernel(const __grid_constant__ 
     for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
     if (lane == 0) {
       float slope;
-      p.r.ref2[at] = (p.lg.cap2 > 0.0f ? ce_logit<true>(dot, p.lg, slope) : ce_logit<false>(dot, p.lg, slope)) + kCeAhead;
+      p.r.ref2[at] = (p.lg.cap2 > 0.0f ? ce_logit<CE_CAP>(dot, p.lg, slope) : ce_logit<CE_NO_CAP>(dot, p.lg, slope)) + kCeAhead;
     }
   }
 }
@@ -626,7 +626,7 @@ static CeLogit ce_logit_of(const lora_ce_t& o) {
   CeLogit lg;
   lg.k2 = o.logit_scale * kLog2e;
   lg.cap2 = o.softcap * kLog2e;
-  lg.kc = o.softcap > 0.0f ? 2.0f * kLog2e * (o.logit_scale / o.softcap) : 0.0f;
+  lg.kc = o.softcap > 0.0f ? o.logit_scale / o.softcap : 0.0f;
   return lg;
 }
 
