@@ -139,10 +139,10 @@ __global__ void __launch_bounds__(norm_threads(T)) norm_kernel(const __grid_cons
     const float sq = squares(1.0f, slots[0]);
     float rstd = rsqrtf(sq / static_cast<float>(p.dim) + p.eps);
     // A row whose squares leave f32's range (above, or below where eps does not cover it) is
-    // summed again 2^70 smaller or larger.
+    // summed again 2^80 smaller, where 32768 squares of bf16's largest value are below 2^112, or 2^70 larger.
     const bool again = sq == INFINITY || (sq < 1e-24f && p.eps < 1e-18f);
     if (T > 32 ? again : __any_sync(0xffffffffu, again)) {
-      const float k = sq == INFINITY ? 0x1p-70f : 0x1p70f;
+      const float k = sq == INFINITY ? 0x1p-80f : 0x1p70f;
       const float q = squares(k, slots[2]);
       if (again) rstd = rsqrtf(q / static_cast<float>(p.dim) + p.eps * k * k) * k;
     }
