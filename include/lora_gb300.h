@@ -421,7 +421,8 @@ lora_status_t lora_paged_attention(int64_t M, int heads_q, const lora_heads_t* q
  *   rn(y * (1 / scale)) of the y that was not rounded; a row whose y holds an infinity or a
  *   NaN gets the scale NaN and codes 0.  Codes are 8-byte aligned.  y_scale f32 [M x heads], NULL
  *   with LORA_NORM_BF16.
- * - rstd f32 [M x heads], or NULL (inference).
+ * - rstd f32 [M x heads], or NULL (inference).  Where it leaves f32's range (eps 0 and a row of zeros, or of values
+ *   below 2.9e-39) it is infinite, and y infinite or NaN.
  * dim a multiple of 8, at most 32768.  M * heads at most 2^31 - 1.  ws: at least 256 bytes. */
 typedef enum { LORA_NORM_BF16 = 0, LORA_NORM_FP8 = 1 } lora_norm_format_t;
 lora_status_t lora_rms_norm(int64_t M, int dim, const lora_heads_t* x, const lora_heads_t* residual,
