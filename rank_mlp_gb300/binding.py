@@ -932,12 +932,24 @@ def scale_rows(x, g, *, out=None, ws=None):
     return out
 
 
+# Whether tensors are at the addresses they had: one call for all, where this PyTorch has it.
+_same_addresses = getattr(torch._C, "_tensors_data_ptrs_at_indices_equal", None) or \
+    (lambda tensors, addresses, _: list(map(torch.Tensor.data_ptr, tensors)) == addresses)
+
+
 class TensorList:
     """The tensors of a call that takes many: contiguous bf16 or f32 tensors on one device, in an order
-    that stays.  A program whose gradients stay where they are builds it once."""
+    that stays.  A program whose gradients stay the same tensors builds it once: it keeps their addresses and
+    compares them at each call, so that a tensor that was given other memory (t.data = ..., set_, resize_) is
+    looked over again.  A gradient that is a new tensor at each step (zero_grad(set_to_none=True), the default)
+    is not the one in the list; pass such gradients as they are."""
 
-    def __init__(self, tensors):
+    def __init__(self, tensors, *, kept=True):
         self.tensors = tuple(tensors)
+        self._kept = kept
+        self._look()
+
+    def _look(self):
         flat = []
         for i, t in enumerate(self.tensors):
             if not isinstance(t, torch.Tensor):
@@ -951,6 +963,10 @@ class TensorList:
             flat += (t.data_ptr(), t.numel(), dtype)
         self._bytes = _pack_tensors(flat)
         self._examples = None
+        if self._kept:
+            # (memory that is held is not given to other tensors: an address that is the same is the same memory)
+            self._memory = [t.untyped_storage() for t in self.tensors]
+            self._compared = list(self.tensors), flat[::3], list(range(len(self.tensors)))
         spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for t in self.tensors if t.numel())
         self.overlap = any(a[1] > b[0] for a, b in zip(spans, spans[1:]))
 
@@ -986,6 +1002,15 @@ def tensor_list(tensors) -> TensorList:
     return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
 
 
+def _list(tensors) -> TensorList:
+    """The list of a call, as its tensors lie now."""
+    if not isinstance(tensors, TensorList):
+        return TensorList(tensors, kept=False)
+    if tensors._kept and not _same_addresses(*tensors._compared):
+        tensors._look()
+    return tensors
+
+
 def _list_device(grads):
     """A tensor of the list's device, or of the current one for an empty list."""
     return grads.tensors[0] if grads.tensors else torch.empty(0, device=torch.device("cuda", _current_device()))
@@ -995,7 +1020,7 @@ def grad_norm(grads, *, norm_type=2.0, ws=None):
     """The norm of all gradients together (a TensorList, or any iterable of tensors), f32, 0-dim: norm_type 2
     or infinity."""
     lib = _LIB or load()
-    grads = tensor_list(grads)
+    grads = _list(grads)
     t = _list_device(grads)
     _together(t, ws)
     norm = torch.empty((), dtype=torch.float32, device=t.device)
@@ -1010,9 +1035,9 @@ def clip_grad_norm(grads, max_norm, *, norm_type=2.0, out=None, ws=None):
     types).  Returns their norm before that, f32, 0-dim.  What is written must not overlap: a gradient twice in the
     list would be scaled twice."""
     lib = _LIB or load()
-    grads = tensor_list(grads)
+    grads = _list(grads)
     t = _list_device(grads)
-    out = None if out is None else tensor_list(out)
+    out = None if out is None else _list(out)
     if (out or grads).overlap:
         raise ValueError("tensors that are written overlap")
     if out is not None:
@@ -1034,7 +1059,7 @@ def clip_examples(grads, max_norm, *, sq_norms=None, scale=1.0, out=None, ws=Non
     grads[i][e], f32.  sq_norms, f32 [examples]: the squared norms if they are known (mlp_backward_per_example's, added
     up), else computed.  out: the f32 tensors for sums."""
     lib = _LIB or load()
-    grads = tensor_list(grads)
+    grads = _list(grads)
     n, shapes, sizes, starts, (pieces, parts), total = grads._example_layout()
     first = grads.tensors[0]
     dev = first.device
@@ -1045,7 +1070,7 @@ def clip_examples(grads, max_norm, *, sq_norms=None, scale=1.0, out=None, ws=Non
         sums = [cut[i] if len(sh) == 1 else cut[i].view(sh) for i, sh in zip(parts, shapes)]
         packed = _pack_tensors([v for a, k in zip(starts, sizes) for v in (base + 4 * a, k, 1)])
     else:
-        out = tensor_list(out)
+        out = _list(out)
         if len(out) != len(grads) or any(o.shape != sh or o.dtype != torch.float32 for o, sh in zip(out.tensors, shapes)):
             raise ValueError("out must be f32 tensors of one example's shapes")
         if out.overlap:

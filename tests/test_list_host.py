@@ -1,0 +1,111 @@
+"""Lists of tensors that are kept from call to call, on a pretended library: no GPU."""
+
+import struct
+import types
+
+import pytest
+import torch
+
+from test_serving_devices import On
+
+F32 = torch.float32
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The binding over a library that keeps what it was given: (name, its arguments)."""
+    from rank_mlp_gb300 import binding as b
+    seen = []
+
+    def entry(name):
+        def f(*a):
+            if not name.endswith("_bytes"):
+                seen.append((name, a))
+            return 0
+        return f
+    names = [n for n in b.EXPORTS if any(k in n for k in ("norm", "clip"))]
+    monkeypatch.setattr(b, "_LIB", types.SimpleNamespace(**{n: entry(n) for n in names}))
+    monkeypatch.setattr(b, "_call", lambda t, n, ws: (0, 256, 256))
+    monkeypatch.setattr(b, "_current_device", lambda: 0)
+    monkeypatch.setattr(b, "torch", types.SimpleNamespace(**{**vars(torch), "empty": lambda *s, dtype=None, device=None: On.make(
+        0, tuple(s[0]) if s and isinstance(s[0], tuple) else s, dtype=dtype or F32)}))
+    return types.SimpleNamespace(b=b, seen=seen)
+
+
+def given(packed):
+    """[(address, elements, type)] of a list as the library gets it."""
+    v = struct.unpack("=" + "QqQ" * (len(packed) // 24), packed)
+    return [tuple(v[i:i + 3]) for i in range(0, len(v), 3)]
+
+
+def of(*ts):
+    return [(t.data_ptr(), t.numel(), {torch.bfloat16: 0, F32: 1}[t.dtype]) for t in ts]
+
+
+def move(t, *shape):
+    """Gives t other memory, as t.data = ... does on a device."""
+    t.set_(torch.zeros(*shape, dtype=t.dtype))
+
+
+@pytest.mark.parametrize("name", ["grad_norm", "clip_grad_norm", "out"])
+def test_a_kept_list_follows_its_tensors(calls, name):
+    """The library gets the addresses that the tensors have at the call."""
+    b = calls.b
+    ts, outs = [On.make(0, 40), On.make(0, 7, dtype=F32)], [On.make(0, 40), On.make(0, 7, dtype=F32)]
+    kept, out = b.tensor_list(ts), b.tensor_list(outs)
+
+    def call():
+        if name == "grad_norm":
+            b.grad_norm(kept)
+        else:
+            b.clip_grad_norm(kept, 1.0, out=out if name == "out" else None)
+        a = calls.seen[-1][1]
+        return given(a[1]), given(a[2]) if name == "out" else None
+    assert call() == (of(*ts), of(*outs) if name == "out" else None)
+    first = call()
+    assert call() == first
+    move(ts[1], 9)
+    move(outs[1], 9)
+    assert call() == (of(*ts), of(*outs) if name == "out" else None) != first
+    ts[0].set_()                                     # nothing is left of it
+    outs[0].set_()
+    assert call()[0] == of(*ts) and call()[0][0][1] == 0
+
+
+def test_examples_follow_too(calls, monkeypatch):
+    b = calls.b
+    monkeypatch.setattr(b, "_together", lambda *ts: None)        # (views of a pretended tensor are on no device)
+    g = On.make(0, 4, 8)
+    kept = b.tensor_list([g])
+    sums, _ = b.clip_examples(kept, 1.0)
+    assert sums[0].shape == (8,) and calls.seen[-1][1][2] == 4
+    move(g, 3, 5)
+    sums, _ = b.clip_examples(kept, 1.0)
+    a = calls.seen[-1][1]
+    assert given(a[1]) == of(g) and a[2] == 3 and sums[0].shape == (5,)
+
+
+def test_a_list_that_moved_is_looked_over_again(calls):
+    """What a list refuses when it is built it refuses later."""
+    b = calls.b
+    t = On.make(0, 6, 8)
+    kept = b.tensor_list([t])
+    t.set_(torch.zeros(8, 6, dtype=torch.bfloat16).t())
+    with pytest.raises(ValueError, match="contiguous"):
+        b.clip_grad_norm(kept, 1.0)
+    u, v = On.make(0, 50), On.make(0, 50)
+    kept = b.tensor_list([u, v])
+    u.set_(v)
+    with pytest.raises(ValueError, match="overlap"):
+        b.clip_grad_norm(kept, 1.0)
+    assert not calls.seen
+
+
+def test_memory_that_a_kept_list_knows_is_not_given_away(calls):
+    """So an address that is the same is the same memory; until the list follows its tensor."""
+    t = On.make(0, 1000)
+    kept, old = calls.b.tensor_list([t]), t.data_ptr()
+    move(t, 10)
+    assert [m.data_ptr() for m in kept._memory] == [old]
+    calls.b.grad_norm(kept)
+    assert [m.data_ptr() for m in kept._memory] == [t.data_ptr()]
