@@ -11,6 +11,7 @@ A [r, in], B [out, r].  Activations are token-major [M, features].
 
 from __future__ import annotations
 
+import bisect
 import ctypes
 import os
 import struct
@@ -967,11 +968,26 @@ class TensorList:
             # (memory that is held is not given to other tensors: an address that is the same is the same memory)
             self._memory = [t.untyped_storage() for t in self.tensors]
             self._compared = list(self.tensors), flat[::3], list(range(len(self.tensors)))
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for t in self.tensors if t.numel())
-        self.overlap = any(a[1] > b[0] for a, b in zip(spans, spans[1:]))
+        self._spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes, i) for i, t in enumerate(self.tensors) if t.numel())
+        self.overlap = any(a[1] > b[0] for a, b in zip(self._spans, self._spans[1:]))
+        self._apart = None
 
     def __len__(self):
         return len(self.tensors)
+
+    def _check_output(self, grads, in_place):
+        """Refuses a list of outputs that overlap each other or the gradients, but (in_place) for the one in their
+        own place."""
+        if self.overlap:
+            raise ValueError("tensors that are written overlap")
+        if self._apart == (grads._bytes, in_place):      # the same addresses and sizes as at the last call
+            return
+        starts = [a for a, _, _ in self._spans]
+        for a, z, i in grads._spans:
+            for own in self._spans[max(bisect.bisect_right(starts, a) - 1, 0):bisect.bisect_left(starts, z)]:
+                if own[1] > a and not (in_place and own == (a, z, i)):
+                    raise ValueError(f"an output overlaps a gradient that is not its own (entries {own[2]} and {i})")
+        self._apart = grads._bytes, in_place
 
     def _example_layout(self):
         """(examples, shapes, sizes, starts, cut, total): one example's parts as one f32 buffer, each 16-byte
@@ -1033,14 +1049,16 @@ def grad_norm(grads, *, norm_type=2.0, ws=None):
 def clip_grad_norm(grads, max_norm, *, norm_type=2.0, out=None, ws=None):
     """Scales all gradients by min(1, max_norm / (norm + 1e-6)), in place or into out (a list of the same shapes and
     types).  Returns their norm before that, f32, 0-dim.  What is written must not overlap: a gradient twice in the
-    list would be scaled twice."""
+    list would be scaled twice; an output may be its own gradient, but overlap no other."""
     lib = _LIB or load()
     grads = _list(grads)
     t = _list_device(grads)
     out = None if out is None else _list(out)
-    if (out or grads).overlap:
-        raise ValueError("tensors that are written overlap")
-    if out is not None:
+    if out is None:
+        if grads.overlap:
+            raise ValueError("tensors that are written overlap")
+    else:
+        out._check_output(grads, True)
         if len(out) != len(grads):                   # (sizes and types are compared in the library)
             raise ValueError("out must match the gradients, tensor by tensor")
         if out.tensors:
@@ -1073,13 +1091,14 @@ def clip_examples(grads, max_norm, *, sq_norms=None, scale=1.0, out=None, ws=Non
         out = _list(out)
         if len(out) != len(grads) or any(o.shape != sh or o.dtype != torch.float32 for o, sh in zip(out.tensors, shapes)):
             raise ValueError("out must be f32 tensors of one example's shapes")
-        if out.overlap:
-            raise ValueError("tensors that are written overlap")
+        out._check_output(grads, False)
         sums, packed = list(out.tensors), out._bytes
     given = sq_norms is not None
     if not given:
         sq_norms = cut[-1] if out is None else torch.empty(n, dtype=torch.float32, device=dev)
     sq_at = _ints(sq_norms, torch.float32, (n,), "sq_norms")
+    if given and out is not None and any(a < sq_at + 4 * n and z > sq_at for a, z, _ in out._spans):
+        raise ValueError("an output overlaps sq_norms")
     _together(first, sums[0], sq_norms, ws)
     stream, wp, wn = _call(first, lib.lora_clip_examples_workspace_bytes(len(grads), n), ws)
     _check(lib.lora_clip_examples(len(grads), grads._bytes, n, packed, max_norm, scale, sq_at, int(given), wp, wn, stream),

@@ -109,3 +109,58 @@ def test_memory_that_a_kept_list_knows_is_not_given_away(calls):
     assert [m.data_ptr() for m in kept._memory] == [old]
     calls.b.grad_norm(kept)
     assert [m.data_ptr() for m in kept._memory] == [t.data_ptr()]
+
+
+def test_an_output_over_another_gradient_is_refused(calls):
+    """out's tensors overlap no gradient but the one in their own place, and that one exactly."""
+    b = calls.b
+    t = On.make(0, 100)
+    part = lambda a, z: as_on(t[a:z])  # noqa: E731
+
+    def as_on(u):
+        u.index = 0
+        return u
+    x, y, z = On.make(0, 30), On.make(0, 30), On.make(0, 30)
+    good = [([x, y], [x, y]), ([x, y], [z, y]), ([x, x], [y, z]), ([part(0, 30), part(30, 60)], [part(0, 30), part(60, 90)]),
+            ([On.make(0, 0), x], [On.make(0, 0), x])]
+    bad = [([x, y], [y, x]), ([x, y], [y, z]), ([x, x], [x, z]), ([part(0, 30)], [part(1, 31)]), ([part(0, 30)], [part(29, 59)]),
+           ([part(0, 60), x], [On.make(0, 60), part(59, 89)]), ([x, part(10, 40)], [part(30, 60), y]),
+           ([part(0, 5), part(40, 60)], [part(20, 25), part(30, 50)])]
+    for grads, out in good + good:
+        b.clip_grad_norm(grads, 1.0, out=out)
+        b.clip_grad_norm(b.tensor_list(grads), 1.0, out=b.tensor_list(out))
+    n = len(calls.seen)
+    for grads, out in bad:
+        with pytest.raises(ValueError, match="overlap"):
+            b.clip_grad_norm(grads, 1.0, out=out)
+    assert len(calls.seen) == n
+    # a list that has been compared with one is compared with another, and again once either has moved
+    out = b.tensor_list([z])
+    b.clip_grad_norm([x], 1.0, out=out)
+    with pytest.raises(ValueError, match="overlap"):
+        b.clip_grad_norm([On.make(0, 30), z], 1.0, out=b.tensor_list([z, y]))
+    with pytest.raises(ValueError, match="overlap"):
+        b.clip_grad_norm([as_on(z[1:])], 1.0, out=b.tensor_list([as_on(z[:-1])]))
+    kept = b.tensor_list([x])
+    b.clip_grad_norm(kept, 1.0, out=out)
+    z.set_(x.untyped_storage(), 10, (20,))
+    with pytest.raises(ValueError, match="overlap"):
+        b.clip_grad_norm(kept, 1.0, out=out)
+    z.set_(x)
+    b.clip_grad_norm(kept, 1.0, out=out)
+
+
+def test_sums_of_examples_over_their_gradients_are_refused(calls):
+    b = calls.b
+    g = On.make(0, 4, 20, dtype=F32)
+    sq = On.make(0, 4, dtype=F32)
+    own = g.view(-1)[40:60]
+    over = sq.as_strided((2,), (1,))
+    own.index = over.index = 0
+    b.clip_examples([g], 1.0, out=[On.make(0, 20, dtype=F32)], sq_norms=sq)
+    n = len(calls.seen)
+    with pytest.raises(ValueError, match="overlap"):
+        b.clip_examples([g], 1.0, out=[own])
+    with pytest.raises(ValueError, match="overlap"):
+        b.clip_examples([On.make(0, 4, 2, dtype=F32)], 1.0, out=[over], sq_norms=sq)
+    assert len(calls.seen) == n
