@@ -844,7 +844,9 @@ def rms_norm(x, weight, *, residual=None, eps=1e-6, offset=0.0, format="bf16", t
         total = _rows(sum_out, "sum_out")
     elif sum_out is not None:
         raise ValueError("sum_out receives x + residual: there is no residual")
-    code = NORM_FORMAT[format]
+    code = NORM_FORMAT.get(format)
+    if code is None:
+        raise ValueError(f"format must be one of {', '.join(NORM_FORMAT)} (got {format!r})")
     scale = None if code == 0 else torch.empty(shape[:-1], dtype=torch.float32, device=dev)
     dtype = _BF16 if code == 0 else torch.float8_e4m3fn
     if out is None:
@@ -1032,6 +1034,13 @@ def _list_device(grads):
     return grads.tensors[0] if grads.tensors else torch.empty(0, device=torch.device("cuda", _current_device()))
 
 
+def _norm_type(norm_type) -> int:
+    code = GRAD_NORM.get(float(norm_type))
+    if code is None:
+        raise ValueError(f"norm_type must be 2 or infinity (got {norm_type!r})")
+    return code
+
+
 def grad_norm(grads, *, norm_type=2.0, ws=None):
     """The norm of all gradients together (a TensorList, or any iterable of tensors), f32, 0-dim: norm_type 2
     or infinity."""
@@ -1041,7 +1050,7 @@ def grad_norm(grads, *, norm_type=2.0, ws=None):
     _together(t, ws)
     norm = torch.empty((), dtype=torch.float32, device=t.device)
     stream, wp, wn = _call(t, lib.lora_grad_norm_workspace_bytes(len(grads)), ws)
-    _check(lib.lora_grad_norm(len(grads), grads._bytes, GRAD_NORM[float(norm_type)], norm.data_ptr(), wp, wn, stream),
+    _check(lib.lora_grad_norm(len(grads), grads._bytes, _norm_type(norm_type), norm.data_ptr(), wp, wn, stream),
            "lora_grad_norm")
     return norm
 
@@ -1066,7 +1075,7 @@ def clip_grad_norm(grads, max_norm, *, norm_type=2.0, out=None, ws=None):
     _together(t, ws)
     norm = torch.empty((), dtype=torch.float32, device=t.device)
     stream, wp, wn = _call(t, lib.lora_grad_norm_workspace_bytes(len(grads)), ws)
-    _check(lib.lora_clip_grads(len(grads), grads._bytes, None if out is None else out._bytes, GRAD_NORM[float(norm_type)],
+    _check(lib.lora_clip_grads(len(grads), grads._bytes, None if out is None else out._bytes, _norm_type(norm_type),
                                max_norm, norm.data_ptr(), wp, wn, stream), "lora_clip_grads")
     return norm
 

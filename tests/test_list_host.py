@@ -164,3 +164,27 @@ def test_sums_of_examples_over_their_gradients_are_refused(calls):
     with pytest.raises(ValueError, match="overlap"):
         b.clip_examples([On.make(0, 4, 2, dtype=F32)], 1.0, out=[over], sq_norms=sq)
     assert len(calls.seen) == n
+
+
+@pytest.mark.parametrize("norm_type", [1.0, 3, 0, -float("inf"), float("nan")])
+def test_other_norms_are_refused_by_name(calls, norm_type):
+    """An error of the call's arguments, as for all others."""
+    b, t = calls.b, On.make(0, 8)
+    for call in (lambda: b.grad_norm([t], norm_type=norm_type), lambda: b.clip_grad_norm([t], 1.0, norm_type=norm_type)):
+        with pytest.raises(ValueError, match="norm_type"):
+            call()
+    assert not calls.seen
+
+
+def test_norm_types_that_there_are(calls):
+    b, t = calls.b, On.make(0, 8)
+    for norm_type, code in ((2, 0), (2.0, 0), ("inf", 1), (float("inf"), 1)):
+        b.grad_norm([t], norm_type=norm_type)
+        assert calls.seen[-1][1][2] == code
+
+
+def test_another_format_of_the_norm_is_refused_by_name(calls):
+    b = calls.b
+    with pytest.raises(ValueError, match="format"):
+        b.rms_norm(On.make(0, 4, 64), On.make(0, 64), format="int8")
+    assert not calls.seen
