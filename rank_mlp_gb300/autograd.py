@@ -124,7 +124,7 @@ class RmsNormFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight, residual, eps: float, offset: float):
-        x2, r2 = _tokens(x), None if residual is None else _tokens(residual)
+        x2, r2 = _tokens(x, residual)
         y, s, rstd = binding.rms_norm(x2, weight, residual=r2, eps=eps, offset=offset, training=True)
         ctx.save_for_backward(s, weight, rstd)
         ctx.offset, ctx.xshape = offset, x.shape
@@ -167,11 +167,15 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
         return dx.reshape(ctx.xshape), None, None, None, None, None, None, None
 
 
-def _tokens(t):
-    """t as rows [tokens, dim] or a view of heads [tokens, heads, dim] that the library takes."""
-    if t.dim() == 2 or (t.dim() == 3 and not t.is_contiguous()):
-        return _strided(t)
-    return _flat(t)
+def _tokens(x, residual):
+    """Both in one layout that the library takes: views of heads [tokens, heads, dim] where that saves a copy (and
+    the library takes so many), else rows [tokens, dim]."""
+    both = [t for t in (x, residual) if t is not None]
+    if all(t.dim() == 3 for t in both) and not all(t.is_contiguous() for t in both) and x.shape[1] <= 65535:
+        both = [_strided(t) for t in both]
+    else:
+        both = [_strided(t) if t.dim() == 2 else _flat(t) for t in both]
+    return both[0], None if residual is None else both[1]
 
 
 def _strided(t):
