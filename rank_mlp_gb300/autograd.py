@@ -155,13 +155,16 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
         total, loss, _, dx = binding.linear_cross_entropy(
             _flat(x), W, labels.reshape(-1).contiguous(), scale=scale, softcap=softcap, smoothing=smoothing,
             ignore_index=ignore_index, reduction="sum" if ctx.none else reduction, grad=ctx.needs_input_grad[0])
-        ctx.save_for_backward(dx)
+        # (a mask: the labels' own buffer may hold the next batch by the time of the backward)
+        ctx.save_for_backward(dx, labels == ignore_index if ctx.none and dx is not None else None)
         return loss.reshape(labels.shape) if ctx.none else total
 
     @staticmethod
     @once_differentiable
     def backward(ctx, g):
-        dx, = ctx.saved_tensors
+        dx, unlabelled = ctx.saved_tensors
+        if ctx.none:
+            g = torch.where(unlabelled, 0.0, g)              # (such a token has no part, whatever g says there)
         # one rounding more where g is no power of two
         dx = binding.scale_rows(dx, g.float().reshape(-1 if ctx.none else ()).contiguous())
         return dx.reshape(ctx.xshape), None, None, None, None, None, None, None
