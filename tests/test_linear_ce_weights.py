@@ -102,3 +102,18 @@ def test_a_piece_that_is_taken_again(lib, head):
     dx = lib.linear_cross_entropy(x, W, y, reduction="sum")[3]
     assert bool(((dx.double() - d64).norm(dim=1) <= slack).all())
     assert lib.poll_status() == 0
+
+
+def test_a_piece_with_a_cap_that_is_taken_again(lib):
+    """The same with a cap above the distance: the weights' own sums come after the row's factors."""
+    x, W, y = problem("near common", 2.0)
+    far = torch.randn(H, generator=torch.Generator(device=DEV).manual_seed(5), device=DEV)
+    x[17] = (30.0 * torch.sign(far)).to(torch.bfloat16)
+    kw = dict(softcap=300.0)
+    z = 300.0 * torch.tanh(x[17].double() @ W.double().T / 300.0)
+    y[17] = int(z.argmin())
+    assert float(z.max() - z.min()) > 110
+    d64, slack = rows64(x, W, y, **kw)
+    dx = lib.linear_cross_entropy(x, W, y, reduction="sum", **kw)[3]
+    assert bool(((dx.double() - d64).norm(dim=1) <= slack).all())
+    assert lib.poll_status() == 0
