@@ -15,11 +15,11 @@ static cudaError_t launch_kind(const CeGemmParams& p, int grid, cudaStream_t st)
 }
 
 cudaError_t launch_ce_gemm(int kind, const CeGemmParams& p, int grid, cudaStream_t st) {
-  const bool parts = p.kb_total > kCeRangeKb;
+  const bool parts = p.kb_range < p.kb_total;
   switch (kind) {
     case CE_STATS: return parts ? launch_kind<CE_STATS, true>(p, grid, st) : launch_kind<CE_STATS, false>(p, grid, st);
     case CE_GRAD: return parts ? launch_kind<CE_GRAD, true>(p, grid, st) : launch_kind<CE_GRAD, false>(p, grid, st);
-    case CE_PART: return launch_kind<CE_PART, false>(p, grid, st);
+    case CE_PART: return parts ? launch_kind<CE_PART, true>(p, grid, st) : launch_kind<CE_PART, false>(p, grid, st);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -50,6 +50,11 @@ constexpr int kCeSlots = kCeWarps / 4;
 // 2048 tokens x 4096 against 50,257 words, the loss alone: 490 us without parts, 496 with parts of 32
 // k-blocks, 508 with 16, 535 with 8; 4096 capped rows with dx the same within 1% but for parts of 8 (2% more).
 constexpr int kCeRangeKb = 16;
+// The same for the product with the head, whose weights are all positive: where the head's rows have a part in
+// common its sums grow steadily over the whole vocabulary.  (4096 rows, 131,072 words, a common part five times the
+// rows' own: dx off by 4e-3 along it without parts, 4.2e-4 with parts of 256 k-blocks, 9e-5 with 64, 5e-5 with 16;
+// 1255, 1265, 1270 and 1280 us at h = 896.)
+constexpr int kCePartKb = 64;
 constexpr int kCeMaxSplits = 32;
 constexpr int kCeTailUnits = 304;        // units of a launch at most that are parts of tiles
 constexpr float kLog2e = 1.4426950408889634f;
@@ -73,7 +78,7 @@ struct CeGemmParams {
   const CePiece* piece;
   int when_redo;           // 1: only if the piece's `redo` is set
   int kb_total, kvalid;    // 64-wide k-blocks, valid K
-  int kb_range;            // CE_STATS, CE_GRAD: k-blocks of a part of the sums
+  int kb_range;            // k-blocks of a part of the sums
   int tiles_n, band;
   int narrow;              // CE_PART: 1 if the last n-tile is 128 columns wide
   unsigned* status;
@@ -130,6 +135,18 @@ __host__ __device__ inline CePiece ce_piece(int live, int tiles_n, int kb, int p
   q.splits = tiles > q.whole ? ce_splits(tiles - q.whole, kb, pairs) : 1;
   q.redo = 0;
   return q;
+}
+
+// Whether a piece of up to `rows` rows can have units of more than kCePartKb k-blocks, however many of them are
+// labelled.  The kernel without parts takes 63 registers a thread instead of 168, so that the next kernel's blocks
+// fit beside it: 64 tokens x 896 x 32,000 64.0 us instead of 65.8.
+inline bool ce_part_long(int64_t rows, int tiles_n, int kb, int pairs) {
+  for (int64_t m = 1; m <= (rows + 255) / 256; ++m) {
+    if (m * tiles_n >= pairs) return kb > kCePartKb;
+    const int s = ce_splits(static_cast<int>(m) * tiles_n, kb, pairs);
+    if ((kb + s - 1) / s > kCePartKb) return true;
+  }
+  return false;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -425,8 +442,7 @@ __device__ __forceinline__ void ce_rows_joined(const CeGemmParams& p, const CeUn
   r.store(p, U, part);
 }
 
-// LONG (CE_STATS, CE_GRAD): rows of more than kCeRangeKb k-blocks.  A tile's parts take the two accumulators in
-// turn, as tiles do otherwise.
+// LONG: units of more than kb_range k-blocks.  A unit's parts take the two accumulators in turn, as units do otherwise.
 template <int KIND, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarps), 1)
     ce_gemm_kernel(const __grid_constant__ CeGemmParams p) {
@@ -660,7 +676,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
         __syncwarp();
         if (lane == 0) arrive_read(tempty_even[acc]);
       };
-      if constexpr (KIND == CE_PART) {
+      if constexpr (KIND == CE_PART && !LONG) {
         constexpr int kSpan = BN / kCeSlots;
         float* dst = p.slab + (static_cast<long long>(U.u) * (2 * kBM) + row_in_tile) * BN;
 #pragma unroll 1
@@ -677,12 +693,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
         release();
       } else if constexpr (LONG) {
         constexpr int kSpan = BN / kCeSlots;
-        uint32_t z[kSpan / 32][32];              // (zeros first, as a case of its own in the loop spilled registers)
+        uint32_t z[kSpan / 32][32];
+        const bool wide = KIND != CE_PART || part == 0 || !p.narrow || U.tn < p.tiles_n - 1;   // the tile has the warp's columns
+        // (zeros first: the first part as a case of its own spilled 1 KB of registers)
 #pragma unroll
         for (int c = 0; c < kSpan; ++c) z[c / 32][c % 32] = 0u;
         bool ok = true;
-        for (int kb = 0; kb < U.kb1; kb += p.kb_range) {
-          if (kb > 0) {
+        for (int kb = U.kb0; kb < U.kb1; kb += p.kb_range) {
+          if (kb > U.kb0) {
             if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
             ok = landed();
             if (!ok) break;
@@ -690,6 +708,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
           }
 #pragma unroll
           for (int c = 0; c < kSpan; c += 16) {
+            if (!wide) break;
             uint32_t v[16];
             __syncwarp();
             tmem_ld16(tacc + part * kSpan + c, v);
@@ -703,7 +722,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
           release();
         }
         if (!ok) break;
-        if (p.lg.cap2 > 0.0f) {
+        if constexpr (KIND == CE_PART) {
+          float* dst = p.slab + (static_cast<long long>(U.u) * (2 * kBM) + row_in_tile) * BN + part * kSpan;
+          if (wide && row < live) {
+#pragma unroll
+            for (int c = 0; c < kSpan; c += 8) st_global_v8(dst + c, &z[c / 32][c % 32]);
+          }
+        } else if (p.lg.cap2 > 0.0f) {
           ce_rows_joined<KIND, true>(p, U, z, row, row < live, part);
         } else {
           ce_rows_joined<KIND, false>(p, U, z, row, row < live, part);

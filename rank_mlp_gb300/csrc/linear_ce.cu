@@ -815,6 +815,7 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
     d.piece = s.piece + k;
     d.blocks = static_cast<int>(P.blocks);
     d.kb_total = kb_v;
+    d.kb_range = ce_part_long(rows, tiles_h, kb_v, num_sms() / 2) ? kCePartKb : kb_v;
     d.kvalid = static_cast<int>(vocab);
     d.tiles_n = tiles_h;
     d.narrow = h - (tiles_h - 1) * int64_t(256) <= 128;

@@ -117,3 +117,31 @@ def test_a_piece_with_a_cap_that_is_taken_again(lib):
     dx = lib.linear_cross_entropy(x, W, y, reduction="sum", **kw)[3]
     assert bool(((dx.double() - d64).norm(dim=1) <= slack).all())
     assert lib.poll_status() == 0
+
+
+@pytest.mark.parametrize("M,h", [(64, 128), (4096, 896), (2400, 2056)])
+def test_a_common_direction_over_a_long_vocabulary(lib, M, h):
+    """No word stands out, so the product with the head grows steadily along the common direction, over 8192 steps.
+    4096 features are summed at a time, 256 steps of up to 2^-23 of the sum each: 2^-16 of half the part's end on average,
+    whichever the rows; the parts join in f32.  Many rows fill whole waves of tiles, few are cut into ranges."""
+    V, n = 131072, 48
+    g = torch.Generator(device=DEV).manual_seed(0)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    common = 5.0 * r(1, h) * h ** -0.5
+    W = (r(V, h) * h ** -0.5 + common).to(torch.bfloat16)
+    x = 1.5 * r(M, h)
+    x = (x - (x @ common.T) * common / common.square().sum()).to(torch.bfloat16)
+    y = torch.randint(0, V, (M,), generator=g, device=DEV)
+    dx = lib.linear_cross_entropy(x, W, y, reduction="sum")[3][:n].double()
+    w64 = W.double()
+    p = torch.softmax(x[:n].double() @ w64.T, 1)
+    p[torch.arange(n), y[:n]] -= 1
+    d64 = p @ w64
+    size = w64.norm(dim=1).mean()
+    slack = (BF16 + 2e-5) * d64.norm(dim=1) + (2.0 ** -17 + 64 * F32) * size + BF16 * 4 * V ** -0.5 * size
+    assert bool(((dx - d64).norm(dim=1) <= slack).all())
+    along = ((dx - d64) @ (common[0] / common.norm()).double()).abs()
+    # the output's rounding along one direction: 2^-8 of a feature, of unlike signs
+    limit = 4 * BF16 * (d64.square() * (common[0] / common.norm()).double().square()).sum(1).sqrt() + (2.0 ** -17 + 64 * F32) * size
+    assert bool((along <= limit).all()), f"{float((along / limit).max()):.2f}"
+    assert lib.poll_status() == 0
