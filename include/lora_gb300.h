@@ -454,7 +454,7 @@ lora_status_t lora_rms_norm_backward(int64_t M, int dim, const lora_heads_t* dy,
  * A token whose label is ignore_index has no part in it: its loss, lse and dx row are 0 and its
  * x is not used.  So has one whose label is outside [0, vocab), which is reported
  * (LORA_ERR_DEVICE_INPUT).  loss, lse f32 [M], or NULL; total f32 [1]; dx bf16 [M x h], or
- * NULL (the loss alone).  dx may not be x.
+ * NULL (the loss alone).  dx may not overlap x or W.
  * Logits, their exponentials and all sums are f32.  The matrix units sum up to 1024 features of a logit and
  * cut what falls below the last place (1e-6 of a logit whose products have one sign); such parts join
  * in f32.  A cap costs a logit 24 units of 2^-24 of itself at most.  For dx the weights of all but the label's word are rounded to bf16 on their way to the

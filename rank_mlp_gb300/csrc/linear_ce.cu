@@ -646,6 +646,11 @@ static lora_status_t check_ce(int64_t M, int64_t h, int64_t vocab, const lora_ce
   return h % 8 ? LORA_ERR_ALIGNMENT : LORA_OK;
 }
 
+static bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q + static_cast<uintptr_t>(b_bytes) && q < p + static_cast<uintptr_t>(a_bytes);
+}
+
 static lora_status_t ce_gemm(int kind, CeGemmParams& p, cudaStream_t st) {
   p.timeout_ns = wait_timeout_ns();
   p.inject_stall = take_expiry();
@@ -673,10 +678,11 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
   NvtxRange nvtx_range("lora_linear_ce");
   if (!W || !total || (M > 0 && (!x || !labels))) return LORA_ERR_INVALID_ARG;
   LGB_TRY(check_ce(M, h, vocab, opts));
-  if (dx != nullptr && dx == x) return LORA_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(W, 16) || !aligned(dx, 16) || !aligned(labels, 8) || !aligned(loss, 4) || !aligned(lse, 4) ||
       !aligned(total, 4))
     return LORA_ERR_ALIGNMENT;
+  // (other rows of x are packed, and W is read, while rows of dx are written)
+  if (dx != nullptr && M > 0 && (overlap(dx, M * h * 2, x, M * h * 2) || overlap(dx, M * h * 2, W, vocab * h * 2))) return LORA_ERR_INVALID_ARG;
   const lora_ce_t& o = *opts;
   const bool want = dx != nullptr, mean = o.reduction == LORA_LOSS_MEAN;
   const CePlan P = ce_plan(M, h, vocab, o, want);
