@@ -985,11 +985,17 @@ class TensorList:
         if self._apart == (grads._bytes, in_place):      # the same addresses and sizes as at the last call
             return
         starts = [a for a, _, _ in self._spans]
-        for a, z, i in grads._spans:
+        for a, z, i in grads._spans if self._meets(grads) else ():
             for own in self._spans[max(bisect.bisect_right(starts, a) - 1, 0):bisect.bisect_left(starts, z)]:
                 if own[1] > a and not (in_place and own == (a, z, i)):
                     raise ValueError(f"an output overlaps a gradient that is not its own (entries {own[2]} and {i})")
         self._apart = grads._bytes, in_place
+
+    def _meets(self, other):
+        """Whether the two lists' memory reaches into each other's at all: two buffers' parts do not."""
+        if not self._spans or not other._spans:
+            return False
+        return self._spans[0][0] < max(z for _, z, _ in other._spans) and other._spans[0][0] < max(z for _, z, _ in self._spans)
 
     def _example_layout(self):
         """(examples, shapes, sizes, starts, cut, total): one example's parts as one f32 buffer, each 16-byte
