@@ -317,32 +317,34 @@ __device__ __forceinline__ void ce_chunk(const CeGemmParams& p, const uint32_t (
       sum += s0 + s1;
     } else {
       uint32_t w[16];
-      float s0 = 0.0f, s1 = 0.0f, r0 = 0.0f, r1 = 0.0f, t0 = 0.0f, t1 = 0.0f;
+      // of the exponentials, of the weights as stored and as they were, two terms an instruction (one each: 64 x 896 x
+      // 32,000 64.9 us instead of 62.0)
+      TwoSums all, stored, before;
 #pragma unroll
       for (int j = 0; j < 32; j += 2) {
-        float e[2];
+        float x[2], e[2], d[2];
+        if (!CAP) fma_two(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), p.lg.k2, -ref2, d[0], d[1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float slope = 1.0f, z = 0.0f;
           if (CAP || !PLAIN || p.zsum != nullptr) z = ce_logit<LOGIT>(__uint_as_float(v[j + h]), p.lg, slope);
-          float x = exp2_approx(CAP ? z - ref2 : fmaf(__uint_as_float(v[j + h]), p.lg.k2, -ref2));
+          x[h] = exp2_approx(CAP ? z - ref2 : d[h]);
           if (p.zsum != nullptr && (PLAIN || j + h < width)) zs += z;
           if (!PLAIN) {
             if (j + h == at) p.zlab[row] = z;
-            if (j + h == at || j + h >= width) x = 0.0f;
+            if (j + h == at || j + h >= width) x[h] = 0.0f;
           }
-          (h ? s1 : s0) += x;
-          e[h] = CAP ? (x - p.minus) * slope : x;
+          e[h] = CAP ? (x[h] - p.minus) * slope : x[h];
           if (CAP && !PLAIN && (j + h == at || j + h >= width)) e[h] = 0.0f;
         }
         w[j / 2] = pack_bf16x2(e[0], e[1]);
-        r0 += __uint_as_float(w[j / 2] << 16);
-        r1 += __uint_as_float(w[j / 2] & 0xFFFF0000u);
-        if (CAP) t0 += e[0], t1 += e[1];
+        all.add(x[0], x[1]);
+        stored.add(__uint_as_float(w[j / 2] << 16), __uint_as_float(w[j / 2] & 0xFFFF0000u));
+        if (CAP) before.add(e[0], e[1]);
       }
-      sum += s0 + s1;
-      ws += r0 + r1;
-      if (CAP) ts += t0 + t1;
+      sum += all.total();
+      ws += stored.total();
+      if (CAP) ts += before.total();
       if (ok) {
         // (the same stores into rows of the whole vocabulary: 635 us for 608)
         __nv_bfloat16* dst = p.e + (static_cast<long long>(row >> 7) * p.blocks + (col0 >> 6)) * 8192 + (row & 127) * 64 + (col0 & 63);

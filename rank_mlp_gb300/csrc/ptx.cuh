@@ -466,6 +466,24 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
+// a0 b + c and a1 b + c by one instruction, each rounded once.
+__device__ __forceinline__ void fma_two(float a0, float a1, float b, float c, float& y0, float& y1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(y0), "=f"(y1) : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+// Two f32 sums that run beside each other, a term added to each by one instruction.
+struct TwoSums {
+  uint64_t both = 0;
+  __device__ __forceinline__ void add(float a, float b) {
+    asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tadd.rn.f32x2 %0, %0, t;\n\t}" : "+l"(both) : "f"(a), "f"(b));
+  }
+  __device__ __forceinline__ float total() const {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(both));
+    return a + b;
+  }
+};
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
