@@ -459,8 +459,10 @@ lora_status_t lora_rms_norm_backward(int64_t M, int dim, const lora_heads_t* dy,
  * cut what falls below the last place (1e-6 of a logit whose products have one sign); such parts join
  * in f32.  A cap costs a logit 24 units of 2^-24 of itself at most.  For dx the weights of all but the label's word are rounded to bf16 on their way to the
  * product with W, and scaled so that their sum stays what it was; the label's stays f32.
- * Tokens are taken in pieces of up to 1 GiB of such exponentials and as much of f32 sums, which live
- * in the workspace.  h a multiple of 8; vocab at most 2^24; x, W, dx 16-byte aligned.  logit_scale finite, not 0;
+ * Tokens are taken in pieces of up to 1 GiB of such weights (256 tokens at least) and as much of f32 sums, which live
+ * in the workspace: a piece has a bf16 number for every logit.  With dx 4096 tokens x 4096 x 131,072 words take
+ * 1.2 GiB, 2048 x 4096 x 50,257 327 MiB, 64 x 896 x 32,000 49 MiB; the loss alone 64, 22 and 0.6 MiB.  A label
+ * more than 100 below its row's largest logit makes its piece take both products again.  h a multiple of 8; vocab at most 2^24; x, W, dx 16-byte aligned.  logit_scale finite, not 0;
  * softcap finite, >= 0; 0 <= smoothing < 1.
  * ws: lora_linear_ce_workspace_bytes (0 for sizes or options that the call refuses), which
  * grows with M by x's own size and the pieces. */
@@ -518,8 +520,8 @@ lora_status_t lora_clip_grads(int64_t n, const lora_tensor_t* grads, const lora_
  * out: n tensors of f32, of count / n_examples elements each, that overlap nothing else.
  * sq_norms f32 [n_examples] holds the examples' squared norms: norms_given != 0 reads them (as
  * lora_mlp_backward_per_example gives them, added over its calls), else the call writes them.
- * Sums are f32, in a fixed order of the examples.  An example
- * whose norm is not finite makes the sums NaN where its factor or its elements do.
+ * Sums are f32, in a fixed order of the examples; squares too, so that elements below 1e-23 count as zero in a
+ * norm and one beyond 1.8e19 is infinite.  An example whose norm is not finite makes the sums NaN where its factor or its elements do.
  * max_norm > 0, scale finite; n_examples at most 65535.
  * ws: lora_clip_examples_workspace_bytes(n, n_examples) (0 for what the call refuses). */
 size_t lora_clip_examples_workspace_bytes(int64_t n, int64_t n_examples);

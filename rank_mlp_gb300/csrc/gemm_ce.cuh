@@ -22,9 +22,9 @@
 // most rows there can be and its units follow from the number it finds.
 //
 // Bound by the matrix units and, at 14 k-blocks a tile, by what the epilogue adds: 3686 rows x 896
-// against 131072 words take 600 us (1.44 PFLOP/s), 538 without the stores of the exponentials, 558 with
-// them all in one place (so their way to memory costs most), 505 with no epilogue.  At 64 k-blocks
-// capped logits run at 1.5 to 1.6 PFLOP/s, the loss alone at 1.75; CE_PART at 1.55 to 1.75.
+// against 131072 words take 615 us (1.41 PFLOP/s).  Before the weights' sums were kept it was 600 us, 538 without
+// the stores of the exponentials, 558 with them all in one place (so their way to memory costs most), 505 with no
+// epilogue.  At 64 k-blocks capped logits run at 1.4 to 1.5 PFLOP/s, the loss alone at 1.65; CE_PART at 1.55 to 1.7.
 #pragma once
 
 #include "gemm_pair.cuh"

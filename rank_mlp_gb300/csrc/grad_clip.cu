@@ -3,9 +3,14 @@
 //
 // A list travels in the launch's parameters (up to kListMax tensors a launch), so nothing is
 // copied to the device ahead of a call and a captured call keeps its own.  Tensors are cut
-// into chunks of kChunk elements and every block takes an equal share of neighbouring chunks: it
-// finds its first tensor by bisection of the chunks' running count, then walks on.  All is
-// bound by memory.
+// into chunks of chunk_of() elements and every block takes an equal share of neighbouring chunks: the host
+// writes which tensor it begins with into the parameters, and it walks on from there.  (A block of the examples'
+// sum has one chunk and finds its tensor by bisection.)  All is bound by memory.
+//
+// Sums are f32.  A thread adds up to 64 squares of a batch of loads (32 of f32 tensors), then its batches, one for
+// each 10 million (5 million) elements of a launch; a block's threads join in 8 steps, the blocks' results in 3
+// and 8.  So a square is rounded fewer than 256 times in lists of up to 10^9 elements a launch, and their sum is off by
+// less than 256 * 2^-24 of itself.
 #include "serve.cuh"
 
 namespace lgb {
@@ -175,7 +180,8 @@ __device__ __forceinline__ float whole_norm(const float* part, int parts, int in
   return inf_norm ? v : sqrtf(v);
 }
 
-// Elements [a, b) of in times k, into out.
+// Elements [a, b) of in times k, into out.  Where the two lie at unlike distances from 16-byte boundaries they go one
+// by one: 126 million f32 in 506 us instead of 241, bf16 in 446 instead of 127.
 template <typename T>
 __device__ __forceinline__ void scale_span(const T* in, T* out, long long a, long long b, float k) {
   constexpr int per = 16 / sizeof(T);

@@ -12,7 +12,8 @@
 // leaves the largest exponential between e^-40 and, where the largest logit stands less than 100
 // above the label's, e^60: it, the sums and the product stay inside the range of f32 and bf16
 // (a weight below 2^-68 of the label's counts as zero).  A row beyond that is seen by its sum,
-// and its piece is taken again the last way.
+// and its piece is taken again the last way: one such token among 4095 x 896 x 131,072, a single piece, makes
+// 1.3 ms 2.6, among 4096 x 4096 x 131,072 5.6 ms 11.
 #include "gemm_ce.cuh"
 #include "serve.cuh"
 
