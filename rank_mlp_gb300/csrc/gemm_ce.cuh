@@ -95,6 +95,7 @@ struct CeGemmParams {
   float* tsum;             // and before their rounding (with a cap; without, they are psum)
   float* zsum;             // [tiles_n * kCeSlots][ldp] sums of z2, label included, or NULL
   float* zlab;             // the label's z2
+  float* slope;            // with a cap: its tanh's slope (z2 near the cap says little of it)
   long long ldp;
   __nv_bfloat16* e;        // [rows / 128][blocks][128][64]: what one CTA takes of a k-block together
   int blocks;              // 64-wide blocks of the vocabulary
@@ -294,7 +295,10 @@ __device__ __forceinline__ void ce_chunk(const CeGemmParams& p, const uint32_t (
         z[j] = ce_logit<LOGIT>(__uint_as_float(v[j]), p.lg, slope);
         if (!PLAIN) {
           if (p.zsum != nullptr && j < width) zs += z[j];
-          if (j == at) p.zlab[row] = z[j];
+          if (j == at) {
+            p.zlab[row] = z[j];
+            if (CAP) p.slope[row] = slope;
+          }
           if (j == at || j >= width) z[j] = -INFINITY;
         }
         most = fmaxf(most, z[j]);
@@ -331,7 +335,10 @@ __device__ __forceinline__ void ce_chunk(const CeGemmParams& p, const uint32_t (
           x[h] = exp2_approx(CAP ? z - ref2 : d[h]);
           if (p.zsum != nullptr && (PLAIN || j + h < width)) zs += z;
           if (!PLAIN) {
-            if (j + h == at) p.zlab[row] = z;
+            if (j + h == at) {
+              p.zlab[row] = z;
+              if (CAP) p.slope[row] = slope;
+            }
             if (j + h == at || j + h >= width) x[h] = 0.0f;
           }
           e[h] = CAP ? (x[h] - p.minus) * slope : x[h];

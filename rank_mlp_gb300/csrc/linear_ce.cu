@@ -35,6 +35,7 @@ struct CeRows {
   int* label;
   float* ref2;             // the reference, in units of ln 2 as all logits here
   float* zlab;             // the label's logit
+  float* slope;            // with a cap: its tanh's slope there
   float* rs;               // factors of the row's gradient: of sum e W, and of W_label
   float* coef;
 };
@@ -341,11 +342,7 @@ __device__ __forceinline__ void ce_join_rows(const CeJoinArgs& p, int live) {
   if (p.lse != nullptr) p.lse[token] = fmaf(zl, kLn2, ce);
   if (MODE == CE_JOIN_LOSS) return;
   const float g = p.scale / (p.mean ? static_cast<float>(count) : 1.0f);
-  float slope = 1.0f;
-  if (p.cap2 > 0.0f) {
-    const float t = zl / p.cap2;
-    slope = 1.0f - t * t;
-  }
+  const float slope = p.cap2 > 0.0f ? __ldcg(p.r.slope + row) : 1.0f;
   const float away = expm1f(-ce);                    // p_label - 1
   if (MODE == CE_JOIN_EXACT) {
     p.r.ref2[row] = fmaf(ce, kLog2e, zl);
@@ -607,6 +604,7 @@ static size_t ce_carve(void* ws, int64_t M, int64_t h, const lora_ce_t& o, bool 
   s.r.label = c.take_n<int>(M);
   s.r.ref2 = c.take_n<float>(M);
   s.r.zlab = c.take_n<float>(M);
+  s.r.slope = o.softcap > 0.0f ? c.take_n<float>(M) : nullptr;
   s.r.rs = c.take_n<float>(M);
   s.r.coef = c.take_n<float>(M);
   s.loss = c.take_n<float>(M);
@@ -745,6 +743,7 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
     r.label += row0;
     r.ref2 += row0;
     r.zlab += row0;
+    if (r.slope != nullptr) r.slope += row0;
     r.rs += row0;
     r.coef += row0;
     CeGemmParams g;
@@ -767,6 +766,7 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
     g.wsum = s.wsum;
     g.tsum = s.tsum;
     g.zlab = r.zlab;
+    g.slope = r.slope;
     g.ldp = P.rows;
     g.e = s.e;
     g.blocks = static_cast<int>(P.blocks);

@@ -49,3 +49,34 @@ def test_a_cap_far_away(lib, cap, smoothing):
         if grad:
             assert bool(((dx.double() - d64).norm(dim=1) <= 3 * BF16 * d64.norm(dim=1)).all())
     assert lib.poll_status() == 0
+
+
+@pytest.mark.parametrize("smoothing", [0.0, 0.1])
+@pytest.mark.parametrize("M,h,V", [(130, 64, 300), (40, 2056, 1000)])
+def test_logits_at_the_cap(lib, M, h, V, smoothing):
+    """Rows whose logits reach 2 to 8 times the cap: all slopes are small, the label's too, and dx keeps its relative
+    precision.  A slope 4 e^(-2x) takes twice the error of its argument (16 times 2e-6 here) and of its
+    exponential; weights their rounding, and with smoothing what moves to the label's row."""
+    cap = 5.0
+    g = torch.Generator(device=DEV).manual_seed(0)
+    u = torch.randn(h, generator=g, device=DEV)
+    u = u / u.norm()
+    reach = torch.linspace(2.0, 8.0, M, device=DEV)[:, None] * cap
+    W = (u + 0.2 * torch.randn(V, h, generator=g, device=DEV) * h ** -0.5).to(torch.bfloat16)
+    x = (reach * u + 0.05 * torch.randn(M, h, generator=g, device=DEV)).to(torch.bfloat16)
+    y = torch.randint(0, V, (M,), generator=g, device=DEV)
+    w64 = W.double()
+    a = x.double() @ w64.T / cap
+    z = cap * torch.tanh(a)
+    slope = torch.cosh(a) ** -2
+    assert float(slope.max(1).values.min()) < 1e-4
+    dz = (torch.softmax(z, 1) - smoothing / V) * slope
+    at = y[:, None]
+    dz.scatter_add_(1, at, -(1 - smoothing) * slope.gather(1, at))
+    d64 = dz @ w64
+    size = (dz.abs() @ w64.norm(dim=1)[:, None])[:, 0]
+    dx = lib.linear_cross_entropy(x, W, y, softcap=cap, smoothing=smoothing, reduction="sum")[3]
+    err = (dx.double() - d64).norm(dim=1)
+    over = err / (BF16 * d64.norm(dim=1) + (3 * BF16 + 1e-4) * size)
+    assert bool((over <= 1).all()), f"{float(over.max()):.1f} times what is allowed"
+    assert lib.poll_status() == 0
