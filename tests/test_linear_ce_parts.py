@@ -72,3 +72,25 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(lib):
         for a, b in zip(want[grad], lib.linear_cross_entropy(x, W, y, grad=grad)):
             assert a is b is None or torch.equal(a, b)
     assert lib.poll_status() == 0
+
+
+@pytest.mark.parametrize("far", [[5], [990], [5, 990]])
+def test_pieces_of_which_some_are_taken_again(lib, far):
+    """Two pieces of tokens; the total waits for the last one's second try."""
+    from train_ref import F32, ce64, within
+    M, h, V = 1000, 24, 600_011
+    x, W, y = problem(M, h, V, seed=3)
+    y[far] = 17
+    d = W[400_000].float() - W[17].float()
+    x[far] = (x[far].float() + 150 * d / d.square().sum()).to(torch.bfloat16)
+    total, loss, lse, dx = lib.linear_cross_entropy(x, W, y)
+    n = int((y != -100).sum())
+    for a in (0, 460, 940):
+        part = slice(a, a + 60)
+        _, l64, s64, d64, off, slack = ce64(x[part], W, y[part], reduction="sum")
+        within(loss[part], l64, off + 4 * F32 * l64.abs(), "loss")
+        within(lse[part], s64, off + 4 * F32 * s64.abs(), "lse")
+        within(dx[part], d64 / n, slack / n, "dx")
+    want = float(loss.double().sum()) / n
+    assert abs(float(total) - want) <= 4 * F32 * want and float(loss[far].min()) > 100
+    assert lib.poll_status() == 0
