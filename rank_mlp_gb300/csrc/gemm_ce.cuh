@@ -104,7 +104,6 @@ struct CeGemmParams {
   float* slab;             // [units][256][256]
   int balance;             // rows' factors follow the weights' sums here: 0 no, 1 yes, 2 if the piece's `redo` is set
   int slots;
-  float limit;
   float* rs;
   float* coef;
 };
@@ -183,10 +182,11 @@ __device__ __forceinline__ float ce_logit(float v, const CeLogit& lg, float& slo
 }
 
 // Factors of a row (rs: of its weights' product with W, coef: of the label's row of W) for weights that
-// summed to t and, rounded, to w.  All weights are multiplied by t / w; where their signs differ and
-// they cancel (t not above `limit`; the smoothing's part, with a cap) the difference goes to the label instead.
-__device__ __forceinline__ void ce_balance(float t, float w, float limit, float& rs, float& coef) {
-  if (t > limit && w > 0.0f) {
+// summed to t and, rounded, to w.  All weights are multiplied by t / w, which weights of one sign move by 2^-8
+// at most.  Where it is more, their signs differ and they cancel (the smoothing's part, with a cap), and the
+// difference goes to the label instead.
+__device__ __forceinline__ void ce_balance(float t, float w, float& rs, float& coef) {
+  if (fabsf(t - w) <= 0x1p-8f * fabsf(t) && w != 0.0f) {
     rs *= t / w;
   } else {
     coef = fmaf(rs, t - w, coef);
@@ -657,7 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(kCeWarp
           }
           if (lane == 0) {
             float rs = __ldcg(p.rs + row), coef = __ldcg(p.coef + row);
-            ce_balance(t, w, p.limit, rs, coef);
+            ce_balance(t, w, rs, coef);
             p.rs[row] = rs;
             p.coef[row] = coef;
           }

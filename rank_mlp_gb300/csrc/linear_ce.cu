@@ -350,7 +350,7 @@ __device__ __forceinline__ void ce_join_rows(const CeJoinArgs& p, int live) {
     p.r.coef[row] = g * slope * (away + eps - p.minus);
   } else {
     float rs = g / (sum + exp2f(zl - ref2)), coef = g * slope * (away + eps);
-    ce_balance(own ? t : sum, w, 0.0f, rs, coef);
+    ce_balance(own ? t : sum, w, rs, coef);
     p.r.rs[row] = rs;
     p.r.coef[row] = coef;
   }
@@ -834,8 +834,6 @@ extern "C" lora_status_t lora_linear_ce(int64_t M, int64_t h, int64_t vocab, con
     d.wsum = s.wsum;
     d.ldp = P.rows;
     d.slots = static_cast<int>(P.slots);
-    // weights of unlike signs: the negative ones come to the smoothing at most
-    d.limit = P.exact ? 2.0f * o.smoothing : 0.0f;
     d.rs = r.rs;
     d.coef = r.coef;
     LGB_TRY(ce_gemm(CE_PART, d, stream));

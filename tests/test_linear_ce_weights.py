@@ -145,3 +145,30 @@ def test_a_common_direction_over_a_long_vocabulary(lib, M, h):
     limit = 4 * BF16 * (d64.square() * (common[0] / common.norm()).double().square()).sum(1).sqrt() + (2.0 ** -17 + 64 * F32) * size
     assert bool((along <= limit).all()), f"{float((along / limit).max()):.2f}"
     assert lib.poll_status() == 0
+
+
+@pytest.mark.parametrize("smoothing", [0.1, 0.6])
+@pytest.mark.parametrize("V", [3, 300, 5003])
+def test_capped_and_smoothed_weights_of_one_size(lib, V, smoothing):
+    """Logits near zero: all weights but the label's are alike and so is their rounding, which their sum's factor takes
+    away.  What is left is the output's rounding, weights that differ by their logits' 0.1 or less and so in
+    a few of their 2^-8 steps, and 1e-5 of the terms."""
+    M, h, n = 200, 64, 1.0
+    g = torch.Generator(device=DEV).manual_seed(V)
+    W = (torch.randn(V, h, generator=g, device=DEV) * h ** -0.5).to(torch.bfloat16)
+    x = (0.001 * torch.randn(M, h, generator=g, device=DEV)).to(torch.bfloat16)
+    y = torch.randint(0, V, (M,), generator=g, device=DEV)
+    w64 = W.double()
+    z = 30.0 * torch.tanh(x.double() @ w64.T / 30.0)
+    slope = 1 - (z / 30.0) ** 2
+    dz = (torch.softmax(z, 1) - smoothing / V) * slope
+    dz.scatter_add_(1, y[:, None], -(1 - smoothing) * slope.gather(1, y[:, None]))
+    d64 = dz @ w64
+    dx = lib.linear_cross_entropy(x, W, y, softcap=30.0, smoothing=smoothing, reduction="sum")[3]
+    size = (1 - smoothing) * w64.norm(dim=1).mean()
+    # weights (1 - smoothing) / V that logits of 0.005 and less put into at most two neighbouring steps: independent of
+    # the rows of W, so their errors add up like sqrt(V) of 2^-8 / V
+    slack = BF16 * d64.norm(dim=1) + size * (BF16 * V ** -0.5 * 3 + 2e-5)
+    assert bool(((dx.double() - d64).norm(dim=1) <= slack).all())
+    elem = BF16 * d64.abs() + size * (BF16 * V ** -0.5 * 3 + 2e-5)
+    assert bool(((dx.double() - d64).abs() <= elem).all())
